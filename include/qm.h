@@ -56,7 +56,8 @@
  *
  * Errors: QM_EINVAL for a bad argument, with qm_last_error() (thread-local,
  * valid until the next call on the thread) naming the part: "w", "codes",
- * "scales", "biases", "x", "y", "out", "ids", "axis", "workspace". QM_ECUDA if
+ * "scales", "biases", "x", "y", "out", "ids", "axis", "workspace" (and for the
+ * cache operators "cache", "batch", "k", "v", "q", "rope" and so on). QM_ECUDA if
  * a launch fails. A device-side wait that runs past its limit (two seconds of
  * the GPU's global timer) abandons its work and raises a device flag;
  * qm_device_status() reads it. No entry point synchronizes the stream.
@@ -90,7 +91,7 @@ typedef enum qm_format {
     QM_Q4_K = 4,
     QM_Q6_K = 5
 } qm_format;
-typedef enum qm_dtype { QM_F32 = 0, QM_BF16 = 1, QM_F16 = 2 } qm_dtype;
+typedef enum qm_dtype { QM_F32 = 0, QM_BF16 = 1, QM_F16 = 2, QM_I8 = 3 } qm_dtype; /* QM_I8: cache codes only */
 typedef enum qm_itype { QM_I32 = 0, QM_I64 = 1 } qm_itype;
 
 #define QM_MAX_NDIM 4
@@ -245,6 +246,122 @@ qm_status qm_apply_experts_static(const qm_weight* w, const void* ids, int32_t i
 qm_status qm_experts_route(const void* ids, int32_t id_type, int64_t P, int64_t E,
                            int32_t* counts, int32_t* offsets, int32_t* perm, void* workspace,
                            size_t workspace_bytes, qm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Between the packed products: head norms and rotation, a paged key/value
+ * cache and the attention that reads it. The pages have no counterpart; these
+ * are the operators a decode step needs between its q/k/v and o products.
+ * All arithmetic is float32, each result rounded once to its type. */
+
+/* Rows of heads: element i of head h of token t at
+ * data[t*token_stride + h*head_stride + i] (strides in elements, multiples of 8,
+ * not negative; the address 16-byte aligned), such as a part of the rows that a
+ * fused q/k/v product leaves. dtype QM_BF16 or QM_F16. */
+typedef struct qm_heads {
+    void* data;
+    int64_t token_stride, head_stride;
+    int32_t heads;
+    int32_t dtype;
+} qm_heads;
+
+typedef enum qm_rope_style {
+    QM_ROPE_HALF = 0, /* pair i is elements (i, i + dim/2) */
+    QM_ROPE_PAIRS = 1 /* pair i is elements (2i, 2i + 1) */
+} qm_rope_style;
+
+/* A rotation of a head's first `dim` elements (a multiple of 8, at most the
+ * head's) by position: table float32 [rows, dim], row p holding position p's
+ * dim/2 cosines then its dim/2 sines; pair (a, b) becomes
+ * (a cos - b sin, b cos + a sin). A position outside [0, rows) meets a row of
+ * zeros, as take gathers them. The table is 16-byte aligned. */
+typedef struct qm_rope {
+    const float* table;
+    int64_t rows;
+    int32_t dim;
+    int32_t style; /* qm_rope_style */
+} qm_rope;
+
+/* A paged key/value cache of `pages` pages of `page_size` tokens: element i of
+ * head h of token row r of page p at k[p*page_stride + h*head_stride +
+ * r*token_stride + i], and likewise in v (elements; strides multiples of 8 for
+ * 16-bit values and 16 for codes, not negative; addresses 16-byte aligned).
+ * dtype QM_BF16 or QM_F16: the values. QM_I8: codes in [-127, 127], value =
+ * code * scale, with one float32 scale per token row and head in k_scales and
+ * v_scales (NULL for the other types) at [p*scale_page_stride +
+ * h*scale_head_stride + r*scale_token_stride]. dim: a head's elements, a
+ * multiple of 8 (16 for QM_I8), at most 128. */
+typedef struct qm_cache {
+    void* k;
+    void* v;
+    float* k_scales;
+    float* v_scales;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+    int64_t pages;
+    int32_t dtype, heads, dim, page_size;
+} qm_cache;
+
+/* The new tokens of a call, sequence by sequence: sequence s has rows
+ * q_offsets[s] .. q_offsets[s+1]-1 of the `tokens` rows (int32 [seqs+1], from 0
+ * up to tokens; NULL: tokens/seqs rows each), and lens[s] tokens with them (int32;
+ * 0 for a slot that holds none), so that its new token i has position
+ * lens[s] - new_s + i; a negative position stores nothing and attends to
+ * nothing. Position p's page is page_table[s*table_stride + p/page_size]
+ * (int32), for p < table_width*page_size: a longer length is cut to that. A page
+ * id outside [0, pages) is a page that is not there: nothing is stored to it and
+ * zeros are read from it. max_new: the most new tokens of a sequence (0 if not
+ * known); it only chooses the kernel. All arrays are on the device. */
+typedef struct qm_batch {
+    const int32_t* lens;
+    const int32_t* page_table;
+    const int32_t* q_offsets;
+    int64_t tokens, table_width, table_stride;
+    int32_t seqs, max_new;
+} qm_batch;
+
+/* Most row sets qm_head_norm_rope takes in one call. */
+#define QM_MAX_HEAD_SETS 4
+
+/* head_norm_rope: for each of `count` row sets xs[i] of `tokens` tokens and heads
+ * of `dim` elements (a multiple of 8, at most 256; all of one dtype, 1 <= count
+ * <= QM_MAX_HEAD_SETS), outs[i] receives every head normed and rotated by its
+ * token's position: n_j = x_j * weight_j / sqrt(mean(x^2) + eps), then the
+ * rotation. weights (host array) or weights[i] NULL: no norm (weights are [dim]
+ * of xs' dtype, 16-byte aligned); rope NULL: no rotation (positions may then be
+ * NULL). positions: [tokens] of pos_type (QM_I32 or QM_I64). outs[i] may be xs[i] (the same
+ * address and strides) and otherwise shares no element with any xs. */
+qm_status qm_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void* const* weights, int32_t count,
+                            int64_t tokens, int32_t dim, float eps, const qm_rope* rope, const void* positions,
+                            int32_t pos_type, qm_stream_t stream);
+
+/* cache_append: stores every new token's keys and values (k and v: batch->tokens
+ * rows of cache->heads heads) at its position's place in the cache. The keys are normed by
+ * k_weight (as in qm_head_norm_rope; NULL: not) and rotated by their position
+ * (rope NULL: not) on the way. A QM_I8 cache stores, per token and head, the scale
+ * amax / 127 and codes by qm_quantize_q8_0's rules with a float32 scale (a NaN
+ * anywhere: scale NaN, codes 0; else an infinity: scale +inf, codes 0). */
+qm_status qm_cache_append(const qm_cache* cache, const qm_batch* batch, const qm_heads* k, const qm_heads* v,
+                          const void* k_weight, float eps, const qm_rope* rope, qm_stream_t stream);
+
+/* Bytes of device workspace qm_cache_attend needs (a multiple of 256; 0 for
+ * invalid arguments or no work). It depends on the shapes alone. */
+size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, int32_t q_heads);
+
+/* cache_attend: attention of every new token over its sequence's tokens in the
+ * cache. q and out have batch->tokens rows of q->heads heads, a multiple of cache->heads: query
+ * head h reads key head h / (q->heads / cache->heads). A token at position p
+ * sees the positions j with max(0, p - window + 1) <= j <= p (window 0: from 0
+ * on) below its sequence's length: out = sum_j w_j v_j, w = softmax over those j
+ * of scale * (q . k_j) (scale > 0). lse (NULL or float32 [tokens, q->heads])
+ * receives the natural logarithm of the sum of exp(scale * (q . k_j)). A token
+ * that sees nothing gets zeros and -infinity; values and scores at positions that
+ * a token does not see never reach its results, whatever they hold. q's dtype is
+ * the cache's, or either 16-bit type over QM_I8; out's is q's. Rows of no
+ * sequence are not written. out shares no element with q or the cache. The
+ * results are the same bits in every run of the same arguments. */
+qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm_heads* q, const qm_heads* out,
+                          float* lse, float scale, int64_t window, void* workspace, size_t workspace_bytes,
+                          qm_stream_t stream);
 
 /* Exercises the failure path of the bounded device waits without a fault:
  * enqueues one warp that waits on a barrier nothing will complete, with the

@@ -14,34 +14,40 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
 import torch
 
 __all__ = [
-    "QM_AFFINE", "QM_Q8_0", "QM_MXFP4", "QM_MXFP4_BLOCKS", "QM_Q4_K", "QM_Q6_K", "QM_WEIGHT_STATIC", "QM_F32", "QM_BF16", "QM_F16", "QM_I32", "QM_I64",
-    "QMError", "QWeight", "library_path", "load_library",
+    "QM_AFFINE", "QM_Q8_0", "QM_MXFP4", "QM_MXFP4_BLOCKS", "QM_Q4_K", "QM_Q6_K", "QM_WEIGHT_STATIC", "QM_F32", "QM_BF16", "QM_F16", "QM_I8", "QM_I32", "QM_I64",
+    "QM_ROPE_HALF", "QM_ROPE_PAIRS",
+    "QMError", "QWeight", "Rope", "Cache", "Batch", "library_path", "load_library",
     "qm_dequant", "qm_quantize_q8_0", "qm_apply", "qm_apply_many", "qm_take", "qm_apply_experts", "qm_apply_experts_workspace",
     "qm_experts_route_workspace",
     "qm_experts_route", "qm_apply_experts_static", "qm_check_wait_timeout", "qm_device_status", "qm_last_error",
-    "qm_version",
+    "qm_version", "qm_head_norm_rope", "qm_cache_append", "qm_cache_attend", "qm_cache_attend_workspace",
     "dequant", "quantize_q8_0", "apply", "apply_many", "take", "apply_experts", "route",
+    "head_norm_rope", "cache_append", "cache_attend",
 ]
 
 QM_OK, QM_EINVAL, QM_ECUDA, QM_ETIMEOUT, QM_ENOTSUP = 0, 1, 2, 3, 4
 QM_AFFINE, QM_Q8_0, QM_MXFP4, QM_MXFP4_BLOCKS, QM_Q4_K, QM_Q6_K = 0, 1, 2, 3, 4, 5
-QM_F32, QM_BF16, QM_F16 = 0, 1, 2
+QM_F32, QM_BF16, QM_F16, QM_I8 = 0, 1, 2, 3
+QM_ROPE_HALF, QM_ROPE_PAIRS = 0, 1
 QM_I32, QM_I64 = 0, 1
 QM_WEIGHT_STATIC = 1
 QM_MAX_NDIM = 4
 QM_MAX_MANY = 8
+QM_MAX_HEAD_SETS = 4
 
 _STATUS = {QM_EINVAL: "QM_EINVAL", QM_ECUDA: "QM_ECUDA", QM_ETIMEOUT: "QM_ETIMEOUT",
            QM_ENOTSUP: "QM_ENOTSUP"}
 _FORMATS = {"affine": QM_AFFINE, "q8_0": QM_Q8_0, "mxfp4": QM_MXFP4, "mxfp4_blocks": QM_MXFP4_BLOCKS,
             "q4_k": QM_Q4_K, "q6_k": QM_Q6_K}
 _DTYPES = {torch.float32: QM_F32, torch.bfloat16: QM_BF16, torch.float16: QM_F16}
+_CACHE_DTYPES = {torch.bfloat16: QM_BF16, torch.float16: QM_F16, torch.int8: QM_I8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -96,6 +102,10 @@ def load_library():
             "qm_apply_experts": ([wp, vp, i32, i64, i64, vp, i64, i32, vp, vp, sz, vp], i32),
             "qm_experts_route": ([vp, i32, i64, i64, vp, vp, vp, vp, sz, vp], i32),
             "qm_apply_experts_static": ([wp, vp, i32, i64, i64, vp, i64, i32, vp, vp], i32),
+            "qm_head_norm_rope": ([vp, vp, ctypes.POINTER(vp), i32, i64, i32, ctypes.c_float, vp, vp, i32, vp], i32),
+            "qm_cache_append": ([vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i32),
+            "qm_cache_attend_workspace": ([vp, vp, i32], sz),
+            "qm_cache_attend": ([vp, vp, vp, vp, vp, ctypes.c_float, i64, vp, sz, vp], i32),
             "qm_device_status": ([vp], i32),
             "qm_last_error": ([], ctypes.c_char_p),
             "qm_version": ([], i32),
@@ -219,6 +229,102 @@ class QWeight:
         return (tuple(lead) + (k // 2,), tuple(lead) + (k // 32,), None)
 
 
+# ---------------------------------------------------------------- heads and the paged cache
+# C descriptors as packed bytes, in include/qm.h's order; a bytes object passes
+# as a pointer to them.
+_HEADS = struct.Struct("Pqqii").pack
+_ROPE = struct.Struct("Pqii").pack
+_CACHE = struct.Struct("4P7q4i").pack
+_BATCH = struct.Struct("3P3q2i").pack
+
+
+def _refuse(message: str):
+    raise QMError(QM_EINVAL, message)
+
+
+def _heads(x: torch.Tensor, tokens: int, heads: int, dim: int, name: str) -> bytes:
+    """The descriptor of x [tokens, heads, dim] (its last axis contiguous, the others strided as they are)."""
+    if x.shape != (tokens, heads, dim):
+        _refuse(f"{name}: shape {tuple(x.shape)}, expected {(tokens, heads, dim)}")
+    ts, hs, es = x.stride()
+    if es != 1 and dim > 1:
+        _refuse(f"{name}: the elements of a head must be contiguous")
+    return _HEADS(x.data_ptr(), ts, hs, heads, _DTYPES.get(x.dtype, -1))
+
+
+def _i32(t: torch.Tensor, name: str) -> int:
+    if t.dtype != torch.int32:
+        _refuse(f"{name}: must be int32")
+    return _ptr(t)
+
+
+class Rope:
+    """A rotation of a head's first elements by position (qm_rope): `table` float32
+    [rows, dim], row p the dim/2 cosines then the dim/2 sines of position p; style
+    "half" pairs elements (i, i + dim/2), "pairs" (2i, 2i + 1)."""
+
+    def __init__(self, table: torch.Tensor, style: str = "half"):
+        if table.dtype != torch.float32 or table.dim() != 2:
+            _refuse("rope: table must be float32 [rows, dim]")
+        if style not in ("half", "pairs"):
+            _refuse('rope: style must be "half" or "pairs"')
+        self.table, self.style = table, style
+        self.dim = table.shape[1]
+        self._c = _ROPE(_ptr(table), table.shape[0], self.dim, QM_ROPE_HALF if style == "half" else QM_ROPE_PAIRS)
+
+
+class Cache:
+    """A paged key/value cache (qm_cache): k and v [pages, heads, page_size, dim],
+    bfloat16 or float16, or int8 codes with float32 k_scales and v_scales [pages,
+    heads, page_size]. Any strides whose last axis is contiguous do (a cache laid
+    out [pages, page_size, heads, dim] is passed permuted), the same for k and v.
+    The descriptor is built here, from the tensors' addresses at that time."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
+            _refuse("cache: k and v must be [pages, heads, page_size, dim] of one shape and dtype")
+        if k.dtype not in _CACHE_DTYPES:
+            _refuse("cache: dtype must be bfloat16, float16 or int8")
+        if k.stride() != v.stride() or (k.stride(3) != 1 and k.shape[3] > 1):
+            _refuse("cache: k and v must have the same strides and contiguous heads")
+        scales = (k_scales, v_scales)
+        if any((s is None) != (k.dtype != torch.int8) for s in scales):
+            _refuse("k_scales: an int8 cache has k_scales and v_scales, another has neither")
+        sst = (0, 0, 0)
+        if k.dtype == torch.int8:
+            if any(s.dtype != torch.float32 or s.shape != k.shape[:3] for s in scales) or k_scales.stride() != v_scales.stride():
+                _refuse("k_scales: scales must be float32 [pages, heads, page_size] of the same strides")
+            sst = k_scales.stride()
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.heads, self.page_size, self.dim = k.shape
+        self._need = {}
+        self._c = _CACHE(k.data_ptr(), v.data_ptr(), *(0 if s is None else s.data_ptr() for s in scales), *k.stride()[:3],
+                         *sst, self.pages, _CACHE_DTYPES[k.dtype], self.heads, self.dim, self.page_size)
+
+
+class Batch:
+    """The new tokens of a call (qm_batch): lens int32 [seqs] (tokens of each sequence
+    with the new ones; 0: an empty slot), page_table int32 [seqs, width], q_offsets
+    int32 [seqs + 1] where each sequence's rows begin (None: tokens / seqs rows
+    each), `tokens` the rows in all (None: seqs), max_new the most new tokens of a sequence
+    if known. The tensors may be updated in place between calls."""
+
+    def __init__(self, lens: torch.Tensor, page_table: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+                 tokens: Optional[int] = None, max_new: int = 0):
+        seqs = lens.shape[0]
+        if lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] != seqs:
+            _refuse("batch: lens must be [seqs] and page_table [seqs, width]")
+        if q_offsets is not None and q_offsets.shape != (seqs + 1,):
+            _refuse("q_offsets: must be [seqs + 1]")
+        if page_table.dtype != torch.int32 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+            _refuse("page_table: must be int32 with contiguous rows")
+        self.lens, self.page_table, self.q_offsets = lens, page_table, q_offsets
+        self.seqs, self.tokens, self.max_new = seqs, seqs if tokens is None else int(tokens), int(max_new)
+        self._c = _BATCH(_i32(lens, "lens"), page_table.data_ptr(), 0 if q_offsets is None else _i32(q_offsets, "q_offsets"),
+                         self.tokens, page_table.shape[1], page_table.stride(0), seqs, self.max_new)
+
+
 # ---------------------------------------------------------------- C entry points
 def qm_version() -> int:
     return load_library().qm_version()
@@ -324,6 +430,66 @@ def qm_experts_route(ids: torch.Tensor, E: int, counts: torch.Tensor, offsets: t
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+def qm_head_norm_rope(xs: Sequence[torch.Tensor], outs: Sequence[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                      rope: Optional[Rope] = None, weights: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                      eps: float = 1e-6, stream=None) -> None:
+    """outs[i] [tokens, heads_i, dim] = the heads of xs[i] normed by weights[i] and rotated by `positions`."""
+    n = len(xs)
+    if not 1 <= n <= QM_MAX_HEAD_SETS or len(outs) != n or (weights is not None and len(weights) != n):
+        _refuse(f"count: 1 .. {QM_MAX_HEAD_SETS} row sets, as many outputs and weights")
+    if xs[0].dim() != 3:
+        _refuse("x: must be [tokens, heads, dim]")
+    T, _, D = xs[0].shape
+    xd = b"".join([_heads(x, T, x.shape[1], D, "x") for x in xs])
+    od = b"".join([_heads(y, T, x.shape[1], D, "out") for x, y in zip(xs, outs)])
+    warr = None
+    if weights is not None:
+        for w, x in zip(weights, xs):
+            if w is not None and (w.shape != (D,) or w.dtype != x.dtype):
+                _refuse("weights: must be [dim] of x's dtype")
+        warr = _PARR[n](*[_ptr(w) for w in weights])
+    pos, ptype = None, QM_I32
+    if positions is not None:
+        if positions.shape != (T,) or positions.dtype not in (torch.int32, torch.int64):
+            _refuse("positions: must be int32 or int64 [tokens]")
+        pos, ptype = _ptr(positions), QM_I64 if positions.dtype == torch.int64 else QM_I32
+    _check(load_library().qm_head_norm_rope(xd, od, warr, n, T, D, eps, None if rope is None else rope._c, pos, ptype,
+                                            _stream(stream)))
+
+
+def qm_cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    if k_weight is not None and (k_weight.shape != (cache.dim,) or k_weight.dtype != k.dtype):
+        _refuse("k_weight: must be [dim] of k's dtype")
+    _check(load_library().qm_cache_append(
+        cache._c, batch._c, _heads(k, batch.tokens, cache.heads, cache.dim, "k"),
+        _heads(v, batch.tokens, cache.heads, cache.dim, "v"), _ptr(k_weight), eps, None if rope is None else rope._c,
+        _stream(stream)))
+
+
+def qm_cache_attend_workspace(cache: Cache, batch: Batch, heads: int) -> int:
+    key = (batch.seqs, batch.tokens, batch.max_new, heads)  # the shapes that it depends on
+    need = cache._need.get(key)
+    if need is None:
+        if len(cache._need) >= 1024:
+            cache._need.clear()
+        need = cache._need[key] = load_library().qm_cache_attend_workspace(cache._c, batch._c, heads)
+    return need
+
+
+def qm_cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, out: torch.Tensor, scale: float,
+                    workspace: Optional[torch.Tensor], window: int = 0, lse: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    if q.dim() != 3:
+        _refuse("q: must be [tokens, heads, dim]")
+    T, H = batch.tokens, q.shape[1]
+    if lse is not None and (lse.shape != (T, H) or lse.dtype != torch.float32):
+        _refuse("lse: must be float32 [tokens, heads]")
+    _check(load_library().qm_cache_attend(
+        cache._c, batch._c, _heads(q, T, H, cache.dim, "q"), _heads(out, T, H, cache.dim, "out"), _ptr(lse), scale, window,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
 def qm_check_wait_timeout(limit_ns: int, stream=None) -> None:
     _check(load_library().qm_check_wait_timeout(limit_ns, _stream(stream)))
 
@@ -396,3 +562,31 @@ def route(ids: torch.Tensor, E: int, stream=None):
     ws = torch.empty(max(qm_experts_route_workspace(P, E), 256), dtype=torch.uint8, device=dev)
     qm_experts_route(ids, E, counts, offsets, perm, ws, stream)
     return counts[:E], offsets, perm[:P]
+
+
+def head_norm_rope(xs: Sequence[torch.Tensor], positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                   weights: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6, stream=None) -> list:
+    """Every head of xs[i] [tokens, heads_i, dim] (queries, keys: any strided rows) normed by weights[i] [dim] and
+    rotated by its token's position."""
+    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
+    qm_head_norm_rope(xs, outs, positions, rope, weights, eps, stream)
+    return outs
+
+
+def cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """Stores the new tokens' keys [tokens, heads, dim] (normed and rotated on the way) and values in the cache."""
+    qm_cache_append(cache, batch, k, v, rope, k_weight, eps, stream)
+
+
+def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+                 lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the new tokens' queries [tokens, heads, dim] over their sequences in the cache; with lse, (out,
+    the scores' log-sum-exp [tokens, heads])."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    total = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
+    if workspace is None:
+        need = qm_cache_attend_workspace(cache, batch, q.shape[1])
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    qm_cache_attend(cache, batch, q, out, cache.dim ** -0.5 if scale is None else scale, workspace, window, total, stream)
+    return (out, total) if lse else out

@@ -34,9 +34,9 @@ qm_status cuda_fail(cudaError_t e, const char* what) {
 
 int dtype_size(int dt) { return dt == QM_F32 ? 4 : 2; }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static bool mul_ok(int64_t a, int64_t b, int64_t* out) {
+bool mul_ok(int64_t a, int64_t b, int64_t* out) {
     if (a < 0 || b < 0) return false;
     if (a != 0 && b > std::numeric_limits<int64_t>::max() / a) return false;
     *out = a * b;
@@ -220,7 +220,7 @@ bool make_tmap_2d(void* map, const void* base, uint64_t inner_bytes, uint64_t ro
     return r == CUDA_SUCCESS;
 }
 
-static qm_status check_launch(cudaError_t e, const char* what) {
+qm_status check_launch(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return cuda_fail(e, what);
     return QM_OK;
 }
@@ -233,7 +233,7 @@ extern "C" {
 
 const char* qm_last_error(void) { return g_last_error.c_str(); }
 
-int32_t qm_version(void) { return 100; }
+int32_t qm_version(void) { return 200; }
 
 qm_status qm_dequant(const qm_weight* w, int32_t out_dtype, void* out, qm_stream_t stream) {
     set_error("");

@@ -1,0 +1,616 @@
+// qm_attend.cu -- attention of new tokens over a paged cache for few rows to a
+// key head (attend_rows_kernel: decode steps, drafted tokens), and the join of
+// items cut between CTAs (attend_join_kernel).
+//
+// o = sum_j w_j v_j, w = softmax over the keys j that a row sees of scale (q . k_j),
+// in one pass over the keys: with m the running maximum of the scores (in powers
+// of two: t = scale log2(e) (q . k)), l = sum 2^(t_j - m) and o = sum 2^(t_j - m) v_j are
+// rescaled by 2^(m - m') when m grows to m'. Scores, weights' sums and o are float32;
+// a weight is rounded to the values' 16-bit type to enter its product (a relative
+// 2^-9 or 2^-12 that does not add up over keys, as the output's own rounding).
+//
+// Every key and value is read once for up to 16 rows, 2 flops a byte and row: what
+// bounds it is HBM. One CTA per SM, eight warps; a warp takes 16 of a unit's 128 keys and
+// streams them through its own ring of shared-memory stages with 16-byte
+// asynchronous copies (whole 2 * DP-byte rows; the pages' places are looked up one
+// step ahead), so that warps wait for nothing but their own copies and an SM keeps
+// some 130 KB in flight. The products are m16n8k16 tensor-core instructions on 16
+// rows (rows that the item lacks are zeros: the tensor pipe has time to spare). At the
+// end of an item the warps' sums are added through shared memory in warp order while
+// the next item's copies are already under way.
+//
+// 8-bit codes are exact in both 16-bit types, so they enter the products as they
+// are: a key's scale multiplies its score, a value's scale its weight. For float16 the
+// running maximum then includes the values' scales, which keeps scaled weights
+// within [0, 2^8] whatever the scales are.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qm_attend.cuh"
+
+namespace qm {
+namespace attend {
+namespace {
+
+constexpr int kRows = 16;
+constexpr int kWarps = 8;
+constexpr float kNegInf = -INFINITY;
+
+// Stage and shared-memory layout of a kernel variant.
+template <int DP, bool I8>
+struct Lay {
+    static constexpr int kRowBytes = I8 ? DP : 2 * DP;
+    static constexpr int kPart = 16 * kRowBytes;                   // 16 keys, or values
+    static constexpr int kStage = 2 * kPart + (I8 ? 128 : 0);      // and 16 + 16 scales
+    static constexpr int kStages = I8 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kRed = kWarps * 8 * DP * 4;
+    static constexpr int kMl = kWarps * kRows * 8;
+    static constexpr int kSmem = kWarps * kStages * kStage + kRed + kMl;
+    // where 16-byte piece c of row r lies: rows that one access reads together
+    // must differ in bank group
+    static QM_DEV uint32_t k_at(int r, int c) {
+        if constexpr (!I8) return r * kRowBytes + ((c ^ (r & 7)) << 4);
+        else if constexpr (DP == 128) return r * kRowBytes + ((c ^ ((r & 1) << 2)) << 4);
+        else return r * kRowBytes + (c << 4);
+    }
+    static QM_DEV uint32_t v_at(int r, int c) {
+        if constexpr (!I8) return r * kRowBytes + ((c ^ (r & 7)) << 4);
+        else if constexpr (DP == 128) return r * kRowBytes + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+        else return r * kRowBytes + ((c ^ (((r >> 1) & 1) << 1)) << 4);
+    }
+};
+
+QM_DEV void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+QM_DEV void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+// Signed bytes 0 and 2 of x as a pair of 16-bit values, exactly. bfloat16 has eight
+// significant bits: 128 + the low seven bits, less 128 or 256 by the sign bit;
+// float16: 1024 + the code with its sign bit turned (code + 128), less 1152.
+template <bool BF16>
+QM_DEV uint32_t codes16(uint32_t x) {
+    if constexpr (BF16) {
+        const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    } else {
+        const uint32_t a = (x & 0x00FF00FFu) ^ 0x64806480u, b = 0x64806480u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+}
+
+// log2 of a value scale, held within 2^+-30 (zero and NaN: the low end).
+QM_DEV float scale_log2(float s) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return fminf(fmaxf(y, -30.f), 30.f);
+}
+
+template <int DP, bool BF16, bool I8>
+__global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __grid_constant__ Args a) {
+    using L = Lay<DP, I8>;
+    constexpr int ST = L::kStages;
+    constexpr int KK = DP / 16;
+    constexpr float kLift = BF16 ? 0.f : 8.f;  // float16 weights in [0, 2^8]: the small ones keep their bits
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * ST * L::kStage;
+    float* red = reinterpret_cast<float*>(smem + kWarps * ST * L::kStage);
+    float2* ml = reinterpret_cast<float2*>(smem + kWarps * ST * L::kStage + L::kRed);
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x);
+    Cursor<kRows> ahead = now;
+    const bool idle = now.left == 0;
+    int first_part = 0;
+    if (idle) {
+        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
+        return;
+    }
+
+    // ---- copies: the place of key row (lane & 15) of the step `ahead` is at
+    int64_t place = -1, splace = 0;
+    auto look = [&]() {
+        if (ahead.left > 0)
+            place = key_offset(a, ahead.s, ahead.h, ahead.u * kUnit + warp * 16 + (lane & 15), ahead.span.lo, ahead.span.hi, splace);
+        else
+            place = -1;
+    };
+    auto issue = [&](int slot) {
+        const uint32_t base = ring + slot * L::kStage;
+        constexpr int per = 32 / L::kChunks;  // rows that the warp copies at once
+        const int c = lane % L::kChunks;
+        const int step = I8 ? 16 : 8;  // elements of a piece
+#pragma unroll
+        for (int i = 0; i < 16 / per; ++i) {
+            const int r = i * per + lane / L::kChunks;
+            const int64_t off = __shfl_sync(0xffffffffu, place, r);
+            const bool on = off >= 0 && c * step < a.dim;
+            const int64_t at = (off + c * step) * (I8 ? 1 : 2);
+            cp_async16(base + L::k_at(r, c), on ? a.k + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+            cp_async16(base + L::kPart + L::v_at(r, c), on ? a.v + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+        }
+        if constexpr (I8) {
+            const float* s = lane < 16 ? a.ks : a.vs;
+            cp_async4(base + 2 * L::kPart + 4 * lane, place >= 0 ? s + splace : reinterpret_cast<const float*>(a.q),
+                      place >= 0 ? 4u : 0u);
+        }
+    };
+    look();
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) {
+        if (ahead.left > 0) {
+            issue(i);
+            ahead.step(a);
+            look();
+        }
+        cp_async_commit();
+    }
+
+    uint32_t qa[KK][4];
+    float acc[DP / 8][4];
+    float top[2], sum[2];
+    int pos[2], kmin[2], kmax[2];  // of rows g and g + 8: the keys they see, [kmin, kmax]
+    bool begin = true;             // the next step begins a part of an item
+    bool whole_start = false;
+    int slot = 0;
+    while (now.left > 0) {
+        if (begin) {
+            begin = false;
+            whole_start = now.first();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = g + 8 * x;
+                top[x] = kNegInf;
+                sum[x] = 0.f;
+                pos[x] = -1;
+                kmin[x] = 0;
+                kmax[x] = -1;
+                const uint16_t* qrow = nullptr;
+                if (r < now.span.rows) {
+                    const unsigned R = now.tile * kRows + r, i = R / a.group, gg = R - i * a.group;
+                    pos[x] = now.seq.len - now.seq.fresh + static_cast<int>(i);
+                    kmin[x] = first_seen(a, pos[x]);
+                    kmax[x] = min(pos[x], a.cap - 1);
+                    qrow = a.q + (now.seq.first + static_cast<int64_t>(i)) * a.q_ts + (now.h * a.group + static_cast<int>(gg)) * a.q_hs;
+                }
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        // codes come four to a lane: their products take the head's elements in that order
+                        const int d = I8 ? 64 * (kk / 4) + 16 * t + 4 * (kk % 4) + 2 * y : 16 * kk + 8 * y + 2 * t;
+                        qa[kk][2 * y + x] = qrow && d < a.dim ? *reinterpret_cast<const uint32_t*>(qrow + d) : 0u;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        }
+        cp_async_wait<ST - 2>();
+        __syncwarp();  // the stage is whole, and its predecessor is free in every lane
+        if (ahead.left > 0) {
+            issue(slot == 0 ? ST - 1 : slot - 1);
+            ahead.step(a);
+            look();
+        }
+        cp_async_commit();
+
+        const int key0 = now.u * kUnit + warp * 16;
+        const Span& sp = now.span;
+        if (key0 < sp.hi && key0 + 16 > sp.lo) {
+            const uint32_t kb = ring + slot * L::kStage, vb = kb + L::kPart;
+            float s[2][4] = {};
+            if constexpr (!I8) {
+                const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint32_t b[4];
+                    ldsm4(kb + L::k_at(r, 2 * kk + c), b);
+                    mma16<BF16>(s[0], qa[kk], b[0], b[1]);
+                    mma16<BF16>(s[1], qa[kk], b[2], b[3]);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] *= a.scale2;
+            } else {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int h = 0; h < KK / 4; ++h) {
+                        const uint4 w = lds_v4(kb + L::k_at(8 * n + g, 4 * h + t));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma16<BF16>(s[n], qa[4 * h + i], codes16<BF16>(prmt(ws[i], 0u, 0x4140)),
+                                        codes16<BF16>(prmt(ws[i], 0u, 0x4342)));
+                    }
+                    const uint2 sc = lds_v2(kb + 2 * L::kPart + 4 * (8 * n + 2 * t));
+                    const float s0 = __uint_as_float(sc.x) * a.scale2, s1 = __uint_as_float(sc.y) * a.scale2;
+                    s[n][0] *= s0; s[n][1] *= s1; s[n][2] *= s0; s[n][3] *= s1;
+                }
+            }
+            // rows differ in what they see, or the step's keys end or begin in between
+            const bool cut = key0 + 15 > min(sp.p0, a.cap - 1) || (a.window && key0 < first_seen(a, sp.p1));
+            uint32_t hidden = 0;  // bit 4n + e
+            if (cut) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 8 * n + 2 * t + (e & 1), x = e >> 1;
+                        if (key < kmin[x] || key > kmax[x]) {
+                            s[n][e] = kNegInf;
+                            hidden |= 1u << (4 * n + e);
+                        }
+                    }
+            }
+            float vs[2][2], lv[2][2];  // value scales of keys 8n + 2t + e, and their logarithms
+            if constexpr (I8) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint2 sc = lds_v2(kb + 2 * L::kPart + 64 + 4 * (8 * n + 2 * t));
+                    vs[n][0] = __uint_as_float(sc.x);
+                    vs[n][1] = __uint_as_float(sc.y);
+                    lv[n][0] = BF16 ? 0.f : scale_log2(vs[n][0]);
+                    lv[n][1] = BF16 ? 0.f : scale_log2(vs[n][1]);
+                }
+            }
+            float from[2];
+            bool grown = false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float m = top[x];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        m = fmaxf(m, (I8 && !BF16) ? s[n][2 * x + e] + lv[n][e] : s[n][2 * x + e]);
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                grown = grown || m > top[x];
+                from[x] = top[x];
+                top[x] = m;
+            }
+            if (__any_sync(0xffffffffu, grown)) {
+                float f[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    f[x] = ex2(from[x] - (top[x] == kNegInf ? 0.f : top[x]));
+                    sum[x] *= f[x];
+                }
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j) {
+                    acc[j][0] *= f[0]; acc[j][1] *= f[0];
+                    acc[j][2] *= f[1]; acc[j][3] *= f[1];
+                }
+            }
+            const float ref[2] = {top[0] == kNegInf ? 0.f : top[0] - kLift, top[1] == kNegInf ? 0.f : top[1] - kLift};
+            float p[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[n][e] = ex2(s[n][e] - ref[e >> 1]);
+                    sum[e >> 1] += p[n][e];
+                    if constexpr (I8) p[n][e] = (hidden >> (4 * n + e)) & 1 ? 0.f : p[n][e] * vs[n][e & 1];
+                }
+            const uint32_t pa[4] = {pack16<BF16>(p[0][0], p[0][1]), pack16<BF16>(p[0][2], p[0][3]),
+                                    pack16<BF16>(p[1][0], p[1][1]), pack16<BF16>(p[1][2], p[1][3])};
+            if constexpr (!I8) {
+                // A value that only some of the rows see must not reach the others: 0 times an
+                // infinity or NaN is NaN. Where the rows differ and such a value is there, the
+                // products are formed one by one.
+                bool odd = false;
+                if (cut && sp.p0 != sp.p1) {
+#pragma unroll 1
+                    for (int i = lane; i < 16 * L::kChunks; i += 32) {
+                        const uint4 w = lds_v4(vb + 16 * i);
+                        odd = odd || nonfinite2<BF16>(w.x) || nonfinite2<BF16>(w.y) || nonfinite2<BF16>(w.z) || nonfinite2<BF16>(w.w);
+                    }
+                    odd = __any_sync(0xffffffffu, odd);
+                }
+                if (!odd) {
+                    const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
+#pragma unroll
+                    for (int j = 0; j < DP / 16; ++j) {
+                        uint32_t b[4];
+                        ldsm4_t(vb + L::v_at(r, 2 * j + c), b);
+                        mma16<BF16>(acc[2 * j], pa, b[0], b[1]);
+                        mma16<BF16>(acc[2 * j + 1], pa, b[2], b[3]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int k = 0; k < 16; ++k) {
+                        // p[row g + 8x][key k] is in lane 4g + (k % 8) / 2, entry [k / 8][2x + k % 2]
+                        const int src = 4 * g + ((k & 7) >> 1);
+                        float pk[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float mine = k < 8 ? ((k & 1) ? p[0][2 * x + 1] : p[0][2 * x]) : ((k & 1) ? p[1][2 * x + 1] : p[1][2 * x]);
+                            pk[x] = __shfl_sync(0xffffffffu, mine, src);
+                        }
+                        const bool see[2] = {key0 + k >= kmin[0] && key0 + k <= kmax[0], key0 + k >= kmin[1] && key0 + k <= kmax[1]};
+#pragma unroll
+                        for (int j = 0; j < DP / 8; ++j) {
+                            const uint32_t w = lds_u32(vb + L::v_at(k, j) + 4 * t);
+                            const float v0 = BF16 ? __uint_as_float(w << 16) : f16_bits_to_f32(w & 0xFFFFu);
+                            const float v1 = BF16 ? __uint_as_float(w & 0xFFFF0000u) : f16_bits_to_f32(w >> 16);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                if (see[x]) {
+                                    acc[j][2 * x] = fmaf(pk[x], v0, acc[j][2 * x]);
+                                    acc[j][2 * x + 1] = fmaf(pk[x], v1, acc[j][2 * x + 1]);
+                                }
+                        }
+                    }
+                }
+            } else {
+                // column n of tile i of 32 elements jb: element 32 jb + 4 n + i
+#pragma unroll
+                for (int jb = 0; jb < DP / 32; ++jb) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+                        w[i] = lds_u32(vb + L::v_at(r, 2 * jb + (g >> 2)) + 4 * (g & 3));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t pick = 0x0400u + 0x0101u * i;  // byte i of the two keys, to bytes 0 and 2
+                        mma16<BF16>(acc[4 * jb + i], pa, codes16<BF16>(prmt(w[0], w[1], pick)), codes16<BF16>(prmt(w[2], w[3], pick)));
+                    }
+                }
+            }
+        }
+        slot = slot + 1 == ST ? 0 : slot + 1;
+
+        const bool ends = now.u + 1 == now.u1;
+        if (ends || now.left == 1) {
+            // ---- the part's end: add the warps' sums
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+                if (t == 0) ml[warp * kRows + g + 8 * x] = make_float2(top[x], sum[x]);
+            }
+            __syncthreads();
+            const int rows = now.span.rows;
+            const bool done = whole_start && ends;
+            const int part = 2 * blockIdx.x + (whole_start ? 1 : 0);
+            // swaps 16-byte pieces of row g of `red` so that the rows' writes differ in bank
+            auto piece = [](int row, int c4) { return c4 ^ (2 * (row & 3) | (row >> 2)); };
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (8 * x >= rows) break;
+                float m = kNegInf;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kRows + g + 8 * x].x);
+                const float f = ex2(top[x] - (m == kNegInf ? 0.f : m));
+                float* mine = red + (warp * 8 + g) * DP;
+                if constexpr (!I8) {
+#pragma unroll
+                    for (int j = 0; j < DP / 8; ++j)
+                        *reinterpret_cast<float2*>(mine + 4 * piece(g, 2 * j + (t >> 1)) + 2 * (t & 1)) =
+                            make_float2(acc[j][2 * x] * f, acc[j][2 * x + 1] * f);
+                } else {
+#pragma unroll
+                    for (int jb = 0; jb < DP / 32; ++jb)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            *reinterpret_cast<float4*>(mine + 4 * piece(g, 8 * jb + 2 * t + y)) =
+                                make_float4(acc[4 * jb][2 * x + y] * f, acc[4 * jb + 1][2 * x + y] * f,
+                                            acc[4 * jb + 2][2 * x + y] * f, acc[4 * jb + 3][2 * x + y] * f);
+                }
+                __syncthreads();
+                const int rr = threadIdx.x / (DP / 4), c4 = threadIdx.x % (DP / 4);
+                const int row = rr + 8 * x;
+                if (rr < 8 && row < rows) {
+                    float mm = kNegInf;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + row].x);
+                    const float mr = mm == kNegInf ? 0.f : mm;
+                    float total = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float2 e = ml[w * kRows + row];
+                        total += e.y * ex2(e.x - mr);
+                        const float4 v = *reinterpret_cast<const float4*>(red + (w * 8 + rr) * DP + 4 * piece(rr, c4));
+                        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+                    }
+                    if (done) {
+                        const unsigned R = now.tile * kRows + row;
+                        int64_t lse_at;
+                        uint16_t* y = out_row(a, now.seq.first, now.h, R, lse_at);
+                        const int at = now.seq.len - now.seq.fresh + static_cast<int>(R / a.group);
+                        const float inv = inverse_total(a, at, total);
+                        if (4 * c4 < a.dim)
+                            *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+                        if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm - kLift, total);
+                    } else {
+                        *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(part) * kRows + row) * DP + 4 * c4) = o;
+                        if (c4 == 0) a.ml[part * kRows + row] = make_float2(mm, total);
+                    }
+                }
+                __syncthreads();
+            }
+            if (!done && threadIdx.x == 0) {
+                int* d = a.desc + blockIdx.x * 8;
+                if (whole_start) {
+                    d[1] = 1;
+                    d[2] = now.seq.first;
+                    d[3] = now.h;
+                    d[4] = static_cast<int>(now.tile * kRows);
+                    d[5] = rows;
+                    d[6] = now.seq.len - now.seq.fresh;
+                }
+            }
+            if (!whole_start) first_part = ends ? 2 : 1;
+            if (now.left == 1 && threadIdx.x == 0) {
+                a.desc[blockIdx.x * 8] = first_part;
+                if (!(whole_start && !ends)) a.desc[blockIdx.x * 8 + 1] = 0;
+            }
+            begin = true;
+        }
+        now.step(a);
+    }
+    cp_async_wait<0>();
+}
+
+// Joins the parts of one item: block x of a CTA whose last part begins an item
+// adds that part and the first parts of the CTAs after it, up to the item's last.
+template <int R, int DP, bool BF16>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Args a, int runs, float lift) {
+    constexpr int C4 = DP / 4, G = 256 / C4;  // groups of threads that take every G-th part
+    __shared__ float4 so[G][C4];
+    __shared__ float2 sm[G];
+    grid_dependency_wait();
+    const int c = blockIdx.x;
+    const int* d = a.desc + c * 8;
+    if (d[1] == 0) return;
+    const int first = d[2], h = d[3], r0 = d[4], rows = d[5], base = d[6];
+    if (static_cast<int>(blockIdx.y) >= rows) return;
+    int last = c + 1;  // the CTA with the item's last part
+    while (last < runs && a.desc[last * 8] == 1) ++last;
+    const int parts = last - c + 1;
+    const int grp = threadIdx.x / C4, c4 = threadIdx.x % C4;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        float m = kNegInf, total = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = grp; i < parts; i += G) {
+            const int part = 2 * (c + i) + (i == 0 ? 1 : 0);
+            const float2 e = a.ml[part * R + row];
+            const float4 v = *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(part) * R + row) * DP + 4 * c4);
+            const float mn = fmaxf(m, e.x), ref = mn == kNegInf ? 0.f : mn;
+            const float f = ex2(m - ref), fe = ex2(e.x - ref);
+            total = total * f + e.y * fe;
+            o.x = o.x * f + v.x * fe; o.y = o.y * f + v.y * fe;
+            o.z = o.z * f + v.z * fe; o.w = o.w * f + v.w * fe;
+            m = mn;
+        }
+        so[grp][c4] = o;
+        if (c4 == 0) sm[grp] = make_float2(m, total);
+        __syncthreads();
+        if (grp == 0) {
+            float mm = kNegInf;
+#pragma unroll
+            for (int w = 0; w < G; ++w) mm = fmaxf(mm, sm[w].x);
+            const float ref = mm == kNegInf ? 0.f : mm;
+            float tt = 0.f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < G; ++w) {
+                const float f = ex2(sm[w].x - ref);
+                const float4 v = so[w][c4];
+                tt += sm[w].y * f;
+                o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+            }
+            int64_t lse_at;
+            uint16_t* y = out_row(a, first, h, static_cast<unsigned>(r0) + row, lse_at);
+            const int at = base + static_cast<int>((static_cast<unsigned>(r0) + row) / a.group);
+            const float inv = inverse_total(a, at, tt);
+            if (4 * c4 < a.dim)
+                *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
+            if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm - lift, tt);
+        }
+        __syncthreads();
+    }
+}
+
+template <int DP, bool BF16, bool I8>
+cudaError_t run_rows(const Args& a, int runs, cudaStream_t st) {
+    auto kern = attend_rows_kernel<DP, BF16, I8>;
+    constexpr int smem = Lay<DP, I8>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(runs), kWarps * 32, smem, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attend_join_kernel<kRows, DP, BF16>, dim3(runs, kRows), 256, 0, st, a, runs, BF16 ? 0.f : 8.f);
+}
+
+// Workspace: [runs][8] int, [runs][2][R] float2, [runs][2][R][DP] float.
+struct Ws {
+    size_t ml, part, all;
+};
+Ws workspace_layout(int runs, int rows, int dp) {
+    Ws w;
+    w.ml = (static_cast<size_t>(runs) * 32 + 255) / 256 * 256;
+    w.part = w.ml + (static_cast<size_t>(runs) * 2 * rows * 8 + 255) / 256 * 256;
+    w.all = w.part + static_cast<size_t>(runs) * 2 * rows * dp * 4;
+    return w;
+}
+
+}  // namespace
+}  // namespace attend
+
+using namespace attend;
+
+size_t attend_workspace_bytes(const qm_cache& c, const qm_batch&, int) {
+    return workspace_layout(num_sms(), kRows, c.dim <= 64 ? 64 : 128).all;
+}
+
+cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_heads& q, const qm_heads& out,
+                                float* lse, float scale, int64_t window, void* workspace, cudaStream_t st) {
+    const int dp = c.dim <= 64 ? 64 : 128;
+    const int runs = num_sms();
+    const Ws ws = workspace_layout(runs, kRows, dp);
+    uint8_t* wb = static_cast<uint8_t*>(workspace);
+    Args a = {};
+    a.q = static_cast<const uint16_t*>(q.data);
+    a.out = static_cast<uint16_t*>(out.data);
+    a.lse = lse;
+    a.q_ts = q.token_stride;
+    a.q_hs = q.head_stride;
+    a.o_ts = out.token_stride;
+    a.o_hs = out.head_stride;
+    a.k = static_cast<const uint8_t*>(c.k);
+    a.v = static_cast<const uint8_t*>(c.v);
+    a.ks = c.k_scales;
+    a.vs = c.v_scales;
+    a.page_stride = c.page_stride;
+    a.head_stride = c.head_stride;
+    a.token_stride = c.token_stride;
+    a.sps = c.scale_page_stride;
+    a.shs = c.scale_head_stride;
+    a.sts = c.scale_token_stride;
+    a.lens = b.lens;
+    a.table = b.page_table;
+    a.q_off = b.q_offsets;
+    a.table_stride = b.table_stride;
+    int64_t cap = 0;
+    a.cap = mul_ok(b.table_width, c.page_size, &cap) && cap <= INT_MAX ? static_cast<int>(cap) : INT_MAX;
+    a.seqs = b.seqs;
+    a.tokens = static_cast<int>(b.tokens);
+    a.each = b.q_offsets ? 0 : static_cast<int>(b.tokens / b.seqs);
+    a.heads = q.heads;
+    a.kv_heads = c.heads;
+    a.group = q.heads / c.heads;
+    a.dim = c.dim;
+    a.page_size = c.page_size;
+    a.pages = static_cast<int>(c.pages);
+    a.window = static_cast<int>(std::min<int64_t>(window, INT_MAX));
+    a.scale2 = scale * 1.4426950408889634f;
+    a.desc = reinterpret_cast<int*>(wb);
+    a.ml = reinterpret_cast<float2*>(wb + ws.ml);
+    a.part = reinterpret_cast<float*>(wb + ws.part);
+    const bool bf16 = q.dtype == QM_BF16, i8 = c.dtype == QM_I8;
+    if (dp == 64) {
+        if (i8) return bf16 ? run_rows<64, true, true>(a, runs, st) : run_rows<64, false, true>(a, runs, st);
+        return bf16 ? run_rows<64, true, false>(a, runs, st) : run_rows<64, false, false>(a, runs, st);
+    }
+    if (i8) return bf16 ? run_rows<128, true, true>(a, runs, st) : run_rows<128, false, true>(a, runs, st);
+    return bf16 ? run_rows<128, true, false>(a, runs, st) : run_rows<128, false, false>(a, runs, st);
+}
+
+}  // namespace qm

@@ -1,0 +1,287 @@
+// qm_attend.cuh -- what the kernels of cache_attend share: the arguments, how
+// the work is cut, and the join of items that several CTAs worked on.
+//
+// The work. Query heads that share a key head are rows over the same keys: a
+// sequence's new tokens and its group of G query heads make new*G rows (row r:
+// token r / G, head r % G of the group), cut into tiles of R rows. An item is one
+// row tile of one key head of one sequence; its work is its span of keys in units
+// of kUnit keys, from the first key that any of its rows sees to the last (one
+// unit where they see none, whose rows are then written as empty). The units of
+// all items, in order of sequence, key head, tile and key, are cut into as many
+// equal runs as there are CTAs: lengths of any mix keep every SM busy to the end,
+// and the host needs to know none of them. Each CTA finds its run from the
+// lengths itself. A CTA that has all of an item writes its rows; one that has a
+// part leaves its unnormalised sums, with their maximum and total, in the
+// workspace, and attend_join_kernel adds an item's parts in order of key. The
+// cut depends on the lengths alone, so the same call gives the same bits.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "qm_device.cuh"
+#include "qm_internal.h"
+
+namespace qm {
+namespace attend {
+
+constexpr int kUnit = 128;  // keys of a unit of work
+
+struct Args {
+    const uint16_t* q;
+    uint16_t* out;
+    float* lse;
+    int64_t q_ts, q_hs, o_ts, o_hs;
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    int64_t page_stride, head_stride, token_stride;  // elements
+    int64_t sps, shs, sts;
+    const int32_t *lens, *table, *q_off;
+    int64_t table_stride;
+    int cap;  // keys that the page table has room for
+    int seqs, tokens, each;
+    int heads, group, kv_heads, dim;
+    int page_size, pages;
+    int window;  // 0: none
+    float scale2;  // scale * log2(e): scores are kept in powers of two
+    // workspace
+    int* desc;     // [grid][8], see Piece
+    float2* ml;    // [grid][2][R]: maximum and total of each row
+    float* part;   // [grid][2][R][DP]
+};
+
+// desc[8] of a CTA: [0] its first part: 0 none, 1 neither end of its item, 2 its
+// item's last; [1] 1 if its last part begins an item that it does not finish
+// (slot 1), whose [2] first token, [3] key head, [4] first row, [5] rows and
+// [6] first row's position, [7] new tokens follow.
+
+QM_DEV int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
+
+// One sequence of the batch: first row, new tokens, length.
+struct Seq {
+    int first, fresh, len;
+};
+
+QM_DEV Seq load_seq(const Args& a, int s) {
+    Seq q;
+    if (a.q_off) {
+        q.first = clampi(__ldg(a.q_off + s), 0, a.tokens);
+        q.fresh = clampi(__ldg(a.q_off + s + 1), q.first, a.tokens) - q.first;
+    } else {
+        q.first = s * a.each;
+        q.fresh = a.each;
+    }
+    q.len = max(__ldg(a.lens + s), 0);
+    return q;
+}
+
+// The first key that position p sees.
+QM_DEV int first_seen(const Args& a, int p) { return a.window && p >= a.window ? p - a.window + 1 : 0; }
+
+// The keys [lo, hi) that rows r0 .. r0 + R - 1 of a sequence see between them (hi
+// <= lo: none); p0 and p1: the first and last row's positions.
+struct Span {
+    int lo, hi, p0, p1, rows;
+    QM_DEV int u0() const { return hi > lo ? lo / kUnit : 0; }
+    QM_DEV int u1() const { return hi > lo ? (hi + kUnit - 1) / kUnit : 1; }
+};
+
+template <int R>
+QM_DEV Span tile_span(const Args& a, const Seq& s, unsigned tile) {
+    const unsigned r0 = tile * R, all = static_cast<unsigned>(s.fresh) * a.group;
+    Span t;
+    t.rows = static_cast<int>(min(static_cast<unsigned>(R), all - r0));
+    const int base = s.len - s.fresh;
+    t.p0 = base + static_cast<int>(r0 / a.group);
+    t.p1 = base + static_cast<int>((r0 + t.rows - 1) / a.group);
+    t.hi = min(a.cap, t.p1 + 1);
+    t.lo = first_seen(a, t.p0);
+    return t;
+}
+
+template <int R>
+QM_DEV unsigned tiles_of(const Args& a, const Seq& s) {
+    return (static_cast<unsigned>(s.fresh) * a.group + R - 1) / R;
+}
+
+// Units of one key head of a sequence.
+template <int R>
+QM_DEV int64_t head_units(const Args& a, const Seq& s) {
+    int64_t n = 0;
+    const unsigned tiles = tiles_of<R>(a, s);
+    for (unsigned t = 0; t < tiles; ++t) {
+        const Span p = tile_span<R>(a, s, t);
+        n += p.u1() - p.u0();
+    }
+    return n;
+}
+
+// A place in a CTA's run of units.
+template <int R>
+struct Cursor {
+    int64_t left;  // units of the run still to come, this one among them
+    int s, h;
+    unsigned tile, tiles;
+    Seq seq;
+    Span span;
+    int u, u1;
+
+    QM_DEV void enter(const Args& a) {  // the item's first unit
+        span = tile_span<R>(a, seq, tile);
+        u = span.u0();
+        u1 = span.u1();
+    }
+    QM_DEV bool first() const { return u == span.u0(); }
+    QM_DEV void next_item(const Args& a) {
+        if (++tile == tiles) {
+            tile = 0;
+            if (++h == a.kv_heads) {
+                h = 0;
+                do {
+                    if (++s >= a.seqs) return;  // only past the last unit
+                    seq = load_seq(a, s);
+                    tiles = tiles_of<R>(a, seq);
+                } while (tiles == 0);
+            }
+        }
+        enter(a);
+    }
+    QM_DEV void step(const Args& a) {
+        --left;
+        if (++u == u1 && left > 0) next_item(a);
+    }
+};
+
+// The calling warp's cursor at the start of run `c` of `runs` (left = 0: the run
+// is empty). Every lane returns the same.
+template <int R>
+QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
+    const int lane = threadIdx.x & 31;
+    Cursor<R> k = {};
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.seqs; s0 += 32) {
+        int64_t n = s0 + lane < a.seqs ? head_units<R>(a, load_seq(a, s0 + lane)) : 0;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
+        total += n;
+    }
+    total *= a.kv_heads;
+    if (total < runs) runs = static_cast<int>(total);  // the CTAs past the last unit have nothing
+    if (c >= runs) return k;
+    const int64_t from = total * c / runs, to = total * (c + 1) / runs;
+    k.left = to - from;
+    int64_t at = 0;  // units before sequence s0
+    for (int s0 = 0; s0 < a.seqs; s0 += 32) {
+        const int64_t n = s0 + lane < a.seqs ? head_units<R>(a, load_seq(a, s0 + lane)) * a.kv_heads : 0;
+        int64_t upto = n;  // units up to and with this lane's sequence
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, upto, m);
+            if (lane >= m) upto += o;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, at + upto > from);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            const int64_t before = at + __shfl_sync(0xffffffffu, upto - n, src);
+            const int64_t each = __shfl_sync(0xffffffffu, n, src) / a.kv_heads;
+            k.s = s0 + src;
+            k.seq = load_seq(a, k.s);
+            k.tiles = tiles_of<R>(a, k.seq);
+            int64_t rem = from - before;
+            k.h = static_cast<int>(rem / each);
+            rem -= k.h * each;
+            for (k.tile = 0;; ++k.tile) {
+                k.enter(a);
+                if (rem < k.u1 - k.u) break;
+                rem -= k.u1 - k.u;
+            }
+            k.u += static_cast<int>(rem);
+            return k;
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    k.left = 0;
+    return k;
+}
+
+// Element offset of key `key`'s row of head h, or -1 where it is not to be read.
+QM_DEV int64_t key_offset(const Args& a, int s, int h, int key, int lo, int hi, int64_t& scale_off) {
+    scale_off = 0;
+    if (key < lo || key >= hi) return -1;
+    const int p = key / a.page_size;
+    const int id = __ldg(a.table + s * a.table_stride + p);
+    if (id < 0 || id >= a.pages) return -1;
+    const int row = key - p * a.page_size;
+    scale_off = id * a.sps + h * a.shs + row * a.sts;
+    return id * a.page_stride + h * a.head_stride + row * a.token_stride;
+}
+
+QM_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+QM_DEV void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+QM_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+QM_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+QM_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool BF16>
+QM_DEV uint32_t pack16(float lo, float hi) {
+    if constexpr (BF16) {
+        uint32_t d;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    } else {
+        return pack_f16x2(lo, hi);
+    }
+}
+
+template <bool BF16>
+QM_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+            "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    } else {
+        mma_f16(d, a[0], a[1], a[2], a[3], b0, b1);
+    }
+}
+
+// A pair of 16-bit values of which one is infinite or NaN.
+template <bool BF16>
+QM_DEV bool nonfinite2(uint32_t v) {
+    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
+}
+
+// Where row r of an item goes: its token and query head.
+QM_DEV uint16_t* out_row(const Args& a, int first, int h, unsigned r, int64_t& lse_at) {
+    const unsigned i = r / a.group, g = r - i * a.group;
+    const int head = h * a.group + static_cast<int>(g);
+    const int64_t t = first + static_cast<int64_t>(i);
+    lse_at = t * a.heads + head;
+    return a.out + t * a.o_ts + head * a.o_hs;
+}
+
+// 1 / total; where the row sees keys but their weights add up to nothing (every score
+// -infinity) the quotient is the definition's 0/0, and 0 where it sees none.
+QM_DEV float inverse_total(const Args& a, int pos, float total) {
+    if (first_seen(a, pos) >= min(a.cap, pos + 1)) return 0.f;
+    return 1.0f / total;
+}
+
+QM_DEV float log_total(float top, float total) {
+    return total == 0.f ? __int_as_float(0xff800000) : (top + log2f(total)) * 0.69314718055994531f;
+}
+
+}  // namespace attend
+}  // namespace qm

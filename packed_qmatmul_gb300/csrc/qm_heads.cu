@@ -1,0 +1,471 @@
+// qm_heads.cu -- head norms with the rotation by position
+// (head_norm_rope_kernel) and the append of new keys and values to a paged
+// cache (cache_append_kernel).
+//
+// A head x of D elements becomes n_j = x_j w_j / sqrt(sum x^2 / D + eps), then
+// pair (a, b) of its first R elements turns: (a cos - b sin, b cos + a sin).
+// Every sum and product is float32; the one rounding is the result's.
+//
+// Both kernels only move memory: each element is read once and written once,
+// some seven operations between. A head belongs to LP = 8, 16 or 32 lanes of
+// a warp, eight elements to a lane, chosen so that both elements of a pair
+// meet in one lane: a rotated lane l holds elements 4l.. 4l+3 and R/2 + 4l ..
+// (halves) or 8l .. 8l+7 (adjacent pairs), two 8-byte accesses either way, and
+// the four cosines and sines 4l .. 4l+3. The norm's sum is the only thing lanes
+// exchange. A group of lanes takes HC heads of one token at a time, whose loads
+// are all in flight before the first is used; HC falls to 1 where the heads in
+// all would leave SMs without work.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qm_device.cuh"
+#include "qm_internal.h"
+
+namespace qm {
+namespace {
+
+struct Rot {
+    const float* table;
+    int64_t rows;
+    int half;   // dim / 2; 0: no rotation
+    int pairs;  // adjacent pairs
+};
+
+static Rot make_rot(const qm_rope* r) {
+    Rot t{nullptr, 0, 0, 0};
+    if (r) t = Rot{r->table, r->rows, r->dim / 2, r->style == QM_ROPE_PAIRS};
+    return t;
+}
+
+template <bool BF16>
+QM_DEV void unpack4(uint2 v, float* f) {
+    if constexpr (BF16) {
+        f[0] = __uint_as_float(v.x << 16);
+        f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(v.y << 16);
+        f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+    }
+}
+
+template <bool BF16>
+QM_DEV uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&t);
+    } else {
+        return pack_f16x2(lo, hi);
+    }
+}
+
+template <bool BF16>
+QM_DEV uint2 pack4(const float* f) {
+    return make_uint2(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]));
+}
+
+// Where a lane's elements lie in a head: four from a, four from b.
+struct Span {
+    int a, b;
+    bool on, turns;  // holds elements; they are rotated
+    int tab;         // its first cosine
+};
+
+QM_DEV Span lane_span(int l, int dim, const Rot& r) {
+    Span s;
+    s.on = l < dim / 8;
+    s.turns = l < r.half / 4;
+    s.tab = 4 * l;
+    s.a = 8 * l;
+    s.b = 8 * l + 4;
+    if (s.turns && !r.pairs) {
+        s.a = 4 * l;
+        s.b = r.half + 4 * l;
+    }
+    return s;
+}
+
+// The lane's cosines and sines of one position (zeros outside the table).
+QM_DEV void load_angles(const Rot& r, const Span& s, int64_t pos, float (&c)[4], float (&z)[4]) {
+    float4 cv = make_float4(0.f, 0.f, 0.f, 0.f), zv = cv;
+    if (s.turns && pos >= 0 && pos < r.rows) {
+        const float* row = r.table + pos * (2 * r.half) + s.tab;
+        cv = __ldg(reinterpret_cast<const float4*>(row));
+        zv = __ldg(reinterpret_cast<const float4*>(row + r.half));
+    }
+    c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+    z[0] = zv.x; z[1] = zv.y; z[2] = zv.z; z[3] = zv.w;
+}
+
+// Norm and rotation of one head spread over LP lanes, in place.
+template <int LP>
+QM_DEV void norm_turn(float (&x)[8], const float (&w)[8], bool norm, float eps, float inv_dim, const Span& s, bool pairs,
+                      const float (&c)[4], const float (&z)[4]) {
+    if (norm) {
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = fmaf(x[i], x[i], q);
+#pragma unroll
+        for (int m = LP / 2; m > 0; m >>= 1) q += __shfl_xor_sync(0xffffffffu, q, m);
+        const float f = rsqrtf(fmaf(q, inv_dim, eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i];
+    }
+    if (s.turns) {
+        if (pairs) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = a * c[i] - b * z[i];
+                x[2 * i + 1] = b * c[i] + a * z[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[i], b = x[4 + i];
+                x[i] = a * c[i] - b * z[i];
+                x[4 + i] = b * c[i] + a * z[i];
+            }
+        }
+    }
+}
+
+QM_DEV uint2 ld8(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
+
+// ------------------------------------------------------------ head_norm_rope
+struct Set {
+    const uint16_t* x;
+    uint16_t* y;
+    const uint16_t* w;
+    int64_t xts, xhs, yts, yhs;
+    int heads, chunk0;  // first chunk of HC heads
+};
+
+struct NormRopeArgs {
+    Set set[QM_MAX_HEAD_SETS];
+    int count, chunks, tokens, dim, pos64;
+    float eps;
+    Rot rot;
+    const void* positions;
+};
+
+template <int LP, int HC, bool BF16>
+__global__ void __launch_bounds__(256) head_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+    const int l = threadIdx.x % LP;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / LP) + threadIdx.x / LP;
+    const Span sp = lane_span(l, a.dim, a.rot);
+    const bool live = t < a.tokens && sp.on;
+    const float inv_dim = 1.0f / static_cast<float>(a.dim);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    float c[4], z[4];
+    int64_t pos = 0;
+    if (a.rot.half && live)
+        pos = a.pos64 ? static_cast<const int64_t*>(a.positions)[t] : static_cast<const int32_t*>(a.positions)[t];
+    load_angles(a.rot, sp, live ? pos : -1, c, z);
+    for (int chunk = blockIdx.y; chunk < a.chunks; chunk += gridDim.y) {
+        int i = 0;
+#pragma unroll
+        for (int j = 1; j < QM_MAX_HEAD_SETS; ++j)
+            if (j < a.count && chunk >= a.set[j].chunk0) i = j;
+        const Set& s = a.set[i];
+        const int h0 = (chunk - s.chunk0) * HC;
+        uint2 va[HC], vb[HC];
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            va[j] = vb[j] = make_uint2(0u, 0u);
+            if (live && h0 + j < s.heads) {
+                const uint16_t* x = s.x + t * s.xts + (h0 + j) * s.xhs;
+                va[j] = ld8(x + sp.a);
+                vb[j] = ld8(x + sp.b);
+            }
+        }
+        const bool norm = s.w != nullptr;
+        float w[8] = {};
+        if (norm && sp.on) {
+            unpack4<BF16>(ld8(s.w + sp.a), w);
+            unpack4<BF16>(ld8(s.w + sp.b), w + 4);
+        }
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            float x[8];
+            unpack4<BF16>(va[j], x);
+            unpack4<BF16>(vb[j], x + 4);
+            norm_turn<LP>(x, w, norm, a.eps, inv_dim, sp, a.rot.pairs, c, z);
+            if (live && h0 + j < s.heads) {
+                uint16_t* y = s.y + t * s.yts + (h0 + j) * s.yhs;
+                *reinterpret_cast<uint2*>(y + sp.a) = pack4<BF16>(x);
+                *reinterpret_cast<uint2*>(y + sp.b) = pack4<BF16>(x + 4);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ cache_append
+struct AppendArgs {
+    const uint16_t *k, *v, *w;
+    int64_t kts, khs, vts, vhs;
+    uint8_t *kc, *vc;
+    float *ks, *vs;
+    int64_t page_stride, head_stride, token_stride;
+    int64_t sps, shs, sts;
+    const int32_t *lens, *table, *q_off;
+    int64_t table_width, table_stride;
+    int seqs, tokens, each;  // each: rows of a sequence where q_off is null
+    int heads, dim, page_size, pages, chunks;
+    float eps;
+    Rot rot;
+};
+
+// The cache row of new token t: its page and row in the page, or page -1 where
+// nothing is stored; pos its position.
+QM_DEV void token_place(const AppendArgs& a, int64_t t, int& page, int& row, int64_t& pos) {
+    page = -1;
+    row = 0;
+    pos = -1;
+    int s, first, next;
+    if (!a.q_off) {
+        s = static_cast<int>(t / a.each);
+        first = s * a.each;
+        next = first + a.each;
+    } else {
+        // sequences of equal lengths are guessed; else the last s with q_off[s] <= t
+        s = static_cast<int>(t * a.seqs / a.tokens);
+        first = __ldg(a.q_off + s);
+        next = __ldg(a.q_off + s + 1);
+        if (!(first <= t && t < next)) {
+            int lo = 0, hi = a.seqs;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(a.q_off + mid) <= t) lo = mid;
+                else hi = mid;
+            }
+            s = lo;
+            first = __ldg(a.q_off + s);
+            next = __ldg(a.q_off + s + 1);
+            if (!(first <= t && t < next)) return;  // a row of no sequence
+        }
+    }
+    pos = static_cast<int64_t>(__ldg(a.lens + s)) - next + t;
+    if (pos < 0) return;
+    const int64_t p = pos / a.page_size;
+    if (p >= a.table_width) return;
+    const int id = __ldg(a.table + s * a.table_stride + p);
+    if (id < 0 || id >= a.pages) return;
+    page = id;
+    row = static_cast<int>(pos - p * a.page_size);
+}
+
+// A head's 8-bit codes and scale, by the rules qm_quantize_q8_0 states with a
+// float32 scale.
+template <int LP>
+QM_DEV float quantize_head(const float (&x)[8], int8_t (&q)[8]) {
+    float amax = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        amax = fmaxf(amax, fabsf(x[i]));
+        nan = nan || isnan(x[i]);
+    }
+    if (nan) amax = __int_as_float(0x7f800001);  // stands for a NaN: as an integer above infinity
+#pragma unroll
+    for (int m = LP / 2; m > 0; m >>= 1)  // magnitudes compare as integers do
+        amax = __int_as_float(max(__float_as_int(amax), __shfl_xor_sync(0xffffffffu, __float_as_int(amax), m)));
+    const bool plain = __float_as_int(amax) < 0x7f800000;
+    const float d = amax / 127.0f;
+    const float inv = d == 0.f ? 0.f : 1.0f / d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float p = x[i] * inv;
+        q[i] = plain && isfinite(p) ? static_cast<int8_t>(roundf(p)) : static_cast<int8_t>(0);
+    }
+    return plain ? d : (__float_as_int(amax) == 0x7f800000 ? __int_as_float(0x7f800000) : __int_as_float(0x7fc00000));
+}
+
+template <int LP, int HC, bool BF16, bool I8>
+__global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ AppendArgs a) {
+    const int l = threadIdx.x % LP;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / LP) + threadIdx.x / LP;
+    const Span sp = lane_span(l, a.dim, a.rot);
+    const float inv_dim = 1.0f / static_cast<float>(a.dim);
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const bool mine = t < a.tokens;
+    const bool on = mine && sp.on;
+    for (int chunk = blockIdx.y; chunk < a.chunks; chunk += gridDim.y) {
+        const int h0 = chunk * HC;
+        uint2 ka[HC], kb[HC];
+        uint4 vv[HC];
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            ka[j] = kb[j] = make_uint2(0u, 0u);
+            vv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (on && h0 + j < a.heads) {
+                const uint16_t* k = a.k + t * a.kts + (h0 + j) * a.khs;
+                ka[j] = ld8(k + sp.a);
+                kb[j] = ld8(k + sp.b);
+                vv[j] = *reinterpret_cast<const uint4*>(a.v + t * a.vts + (h0 + j) * a.vhs + 8 * l);
+            }
+        }
+        int page = -1, row = 0;
+        int64_t pos = -1;
+        if (mine) token_place(a, t, page, row, pos);
+        float c[4], z[4];
+        load_angles(a.rot, sp, pos, c, z);
+        const bool store = on && page >= 0;
+        const bool norm = a.w != nullptr;
+        float w[8] = {};
+        if (norm && sp.on) {
+            unpack4<BF16>(ld8(a.w + sp.a), w);
+            unpack4<BF16>(ld8(a.w + sp.b), w + 4);
+        }
+        const int64_t base = page * a.page_stride + row * a.token_stride;
+#pragma unroll
+        for (int j = 0; j < HC; ++j) {
+            float x[8];
+            unpack4<BF16>(ka[j], x);
+            unpack4<BF16>(kb[j], x + 4);
+            norm_turn<LP>(x, w, norm, a.eps, inv_dim, sp, a.rot.pairs, c, z);
+            const int64_t at = base + (h0 + j) * a.head_stride;
+            const bool st = store && h0 + j < a.heads;
+            if constexpr (!I8) {
+                if (st) {
+                    uint16_t* kc = reinterpret_cast<uint16_t*>(a.kc) + at;
+                    *reinterpret_cast<uint2*>(kc + sp.a) = pack4<BF16>(x);
+                    *reinterpret_cast<uint2*>(kc + sp.b) = pack4<BF16>(x + 4);
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.vc) + at + 8 * l) = vv[j];
+                }
+            } else {
+                const int64_t sat = page * a.sps + row * a.sts + (h0 + j) * a.shs;
+                int8_t q[8];
+                float d = quantize_head<LP>(x, q);
+                if (st) {
+                    *reinterpret_cast<char4*>(a.kc + at + sp.a) = make_char4(q[0], q[1], q[2], q[3]);
+                    *reinterpret_cast<char4*>(a.kc + at + sp.b) = make_char4(q[4], q[5], q[6], q[7]);
+                    if (l == 0) a.ks[sat] = d;
+                }
+                unpack4<BF16>(make_uint2(vv[j].x, vv[j].y), x);
+                unpack4<BF16>(make_uint2(vv[j].z, vv[j].w), x + 4);
+                d = quantize_head<LP>(x, q);
+                if (st) {
+                    *reinterpret_cast<char4*>(a.vc + at + 8 * l) = make_char4(q[0], q[1], q[2], q[3]);
+                    *reinterpret_cast<char4*>(a.vc + at + 8 * l + 4) = make_char4(q[4], q[5], q[6], q[7]);
+                    if (l == 0) a.vs[sat] = d;
+                }
+            }
+        }
+    }
+}
+
+// Lanes to a head.
+static int lanes_for(int dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
+
+template <int LP, int HC>
+static cudaError_t run_norm_rope(NormRopeArgs& a, bool bf16, cudaStream_t st) {
+    int chunks = 0;
+    for (int i = 0; i < a.count; ++i) {
+        a.set[i].chunk0 = chunks;
+        chunks += (a.set[i].heads + HC - 1) / HC;
+    }
+    a.chunks = chunks;
+    const int per = 256 / LP;
+    // few tokens: blocks of fewer groups, so that no block idles for lack of tokens
+    const int groups = a.tokens >= per ? per : std::max(32 / LP, a.tokens);
+    const unsigned threads = static_cast<unsigned>((groups * LP + 31) / 32 * 32);
+    const int gpb = static_cast<int>(threads) / LP;
+    const dim3 grid(static_cast<unsigned>((a.tokens + gpb - 1) / gpb), static_cast<unsigned>(std::min(chunks, 65535)));
+    return bf16 ? launch_pdl(head_norm_rope_kernel<LP, HC, true>, grid, threads, 0, st, a)
+                : launch_pdl(head_norm_rope_kernel<LP, HC, false>, grid, threads, 0, st, a);
+}
+
+template <int LP, int HC>
+static cudaError_t run_append(AppendArgs& a, bool bf16, bool i8, cudaStream_t st) {
+    a.chunks = (a.heads + HC - 1) / HC;
+    const int per = 256 / LP;
+    const int groups = a.tokens >= per ? per : std::max(32 / LP, a.tokens);
+    const unsigned threads = static_cast<unsigned>((groups * LP + 31) / 32 * 32);
+    const int gpb = static_cast<int>(threads) / LP;
+    const dim3 grid(static_cast<unsigned>((a.tokens + gpb - 1) / gpb), static_cast<unsigned>(std::min(a.chunks, 65535)));
+    if (i8)
+        return bf16 ? launch_pdl(cache_append_kernel<LP, HC, true, true>, grid, threads, 0, st, a)
+                    : launch_pdl(cache_append_kernel<LP, HC, false, true>, grid, threads, 0, st, a);
+    return bf16 ? launch_pdl(cache_append_kernel<LP, HC, true, false>, grid, threads, 0, st, a)
+                : launch_pdl(cache_append_kernel<LP, HC, false, false>, grid, threads, 0, st, a);
+}
+
+}  // namespace
+
+// Heads that a group of lanes takes at once: four where that still gives every
+// SM several blocks, else one.
+static bool many_heads(int64_t tokens, int64_t heads, int lp) { return tokens * heads * lp >= int64_t(4) * 256 * 8 * num_sms(); }
+
+cudaError_t launch_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void* const* weights, int count,
+                                  int64_t tokens, int dim, float eps, const qm_rope* rope, const void* positions,
+                                  int pos64, cudaStream_t st) {
+    NormRopeArgs a = {};
+    int64_t heads = 0;
+    for (int i = 0; i < count; ++i) {
+        a.set[i] = Set{static_cast<const uint16_t*>(xs[i].data), static_cast<uint16_t*>(outs[i].data),
+                       static_cast<const uint16_t*>(weights ? weights[i] : nullptr), xs[i].token_stride,
+                       xs[i].head_stride, outs[i].token_stride, outs[i].head_stride, xs[i].heads, 0};
+        heads += xs[i].heads;
+    }
+    a.count = count;
+    a.tokens = static_cast<int>(tokens);
+    a.dim = dim;
+    a.pos64 = pos64;
+    a.eps = eps;
+    a.rot = make_rot(rope);
+    a.positions = positions;
+    const bool bf16 = xs[0].dtype == QM_BF16;
+    const int lp = lanes_for(dim);
+    const bool many = many_heads(tokens, heads, lp);
+    if (lp == 8) return many ? run_norm_rope<8, 4>(a, bf16, st) : run_norm_rope<8, 1>(a, bf16, st);
+    if (lp == 16) return many ? run_norm_rope<16, 4>(a, bf16, st) : run_norm_rope<16, 1>(a, bf16, st);
+    return many ? run_norm_rope<32, 4>(a, bf16, st) : run_norm_rope<32, 1>(a, bf16, st);
+}
+
+cudaError_t launch_cache_append(const qm_cache& c, const qm_batch& b, const qm_heads& k, const qm_heads& v,
+                                const void* k_weight, float eps, const qm_rope* rope, cudaStream_t st) {
+    AppendArgs a = {};
+    a.k = static_cast<const uint16_t*>(k.data);
+    a.v = static_cast<const uint16_t*>(v.data);
+    a.w = static_cast<const uint16_t*>(k_weight);
+    a.kts = k.token_stride;
+    a.khs = k.head_stride;
+    a.vts = v.token_stride;
+    a.vhs = v.head_stride;
+    a.kc = static_cast<uint8_t*>(c.k);
+    a.vc = static_cast<uint8_t*>(c.v);
+    a.ks = c.k_scales;
+    a.vs = c.v_scales;
+    a.page_stride = c.page_stride;
+    a.head_stride = c.head_stride;
+    a.token_stride = c.token_stride;
+    a.sps = c.scale_page_stride;
+    a.shs = c.scale_head_stride;
+    a.sts = c.scale_token_stride;
+    a.lens = b.lens;
+    a.table = b.page_table;
+    a.q_off = b.q_offsets;
+    a.table_width = b.table_width;
+    a.table_stride = b.table_stride;
+    a.seqs = b.seqs;
+    a.tokens = static_cast<int>(b.tokens);
+    a.each = b.q_offsets ? 0 : static_cast<int>(b.tokens / b.seqs);
+    a.heads = c.heads;
+    a.dim = c.dim;
+    a.page_size = c.page_size;
+    a.pages = static_cast<int>(c.pages);
+    a.eps = eps;
+    a.rot = make_rot(rope);
+    const bool bf16 = k.dtype == QM_BF16, i8 = c.dtype == QM_I8;
+    const bool many = many_heads(b.tokens, c.heads, lanes_for(c.dim));
+    if (lanes_for(c.dim) == 8) return many ? run_append<8, 2>(a, bf16, i8, st) : run_append<8, 1>(a, bf16, i8, st);
+    return many ? run_append<16, 2>(a, bf16, i8, st) : run_append<16, 1>(a, bf16, i8, st);
+}
+
+}  // namespace qm

@@ -33,6 +33,10 @@ struct WDesc {
 void set_error(const std::string& msg);
 qm_status fail(qm_status st, const std::string& msg);
 qm_status cuda_fail(cudaError_t e, const char* what);
+qm_status check_launch(cudaError_t e, const char* what);  // QM_OK or cuda_fail
+
+bool aligned16(const void* p);
+bool mul_ok(int64_t a, int64_t b, int64_t* out);  // a * b without overflow, both >= 0
 
 // Validates w and fills d. On failure sets the message and returns QM_EINVAL.
 qm_status validate_weight(const qm_weight* w, WDesc* d);
@@ -144,6 +148,17 @@ qm_status apply_experts_checked(const qm_weight* w, const void* ids, int32_t id_
                                 int64_t topk, const void* x, int64_t x_rows, int32_t x_dtype, void* y,
                                 void* workspace, size_t workspace_bytes, qm_stream_t stream,
                                 bool allow_tensor);
+
+// Head norms, rotation and the paged cache (qm_heads.cu, qm_attend.cu); the
+// arguments are validated (qm_cache.cu).
+cudaError_t launch_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void* const* weights, int count,
+                                  int64_t tokens, int dim, float eps, const qm_rope* rope, const void* positions,
+                                  int pos64, cudaStream_t st);
+cudaError_t launch_cache_append(const qm_cache& c, const qm_batch& b, const qm_heads& k, const qm_heads& v,
+                                const void* k_weight, float eps, const qm_rope* rope, cudaStream_t st);
+size_t attend_workspace_bytes(const qm_cache& c, const qm_batch& b, int q_heads);
+cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_heads& q, const qm_heads& out,
+                                float* lse, float scale, int64_t window, void* workspace, cudaStream_t st);
 
 // One warp waiting on a barrier nothing arrives at, giving up after limit_ns.
 cudaError_t launch_wait_timeout(uint64_t limit_ns, cudaStream_t st);
