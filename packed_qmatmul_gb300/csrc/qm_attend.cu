@@ -20,9 +20,10 @@
 // the next item's copies are already under way.
 //
 // 8-bit codes are exact in both 16-bit types, so they enter the products as they
-// are: a key's scale multiplies its score, a value's scale its weight. For float16 the
-// running maximum then includes the values' scales, which keeps scaled weights
-// within [0, 2^8] whatever the scales are.
+// are: a key's scale multiplies its score, a value's scale its weight. Scaled weights
+// and value codes are float16 whatever q's type (three bits more than bfloat16, whose
+// range they do not need: the running maximum includes the values' scales, which
+// keeps them within [0, 2^8]).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -71,35 +72,13 @@ QM_DEV void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 
-// Signed bytes 0 and 2 of x as a pair of 16-bit values, exactly. bfloat16 has eight
-// significant bits: 128 + the low seven bits, less 128 or 256 by the sign bit;
-// float16: 1024 + the code with its sign bit turned (code + 128), less 1152.
-template <bool BF16>
-QM_DEV uint32_t codes16(uint32_t x) {
-    if constexpr (BF16) {
-        const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&d);
-    } else {
-        const uint32_t a = (x & 0x00FF00FFu) ^ 0x64806480u, b = 0x64806480u;
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&d);
-    }
-}
-
-// log2 of a value scale, held within 2^+-30 (zero and NaN: the low end).
-QM_DEV float scale_log2(float s) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
-    return fminf(fmaxf(y, -30.f), 30.f);
-}
-
 template <int DP, bool BF16, bool I8>
 __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __grid_constant__ Args a) {
     using L = Lay<DP, I8>;
     constexpr int ST = L::kStages;
     constexpr int KK = DP / 16;
-    constexpr float kLift = BF16 ? 0.f : 8.f;  // float16 weights in [0, 2^8]: the small ones keep their bits
+    constexpr bool PBF = BF16 && !I8;           // type of the weights and values in their product
+    constexpr float kLift = PBF ? 0.f : 8.f;    // float16 weights in [0, 2^8]: the small ones keep their bits
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -207,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 
         const int key0 = now.u * kUnit + warp * 16;
         const Span& sp = now.span;
-        if (key0 < sp.hi && key0 + 16 > sp.lo) {
+        if (key0 < sp.hi && key0 + 15 >= sp.lo) {
             const uint32_t kb = ring + slot * L::kStage, vb = kb + L::kPart;
             float s[2][4] = {};
             if constexpr (!I8) {
@@ -262,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     const uint2 sc = lds_v2(kb + 2 * L::kPart + 64 + 4 * (8 * n + 2 * t));
                     vs[n][0] = __uint_as_float(sc.x);
                     vs[n][1] = __uint_as_float(sc.y);
-                    lv[n][0] = BF16 ? 0.f : scale_log2(vs[n][0]);
-                    lv[n][1] = BF16 ? 0.f : scale_log2(vs[n][1]);
+                    lv[n][0] = scale_log2(vs[n][0]);
+                    lv[n][1] = scale_log2(vs[n][1]);
                 }
             }
             float from[2];
@@ -275,7 +254,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        m = fmaxf(m, (I8 && !BF16) ? s[n][2 * x + e] + lv[n][e] : s[n][2 * x + e]);
+                        m = fmaxf(m, I8 ? s[n][2 * x + e] + lv[n][e] : s[n][2 * x + e]);
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 grown = grown || m > top[x];
@@ -305,8 +284,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     sum[e >> 1] += p[n][e];
                     if constexpr (I8) p[n][e] = (hidden >> (4 * n + e)) & 1 ? 0.f : p[n][e] * vs[n][e & 1];
                 }
-            const uint32_t pa[4] = {pack16<BF16>(p[0][0], p[0][1]), pack16<BF16>(p[0][2], p[0][3]),
-                                    pack16<BF16>(p[1][0], p[1][1]), pack16<BF16>(p[1][2], p[1][3])};
+            const uint32_t pa[4] = {pack16<PBF>(p[0][0], p[0][1]), pack16<PBF>(p[0][2], p[0][3]),
+                                    pack16<PBF>(p[1][0], p[1][1]), pack16<PBF>(p[1][2], p[1][3])};
             if constexpr (!I8) {
                 // A value that only some of the rows see must not reach the others: 0 times an
                 // infinity or NaN is NaN. Where the rows differ and such a value is there, the
@@ -368,7 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t pick = 0x0400u + 0x0101u * i;  // byte i of the two keys, to bytes 0 and 2
-                        mma16<BF16>(acc[4 * jb + i], pa, codes16<BF16>(prmt(w[0], w[1], pick)), codes16<BF16>(prmt(w[2], w[3], pick)));
+                        mma16<PBF>(acc[4 * jb + i], pa, codes16<PBF>(prmt(w[0], w[1], pick)), codes16<PBF>(prmt(w[2], w[3], pick)));
                     }
                 }
             }
@@ -440,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm - kLift, total);
                     } else {
                         *reinterpret_cast<float4*>(a.part + (static_cast<int64_t>(part) * kRows + row) * DP + 4 * c4) = o;
-                        if (c4 == 0) a.ml[part * kRows + row] = make_float2(mm, total);
+                        if (c4 == 0) a.ml[part * kRows + row] = make_float2(mm - kLift, total);
                     }
                 }
                 __syncthreads();
@@ -471,7 +450,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 // Joins the parts of one item: block x of a CTA whose last part begins an item
 // adds that part and the first parts of the CTAs after it, up to the item's last.
 template <int R, int DP, bool BF16>
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Args a, int runs, float lift) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Args a, int runs) {
     constexpr int C4 = DP / 4, G = 256 / C4;  // groups of threads that take every G-th part
     __shared__ float4 so[G][C4];
     __shared__ float2 sm[G];
@@ -522,7 +501,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
             const float inv = inverse_total(a, at, tt);
             if (4 * c4 < a.dim)
                 *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
-            if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm - lift, tt);
+            if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm, tt);
         }
         __syncthreads();
     }
@@ -532,11 +511,29 @@ template <int DP, bool BF16, bool I8>
 cudaError_t run_rows(const Args& a, int runs, cudaStream_t st) {
     auto kern = attend_rows_kernel<DP, BF16, I8>;
     constexpr int smem = Lay<DP, I8>::kSmem;
+    static_assert(smem <= 227 * 1024, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(runs), kWarps * 32, smem, st, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(attend_join_kernel<kRows, DP, BF16>, dim3(runs, kRows), 256, 0, st, a, runs, BF16 ? 0.f : 8.f);
+    return launch_pdl(kern, dim3(runs), kWarps * 32, smem, st, a);
+}
+
+cudaError_t launch_rows(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st) {
+    if (dp == 64) {
+        if (i8) return bf16 ? run_rows<64, true, true>(a, runs, st) : run_rows<64, false, true>(a, runs, st);
+        return bf16 ? run_rows<64, true, false>(a, runs, st) : run_rows<64, false, false>(a, runs, st);
+    }
+    if (i8) return bf16 ? run_rows<128, true, true>(a, runs, st) : run_rows<128, false, true>(a, runs, st);
+    return bf16 ? run_rows<128, true, false>(a, runs, st) : run_rows<128, false, false>(a, runs, st);
+}
+
+template <int R>
+cudaError_t launch_join(const Args& a, int runs, int dp, bool bf16, cudaStream_t st) {
+    const dim3 grid(runs, 16);
+    if (dp == 64)
+        return bf16 ? launch_pdl(attend_join_kernel<R, 64, true>, grid, 256, 0, st, a, runs)
+                    : launch_pdl(attend_join_kernel<R, 64, false>, grid, 256, 0, st, a, runs);
+    return bf16 ? launch_pdl(attend_join_kernel<R, 128, true>, grid, 256, 0, st, a, runs)
+                : launch_pdl(attend_join_kernel<R, 128, false>, grid, 256, 0, st, a, runs);
 }
 
 // Workspace: [runs][8] int, [runs][2][R] float2, [runs][2][R][DP] float.
@@ -551,20 +548,28 @@ Ws workspace_layout(int runs, int rows, int dp) {
     return w;
 }
 
+// Whether the rows that share a key head (the most of any sequence, if the caller
+// said; else the average) are few.
+bool few_rows(const qm_batch& b, int group) {
+    const int64_t most = b.max_new > 0 ? std::min<int64_t>(b.max_new, b.tokens) : (b.tokens + b.seqs - 1) / b.seqs;
+    return most * group <= kRows;
+}
+
 }  // namespace
 }  // namespace attend
 
 using namespace attend;
 
-size_t attend_workspace_bytes(const qm_cache& c, const qm_batch&, int) {
-    return workspace_layout(num_sms(), kRows, c.dim <= 64 ? 64 : 128).all;
+size_t attend_workspace_bytes(const qm_cache& c, const qm_batch& b, int q_heads) {
+    return workspace_layout(num_sms(), few_rows(b, q_heads / c.heads) ? kRows : kTileRows, c.dim <= 64 ? 64 : 128).all;
 }
 
 cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_heads& q, const qm_heads& out,
                                 float* lse, float scale, int64_t window, void* workspace, cudaStream_t st) {
     const int dp = c.dim <= 64 ? 64 : 128;
     const int runs = num_sms();
-    const Ws ws = workspace_layout(runs, kRows, dp);
+    const bool few = few_rows(b, q.heads / c.heads);
+    const Ws ws = workspace_layout(runs, few ? kRows : kTileRows, dp);
     uint8_t* wb = static_cast<uint8_t*>(workspace);
     Args a = {};
     a.q = static_cast<const uint16_t*>(q.data);
@@ -605,12 +610,9 @@ cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_h
     a.ml = reinterpret_cast<float2*>(wb + ws.ml);
     a.part = reinterpret_cast<float*>(wb + ws.part);
     const bool bf16 = q.dtype == QM_BF16, i8 = c.dtype == QM_I8;
-    if (dp == 64) {
-        if (i8) return bf16 ? run_rows<64, true, true>(a, runs, st) : run_rows<64, false, true>(a, runs, st);
-        return bf16 ? run_rows<64, true, false>(a, runs, st) : run_rows<64, false, false>(a, runs, st);
-    }
-    if (i8) return bf16 ? run_rows<128, true, true>(a, runs, st) : run_rows<128, false, true>(a, runs, st);
-    return bf16 ? run_rows<128, true, false>(a, runs, st) : run_rows<128, false, false>(a, runs, st);
+    const cudaError_t e = few ? launch_rows(a, runs, dp, bf16, i8, st) : launch_tiles(a, runs, dp, bf16, i8, st);
+    if (e != cudaSuccess) return e;
+    return few ? launch_join<kRows>(a, runs, dp, bf16, st) : launch_join<kTileRows>(a, runs, dp, bf16, st);
 }
 
 }  // namespace qm

@@ -26,7 +26,8 @@
 namespace qm {
 namespace attend {
 
-constexpr int kUnit = 128;  // keys of a unit of work
+constexpr int kUnit = 128;      // keys of a unit of work
+constexpr int kTileRows = 256;  // rows of an item of attend_tiles_kernel
 
 struct Args {
     const uint16_t* q;
@@ -84,7 +85,7 @@ QM_DEV int first_seen(const Args& a, int p) { return a.window && p >= a.window ?
 struct Span {
     int lo, hi, p0, p1, rows;
     QM_DEV int u0() const { return hi > lo ? lo / kUnit : 0; }
-    QM_DEV int u1() const { return hi > lo ? (hi + kUnit - 1) / kUnit : 1; }
+    QM_DEV int u1() const { return hi > lo ? (hi - 1) / kUnit + 1 : 1; }
 };
 
 template <int R>
@@ -256,6 +257,29 @@ QM_DEV void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
     }
 }
 
+// Signed bytes 0 and 2 of x as a pair of 16-bit values, exactly. bfloat16 has eight
+// significant bits: 128 + the low seven bits, less 128 or 256 by the sign bit;
+// float16: 1024 + the code with its sign bit turned (code + 128), less 1152.
+template <bool BF16>
+QM_DEV uint32_t codes16(uint32_t x) {
+    if constexpr (BF16) {
+        const uint32_t a = (x & 0x007F007Fu) | 0x43004300u, b = (x & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    } else {
+        const uint32_t a = (x & 0x00FF00FFu) ^ 0x64806480u, b = 0x64806480u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+}
+
+// log2 of a value scale, held within 2^+-30 (zero and NaN: the low end).
+QM_DEV float scale_log2(float s) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return fminf(fmaxf(y, -30.f), 30.f);
+}
+
 // A pair of 16-bit values of which one is infinite or NaN.
 template <bool BF16>
 QM_DEV bool nonfinite2(uint32_t v) {
@@ -282,6 +306,9 @@ QM_DEV float inverse_total(const Args& a, int pos, float total) {
 QM_DEV float log_total(float top, float total) {
     return total == 0.f ? __int_as_float(0xff800000) : (top + log2f(total)) * 0.69314718055994531f;
 }
+
+// attend_tiles_kernel (qm_attend_tc.cu).
+cudaError_t launch_tiles(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st);
 
 }  // namespace attend
 }  // namespace qm

@@ -1,0 +1,663 @@
+// qm_attend_tc.cu -- attention of new tokens over a paged cache for many rows to
+// a key head (attend_tiles_kernel: chunks of prompts), on the 5th-generation
+// tensor cores.
+//
+// The mathematics is qm_attend.cu's: one pass over the keys with the running
+// maximum and total of every row in float32. An item is 256 rows, two tiles of 128,
+// over the same keys; a unit of 128 keys costs each tile two products, S = Q K^T and
+// O += P V, of 128 x 128 x dim. What bounds it is those products as long as the
+// exponentials (one for every element of S) fit beside them, so the two tiles take
+// turns: while one tile's weights are formed, the tensor cores work on the other's.
+// One CTA per SM, three warpgroups:
+//  * warpgroups 0 and 1, one tile each, one row a thread: S from tensor memory to
+//    registers, weights P = 2^(t - ref) rounded to 16 bits back over it. ref follows
+//    the running maximum lazily: only when it has grown by kSlack (a factor of 2^8
+//    or 2^4) is O rescaled, which is exact in float32 whenever it happens; weights stay
+//    below 2^8 (bfloat16) or 2^12 (float16).
+//  * warp 8: issues the products: Q and K from shared memory (128-byte swizzle, K
+//    major), P from tensor memory, V from shared memory as it lies in the cache
+//    (rows of keys: MN major); S and O of both tiles fill the 512 tensor-memory columns.
+//  * warps 9..11: fill a ring of 32 KB slots (a unit's keys, then its values) by
+//    16-byte asynchronous copies, each row's place looked up in the page table; they
+//    take any page size, stride and length, fill what is not there with zeros, and
+//    publish a slot to the tensor cores with a proxy fence. 8-bit codes pass through
+//    their registers on the way and enter the products exactly.
+// Every wait is bounded; a wait that gives up raises the device flag and the CTA
+// winds down with its copies and products drained.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qm_attend.cuh"
+
+namespace qm {
+namespace attend {
+namespace {
+
+__device__ uint32_t g_err_attend = 0;
+
+constexpr int kRows = kTileRows;
+constexpr int kThreads = 384;
+constexpr int kLoaders = 3;  // warps
+
+// Shared memory: Q (two tiles of 128 rows x DP), the ring, scales of 8-bit codes,
+// barriers.
+template <int DP, bool I8>
+struct Lay {
+    static constexpr int kPanel = 128 * 128;           // 128 rows of 64 16-bit elements
+    static constexpr int kTile = kPanel * (DP / 64);   // 128 rows of a head
+    static constexpr int kQ = 2 * kTile;
+    static constexpr int kSlots = I8 ? 4 : DP == 128 ? 5 : 8;
+    static constexpr int kLag = 2;                     // 16-bit slots in flight that are not yet published
+    static constexpr int kScale = kQ + kSlots * kTile;  // [2][3][128] floats: key scales, value scales, their logarithms
+    static constexpr int kBars = kScale + (I8 ? 2 * 3 * 512 : 0);
+    static constexpr int kSmem = kBars + 256;
+};
+
+QM_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
+// Descriptor of values as they lie: rows of keys (the product's K), 64 elements (its
+// N) to a 128-byte swizzled row; 8-row groups 1024 bytes apart, panels of 64
+// elements kPanel bytes apart.
+QM_DEV uint64_t desc_rows_of_k(uint32_t addr, uint32_t panel) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>(panel >> 4) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+
+// Instruction descriptor, kind::f16, f32 sums, 128 x N; B K-major or (mn) MN-major.
+QM_DEV uint32_t idesc16(bool bf16, int N, bool mn) {
+    const uint32_t f = bf16 ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+QM_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+QM_DEV void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+}
+
+// Where 16-byte piece c of row r lies in a tile.
+template <int DP>
+QM_DEV uint32_t at16(int r, int c) {
+    return (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// O[row] += P[row] V over the unit's keys that the row sees, product by product:
+// for a unit in which rows see different keys and a value is infinite or NaN (0
+// times it would be NaN in rows that do not see it). p: the row's weights in tensor
+// memory (16-bit pairs), o: its sums, zeros instead if `fresh`; keys [a, b] are seen.
+template <int DP, bool BF16>
+__device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, uint32_t v, int a, int b) {
+#pragma unroll 1
+    for (int c = 0; c < DP / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(o + 32 * c, r);
+        tmem_wait_ld();
+        float acc[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] = fresh ? 0.f : __uint_as_float(r[i]);
+#pragma unroll 1
+        for (int kb = 0; kb < 8; ++kb) {
+            uint32_t w[8];
+            tmem_ld8(p + 8 * kb, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int key = 16 * kb + k;
+                const uint32_t h = (k & 1) ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
+                const float pk = BF16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+                const bool see = key >= a && key <= b;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 x = lds_v4(v + at16<DP>(key, 4 * c + q));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v0 = BF16 ? __uint_as_float(xs[e] << 16) : f16_bits_to_f32(xs[e] & 0xFFFFu);
+                        const float v1 = BF16 ? __uint_as_float(xs[e] & 0xFFFF0000u) : f16_bits_to_f32(xs[e] >> 16);
+                        if (see) {
+                            acc[8 * q + 2 * e] = fmaf(pk, v0, acc[8 * q + 2 * e]);
+                            acc[8 * q + 2 * e + 1] = fmaf(pk, v1, acc[8 * q + 2 * e + 1]);
+                        }
+                    }
+                }
+            }
+        }
+        uint32_t lo[16], hi[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lo[i] = __float_as_uint(acc[i]);
+            hi[i] = __float_as_uint(acc[16 + i]);
+        }
+        tmem_st16(o + 32 * c, lo);
+        tmem_st16(o + 32 * c + 16, hi);
+        tmem_wait_st();
+    }
+}
+
+template <int DP, bool BF16, bool I8>
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_constant__ Args a) {
+    using L = Lay<DP, I8>;
+    constexpr int NS = L::kSlots;
+    constexpr bool PBF = BF16 && !I8;  // type of the weights and values in their product
+    constexpr float kLift = PBF ? 0.f : 8.f, kSlack = PBF ? 8.f : 4.f;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sq = smem_u32(smem), ring = sq + L::kQ, b0 = sq + L::kBars;
+    auto kv_full = [&](int i) { return b0 + 8 * i; };
+    auto kv_free = [&](int i) { return b0 + 8 * (NS + i); };
+    const uint32_t q_free = b0 + 8 * (2 * NS), done = q_free + 8;
+    auto s_full = [&](int t) { return q_free + 16 + 8 * t; };
+    auto p_full = [&](int t) { return q_free + 32 + 8 * t; };
+    auto o_full = [&](int t) { return q_free + 48 + 8 * t; };
+    auto agreed = [&](int t) { return q_free + 64 + 8 * t; };
+    uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * (2 * NS) + 80);
+    uint32_t* tmem_slot = words;
+    volatile uint32_t* skip = words + 1;  // [2]: the tile's values were added without the tensor cores
+    uint32_t* odd_word = words + 3;       // [2][2]: a warp of the tile saw a value that is infinite or NaN
+
+    grid_launch_dependents();
+    grid_dependency_wait();
+    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x);
+    if (now.left == 0) {
+        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(kv_full(i), kLoaders);
+            mbar_init(kv_free(i), 1);
+        }
+        mbar_init(q_free, 1);
+        mbar_init(done, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), 4);
+            mbar_init(o_full(t), 1);
+            mbar_init(agreed(t), 4);
+            skip[t] = odd_word[t] = odd_word[2 + t] = 0;
+        }
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto give_up = [&]() { atomicOr(&g_err_attend, DEV_ERR_TIMEOUT); };
+    const int ksteps = (a.dim + 15) / 16;
+    // units of the run's part that `now` is in
+    auto part_units = [](const Cursor<kRows>& c) { return static_cast<int>(min(static_cast<int64_t>(c.u1 - c.u), c.left)); };
+    auto skip_part = [&](Cursor<kRows>& c, int n) {
+        c.left -= n;
+        c.u += n;
+        if (c.u == c.u1 && c.left > 0) c.next_item(a);
+    };
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ weights of one tile
+        const int t = warp >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
+        int nth = 0, parts = 0, checks = 0;  // units, parts and value checks of this tile so far
+        int64_t index = 0;       // units of the CTA so far
+        int first_part = 0;
+        bool ok = true;
+        while (now.left > 0 && ok) {
+            const int n = part_units(now);
+            const bool starts = now.first(), ends = now.u + n == now.u1, done_here = starts && ends;
+            const int rows = now.span.rows;
+            const unsigned R = now.tile * kRows + 128 * t + row;
+            const bool mine = 128 * t + row < rows;
+            const int pos = now.seq.len - now.seq.fresh + static_cast<int>(R / a.group);
+            const int kmin = mine ? first_seen(a, pos) : 0, kmax = mine ? min(pos, a.cap - 1) : -1;
+            float ref = -INFINITY, total = 0.f;
+            if (128 * t < rows) {
+                // keys that every row of the item sees lie within [all_lo, all_hi]
+                const int all_hi = min(now.span.p0, a.cap - 1), all_lo = first_seen(a, now.span.p1);
+                const bool differ = now.span.p0 != now.span.p1;
+                for (int j = 0; j < n; ++j, ++nth) {
+                    const int key0 = (now.u + j) * kUnit;
+                    const bool cut = key0 + kUnit - 1 > all_hi || key0 < all_lo;
+                    const int sa = max(kmin - key0, 0), sb = min(kmax - key0, kUnit - 1);  // the unit's keys that the row sees
+                    const int64_t vi = 2 * (index + j) + 1;  // the values' slot
+                    const int slot = static_cast<int>(vi % NS);
+                    const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
+                    if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
+                    if (I8 && !mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                    tc_fence_after();
+                    uint32_t raw[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, raw[c]);
+                    tmem_wait_ld();
+                    float s[128];
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(raw[i / 32][i % 32]);
+                    if constexpr (I8) {
+#pragma unroll
+                        for (int i = 0; i < 128; i += 4) {
+                            const float4 k = *reinterpret_cast<const float4*>(sc + i);
+                            s[i] *= k.x; s[i + 1] *= k.y; s[i + 2] *= k.z; s[i + 3] *= k.w;
+                        }
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i < sa || i > sb) s[i] = -INFINITY;
+                    }
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if constexpr (I8) {
+#pragma unroll
+                        for (int i = 0; i < 128; i += 4) {
+                            const float4 lv = *reinterpret_cast<const float4*>(sc + 256 + i);
+                            m[0] = fmaxf(m[0], s[i] + lv.x);
+                            m[1] = fmaxf(m[1], s[i + 1] + lv.y);
+                            m[2] = fmaxf(m[2], s[i + 2] + lv.z);
+                            m[3] = fmaxf(m[3], s[i + 3] + lv.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + 4 + e]);
+                        }
+                    }
+                    // scores of 8-bit codes are in powers of two already (their key scales hold the factor)
+                    const float top = max3(max3(m[0], m[1], m[2]), m[3], m[3]) * (I8 ? 1.f : a.scale2) - kLift;
+                    if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                        const float old = ref;
+                        ref = fmaxf(ref, top);
+                        const float f = ex2(old - (ref == -INFINITY ? 0.f : ref));
+                        total *= f;
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < DP / 16; ++c) {
+                                uint32_t r[16];
+                                tmem_ld16(to + 16 * c, r);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                                tmem_st16(to + 16 * c, r);
+                            }
+                        }
+                    }
+                    const float base = ref == -INFINITY ? 0.f : ref;
+                    const float2 sc2 = I8 ? make_float2(1.f, 1.f) : make_float2(a.scale2, a.scale2), nb = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int k = 32 * c + 2 * i;
+                            const float2 x = fma2(make_float2(s[k], s[k + 1]), sc2, nb);
+                            float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            sum[i & 1] = add2(sum[i & 1], p);
+                            if constexpr (I8) {
+                                p = mul2(p, *reinterpret_cast<const float2*>(sc + 128 + k));
+                                if (cut) {  // a scale that the row does not see may be infinite or NaN
+                                    if (k < sa || k > sb) p.x = 0.f;
+                                    if (k + 1 < sa || k + 1 > sb) p.y = 0.f;
+                                }
+                            }
+                            w[i] = pack16<PBF>(p.x, p.y);
+                        }
+                        tmem_st16(ts + 16 * c, w);
+                    }
+                    total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_wait_st();
+                    if constexpr (!I8) {
+                        bool odd = false;
+                        if (cut && differ) {
+                            if (!mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                            const uint32_t v = ring + slot * L::kTile;
+                            for (int c = 0; c < 2 * ksteps; ++c) {  // each thread looks at one key's values
+                                const uint4 x = lds_v4(v + at16<DP>(row, c));
+                                odd = odd || nonfinite2<BF16>(x.x) || nonfinite2<BF16>(x.y) || nonfinite2<BF16>(x.z) || nonfinite2<BF16>(x.w);
+                            }
+                            uint32_t* word = odd_word + 2 * (checks & 1) + t;
+                            if (odd) atomicOr(word, 1u);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(agreed(t));
+                            if (!mbar_wait(agreed(t), checks & 1)) { ok = false; break; }
+                            odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
+                            if (row == 0) odd_word[2 * (~checks & 1) + t] = 0;  // every warp has read it
+                            ++checks;
+                            if (odd) exact_values<DP, BF16>(ts, to, j == 0, v, sa, sb);
+                        }
+                        if (row == 0) skip[t] = odd ? 1u : 0u;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(t));
+                }
+                // ---- the part's end
+                if (ok && !mbar_wait(o_full(t), parts & 1)) ok = false;
+                ++parts;
+                tc_fence_after();
+                const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+                uint16_t* y = nullptr;
+                int64_t lse_at = 0;
+                float inv = 1.f;
+                if (mine && done_here) {
+                    y = out_row(a, now.seq.first, now.h, R, lse_at);
+                    inv = inverse_total(a, pos, total);
+                }
+                float* po = a.part + (static_cast<int64_t>(part) * kRows + 128 * t + row) * DP;
+#pragma unroll 1
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(to + 32 * c, r);
+                    tmem_wait_ld();
+                    if (!mine || !ok) continue;
+                    if (done_here) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack16<BF16>(__uint_as_float(r[8 * q + 2 * e]) * inv, __uint_as_float(r[8 * q + 2 * e + 1]) * inv);
+                            if (32 * c + 8 * q < a.dim) *reinterpret_cast<uint4*>(y + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<uint4*>(po + 32 * c + 4 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                    }
+                }
+                tc_fence_before();  // the next part's products come after these reads
+                if (mine && ok) {
+                    if (done_here) {
+                        if (a.lse) a.lse[lse_at] = log_total(ref, total);
+                    } else {
+                        a.ml[part * kRows + 128 * t + row] = make_float2(ref, total);
+                    }
+                }
+            }
+            if (threadIdx.x == 0 && !done_here && starts) {
+                int* d = a.desc + blockIdx.x * 8;
+                d[1] = 1;
+                d[2] = now.seq.first;
+                d[3] = now.h;
+                d[4] = static_cast<int>(now.tile * kRows);
+                d[5] = rows;
+                d[6] = now.seq.len - now.seq.fresh;
+            }
+            if (!starts) first_part = ends ? 2 : 1;
+            if (now.left == n && threadIdx.x == 0) {
+                a.desc[blockIdx.x * 8] = first_part;
+                if (!(starts && !ends)) a.desc[blockIdx.x * 8 + 1] = 0;
+            }
+            index += n;
+            skip_part(now, n);
+        }
+        if (!ok) give_up();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ products
+        const uint32_t id_s = idesc16(BF16, 128, false), id_o = idesc16(PBF, 16 * ksteps, true);
+        int64_t i = 0;  // slots so far
+        int nth[2] = {0, 0};
+        bool ok = true;
+        auto wait_slot = [&](int64_t k) { return mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1); };
+        auto scores = [&](int t, int64_t k) {  // S of tile t over the keys in slot k
+            if (elect_one()) {
+                const uint64_t qd = umma_desc_sw128(sq + t * L::kTile), kd = umma_desc_sw128(ring + static_cast<uint32_t>(k % NS) * L::kTile);
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk)
+                    if (kk < ksteps) {
+                        const uint32_t off = ((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4;
+                        umma_f16(tmem + 128 * t, qd + off, kd + off, id_s, kk > 0);
+                    }
+                umma_commit(s_full(t));
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint32_t bar) {
+            if (elect_one()) umma_commit(bar);
+            __syncwarp();
+        };
+        while (now.left > 0 && ok) {
+            const int n = part_units(now);
+            const int tiles = now.span.rows > 128 ? 2 : 1;
+            if (!(ok = wait_slot(i))) break;
+            tc_fence_after();
+            for (int t = 0; t < tiles; ++t) scores(t, i);
+            commit(kv_free(static_cast<int>(i % NS)));
+            if (n == 1) commit(q_free);
+            for (int j = 0; j < n && ok; ++j) {
+                for (int t = 0; t < tiles; ++t) {
+                    if (!(ok = mbar_wait(p_full(t), nth[t] & 1))) break;
+                    ++nth[t];
+                    if (t == 0 && !(ok = wait_slot(i + 1))) break;
+                    tc_fence_after();
+                    if (!skip[t] && elect_one()) {
+                        const uint64_t vd = desc_rows_of_k(ring + static_cast<uint32_t>((i + 1) % NS) * L::kTile, L::kPanel);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + ((kk * 2048) >> 4), id_o, j > 0 || kk > 0);
+                    }
+                    __syncwarp();
+                    if (t == tiles - 1) commit(kv_free(static_cast<int>((i + 1) % NS)));
+                    if (j == n - 1) {
+                        commit(o_full(t));
+                    } else {
+                        if (t == 0 && !(ok = wait_slot(i + 2))) break;
+                        tc_fence_after();
+                        scores(t, i + 2);
+                    }
+                }
+                if (!ok) break;
+                if (j < n - 1) {
+                    commit(kv_free(static_cast<int>((i + 2) % NS)));
+                    if (j == n - 2) commit(q_free);
+                }
+                i += 2;
+            }
+            skip_part(now, n);
+        }
+        if (!ok) give_up();
+        commit(done);  // drains whatever was issued
+        (void)mbar_wait(done, 0);
+    } else {
+        // ------------------------------------------------------------ copies
+        const int lw = warp - 9;
+        constexpr int C = DP / 8;           // 16-byte pieces of a 16-bit row
+        const int pieces = 2 * ksteps;      // of which the products read these
+        int64_t i = 0;                      // slots so far
+        int64_t published = 0;
+        int parts = 0;
+        bool ok = true;
+        auto publish = [&]() {  // the next slot in order: its copies have landed
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv_full(static_cast<int>(published % NS)));
+            ++published;
+        };
+        auto drain = [&]() {
+            cp_async_wait<0>();
+            while (published < i) publish();
+        };
+        int64_t place[4], splace[4];  // of rows lane + 32 x of the unit
+        auto look = [&](const Cursor<kRows>& c) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                place[x] = key_offset(a, c.s, c.h, c.u * kUnit + 32 * x + lane, c.span.lo, c.span.hi, splace[x]);
+        };
+        auto load_q = [&]() {
+            constexpr int per = 32 / C;
+            const int c = lane % C;
+            const int tiles = now.span.rows > 128 ? 2 : 1;
+            for (int r = lw * per + lane / C; r < 128 * tiles; r += kLoaders * per) {
+                const unsigned R = now.tile * kRows + r, tok = R / a.group, g = R - tok * a.group;
+                const bool on = r < now.span.rows && 8 * c < a.dim;
+                const uint16_t* src = a.q;
+                if (on) src += (now.seq.first + static_cast<int64_t>(tok)) * a.q_ts + (now.h * a.group + static_cast<int>(g)) * a.q_hs + 8 * c;
+                if (c < pieces) cp_async16(sq + (r >> 7) * L::kTile + at16<DP>(r & 127, c), src, on ? 16u : 0u);
+            }
+        };
+        look(now);
+        while (now.left > 0 && ok) {
+            const int n = part_units(now);
+            if (parts > 0) {
+                drain();  // nothing may wait for what is not published
+                if (!(ok = mbar_wait(q_free, (parts - 1) & 1))) break;
+            }
+            ++parts;
+            load_q();
+            for (int j = 0; j < n && ok; ++j) {
+                if constexpr (!I8) {
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const int slot = static_cast<int>(i % NS);
+                        if (i >= NS && !(ok = mbar_wait(kv_free(slot), ((i / NS) & 1) ^ 1))) break;
+                        const uint32_t dst = ring + slot * L::kTile;
+                        const uint8_t* src = v ? a.v : a.k;
+                        constexpr int per = 32 / C;
+                        const int c = lane % C;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < (32 / per + kLoaders - 1) / kLoaders; ++y) {
+                                const int grp = lw + kLoaders * y;
+                                if (grp < 32 / per) {
+                                    const int r = grp * per + lane / C;
+                                    const int64_t off = __shfl_sync(0xffffffffu, place[x], r);
+                                    const bool on = off >= 0 && 8 * c < a.dim;
+                                    if (c < pieces)
+                                        cp_async16(dst + at16<DP>(32 * x + r, c),
+                                                   on ? src + (off + 8 * c) * 2 : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+                                }
+                            }
+                        cp_async_commit();
+                        ++i;
+                        if (i - published > L::kLag) {
+                            cp_async_wait<L::kLag>();
+                            publish();
+                        }
+                    }
+                } else {
+                    // codes: through registers, as exact 16-bit values
+                    constexpr int C8 = DP / 16, per = 32 / C8, groups = 32 / per, turns = (groups + kLoaders - 1) / kLoaders;
+                    const int c = lane % C8;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const uint8_t* src = v ? a.v : a.k;
+                        uint4 w[4][turns];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < turns; ++y) {
+                                const int grp = lw + kLoaders * y;
+                                w[x][y] = make_uint4(0u, 0u, 0u, 0u);
+                                if (grp < groups) {
+                                    const int64_t off = __shfl_sync(0xffffffffu, place[x], grp * per + lane / C8);
+                                    if (off >= 0 && 16 * c < a.dim) w[x][y] = *reinterpret_cast<const uint4*>(src + off + 16 * c);
+                                }
+                            }
+                        const int slot = static_cast<int>(i % NS);
+                        if (i >= NS && !(ok = mbar_wait(kv_free(slot), ((i / NS) & 1) ^ 1))) break;
+                        uint8_t* dst = smem + L::kQ + slot * L::kTile;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < turns; ++y) {
+                                const int grp = lw + kLoaders * y;
+                                if (grp < groups && 2 * c < pieces) {
+                                    const int r = 32 * x + grp * per + lane / C8;
+                                    const uint32_t ws[4] = {w[x][y].x, w[x][y].y, w[x][y].z, w[x][y].w};
+                                    uint32_t o[8];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t lo = prmt(ws[e], 0u, 0x4140), hi = prmt(ws[e], 0u, 0x4342);
+                                        o[2 * e] = v ? codes16<false>(lo) : codes16<BF16>(lo);
+                                        o[2 * e + 1] = v ? codes16<false>(hi) : codes16<BF16>(hi);
+                                    }
+                                    *reinterpret_cast<uint4*>(dst + at16<DP>(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+                                    *reinterpret_cast<uint4*>(dst + at16<DP>(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                                }
+                            }
+                        if (v == 1 && lw == 0) {
+                            // the values two units back have been used, so their scales have been read
+                            float* sc = reinterpret_cast<float*>(smem + L::kScale) + ((i >> 1) & 1) * 384;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float ks = place[x] >= 0 ? __ldg(a.ks + splace[x]) : 0.f, vs = place[x] >= 0 ? __ldg(a.vs + splace[x]) : 0.f;
+                                sc[32 * x + lane] = ks * a.scale2;
+                                sc[128 + 32 * x + lane] = vs;
+                                sc[256 + 32 * x + lane] = scale_log2(vs);
+                            }
+                        }
+                        if (j == 0 && v == 0) {  // Q
+                            cp_async_commit();
+                            cp_async_wait<0>();
+                        }
+                        ++i;
+                        publish();
+                    }
+                }
+                if (!ok) break;
+                now.step(a);
+                if (now.left > 0) look(now);
+            }
+        }
+        drain();
+        if (!ok) give_up();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int DP, bool BF16, bool I8>
+cudaError_t run_tiles(const Args& a, int runs, cudaStream_t st) {
+    auto kern = attend_tiles_kernel<DP, BF16, I8>;
+    constexpr int smem = Lay<DP, I8>::kSmem;
+    static_assert(smem <= 227 * 1024 && 16 * Lay<DP, I8>::kSlots + 108 <= 256, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(runs), kThreads, smem, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st) {
+    if (dp == 64) {
+        if (i8) return bf16 ? run_tiles<64, true, true>(a, runs, st) : run_tiles<64, false, true>(a, runs, st);
+        return bf16 ? run_tiles<64, true, false>(a, runs, st) : run_tiles<64, false, false>(a, runs, st);
+    }
+    if (i8) return bf16 ? run_tiles<128, true, true>(a, runs, st) : run_tiles<128, false, true>(a, runs, st);
+    return bf16 ? run_tiles<128, true, false>(a, runs, st) : run_tiles<128, false, false>(a, runs, st);
+}
+
+}  // namespace attend
+
+uint32_t attend_read_clear_error() {
+    uint32_t v = 0, z = 0;
+    cudaMemcpyFromSymbol(&v, attend::g_err_attend, sizeof(v));
+    cudaMemcpyToSymbol(attend::g_err_attend, &z, sizeof(z));
+    return v;
+}
+
+}  // namespace qm

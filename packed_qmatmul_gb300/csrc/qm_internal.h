@@ -149,7 +149,7 @@ qm_status apply_experts_checked(const qm_weight* w, const void* ids, int32_t id_
                                 void* workspace, size_t workspace_bytes, qm_stream_t stream,
                                 bool allow_tensor);
 
-// Head norms, rotation and the paged cache (qm_heads.cu, qm_attend.cu); the
+// Head norms, rotation and the paged cache (qm_heads.cu, qm_attend.cu, qm_attend_tc.cu); the
 // arguments are validated (qm_cache.cu).
 cudaError_t launch_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void* const* weights, int count,
                                   int64_t tokens, int dim, float eps, const qm_rope* rope, const void* positions,
@@ -168,5 +168,6 @@ uint32_t elementwise_read_clear_error();
 uint32_t gemv_read_clear_error();
 uint32_t gemm_read_clear_error();
 uint32_t experts_read_clear_error();
+uint32_t attend_read_clear_error();
 
 }  // namespace qm
