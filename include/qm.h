@@ -289,7 +289,7 @@ typedef struct qm_rope {
  * code * scale, with one float32 scale per token row and head in k_scales and
  * v_scales (NULL for the other types) at [p*scale_page_stride +
  * h*scale_head_stride + r*scale_token_stride]. dim: a head's elements, a
- * multiple of 8 (16 for QM_I8), at most 128. */
+ * multiple of 8 (16 for QM_I8), at most 128. k and v span less than 64 GB each. */
 typedef struct qm_cache {
     void* k;
     void* v;

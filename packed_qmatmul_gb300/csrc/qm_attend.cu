@@ -98,31 +98,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     }
 
     // ---- copies: the place of key row (lane & 15) of the step `ahead` is at
-    int64_t place = -1, splace = 0;
+    Lookup found = {0, -1};
+    int head = 0;
     auto look = [&]() {
-        if (ahead.left > 0)
-            place = key_offset(a, ahead.s, ahead.h, ahead.u * kUnit + warp * 16 + (lane & 15), ahead.span.lo, ahead.span.hi, splace);
-        else
-            place = -1;
+        if (ahead.left > 0) {
+            head = ahead.h;
+            found = begin_lookup(a, ahead.s, ahead.u * kUnit + warp * 16 + (lane & 15), ahead.span.lo, ahead.span.hi);
+        }
     };
     auto issue = [&](int slot) {
         const uint32_t base = ring + slot * L::kStage;
+        int64_t splace;
+        const uint32_t place = finish_lookup<I8>(a, found, head, splace);
         constexpr int per = 32 / L::kChunks;  // rows that the warp copies at once
         const int c = lane % L::kChunks;
         const int step = I8 ? 16 : 8;  // elements of a piece
 #pragma unroll
         for (int i = 0; i < 16 / per; ++i) {
             const int r = i * per + lane / L::kChunks;
-            const int64_t off = __shfl_sync(0xffffffffu, place, r);
-            const bool on = off >= 0 && c * step < a.dim;
-            const int64_t at = (off + c * step) * (I8 ? 1 : 2);
+            const uint32_t off = __shfl_sync(0xffffffffu, place, r);
+            const bool on = off != kNoRow && c * step < a.dim;
+            const uint64_t at = (static_cast<uint64_t>(off) + c) * 16;
             cp_async16(base + L::k_at(r, c), on ? a.k + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
             cp_async16(base + L::kPart + L::v_at(r, c), on ? a.v + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
         }
         if constexpr (I8) {
             const float* s = lane < 16 ? a.ks : a.vs;
-            cp_async4(base + 2 * L::kPart + 4 * lane, place >= 0 ? s + splace : reinterpret_cast<const float*>(a.q),
-                      place >= 0 ? 4u : 0u);
+            cp_async4(base + 2 * L::kPart + 4 * lane, place != kNoRow ? s + splace : reinterpret_cast<const float*>(a.q),
+                      place != kNoRow ? 4u : 0u);
         }
     };
     look();
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 kmax[x] = -1;
                 const uint16_t* qrow = nullptr;
                 if (r < now.span.rows) {
-                    const unsigned R = now.tile * kRows + r, i = R / a.group, gg = R - i * a.group;
+                    const unsigned R = now.tile * kRows + r, i = token_of(a, R), gg = R - i * a.group;
                     pos[x] = now.seq.len - now.seq.fresh + static_cast<int>(i);
                     kmin[x] = first_seen(a, pos[x]);
                     kmax[x] = min(pos[x], a.cap - 1);
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         const unsigned R = now.tile * kRows + row;
                         int64_t lse_at;
                         uint16_t* y = out_row(a, now.seq.first, now.h, R, lse_at);
-                        const int at = now.seq.len - now.seq.fresh + static_cast<int>(R / a.group);
+                        const int at = now.seq.len - now.seq.fresh + static_cast<int>(token_of(a, R));
                         const float inv = inverse_total(a, at, total);
                         if (4 * c4 < a.dim)
                             *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
             }
             int64_t lse_at;
             uint16_t* y = out_row(a, first, h, static_cast<unsigned>(r0) + row, lse_at);
-            const int at = base + static_cast<int>((static_cast<unsigned>(r0) + row) / a.group);
+            const int at = base + static_cast<int>(token_of(a, static_cast<unsigned>(r0) + row));
             const float inv = inverse_total(a, at, tt);
             if (4 * c4 < a.dim)
                 *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
@@ -548,6 +551,18 @@ Ws workspace_layout(int runs, int rows, int dp) {
     return w;
 }
 
+// With 2^(l-1) < d <= 2^l and mul = ceil(2^(31+l) / d), n * mul exceeds n 2^(31+l) / d
+// by less than 2^(31+l) / d for every n < 2^31: the quotient is exact.
+void set_quotient(int d, uint32_t* mul, int* shift) {
+    *mul = 0;
+    *shift = 0;
+    if (d <= 1) return;
+    int l = 1;
+    while ((int64_t(1) << l) < d) ++l;
+    *mul = static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d);
+    *shift = l - 1;
+}
+
 // Whether the rows that share a key head (the most of any sequence, if the caller
 // said; else the average) are few.
 bool few_rows(const qm_batch& b, int group) {
@@ -583,9 +598,10 @@ cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_h
     a.v = static_cast<const uint8_t*>(c.v);
     a.ks = c.k_scales;
     a.vs = c.v_scales;
-    a.page_stride = c.page_stride;
-    a.head_stride = c.head_stride;
-    a.token_stride = c.token_stride;
+    const int step = c.dtype == QM_I8 ? 16 : 8;
+    a.page_stride = static_cast<uint32_t>(c.page_stride / step);
+    a.head_stride = static_cast<uint32_t>(c.head_stride / step);
+    a.token_stride = static_cast<uint32_t>(c.token_stride / step);
     a.sps = c.scale_page_stride;
     a.shs = c.scale_head_stride;
     a.sts = c.scale_token_stride;
@@ -604,13 +620,15 @@ cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_h
     a.dim = c.dim;
     a.page_size = c.page_size;
     a.pages = static_cast<int>(c.pages);
+    set_quotient(c.page_size, &a.page_mul, &a.page_shift);
+    set_quotient(a.group, &a.group_mul, &a.group_shift);
     a.window = static_cast<int>(std::min<int64_t>(window, INT_MAX));
     a.scale2 = scale * 1.4426950408889634f;
     a.desc = reinterpret_cast<int*>(wb);
     a.ml = reinterpret_cast<float2*>(wb + ws.ml);
     a.part = reinterpret_cast<float*>(wb + ws.part);
     const bool bf16 = q.dtype == QM_BF16, i8 = c.dtype == QM_I8;
-    const cudaError_t e = few ? launch_rows(a, runs, dp, bf16, i8, st) : launch_tiles(a, runs, dp, bf16, i8, st);
+    const cudaError_t e = few ? launch_rows(a, runs, dp, bf16, i8, st) : launch_tiles(a, c, runs, bf16, st);
     if (e != cudaSuccess) return e;
     return few ? launch_join<kRows>(a, runs, dp, bf16, st) : launch_join<kTileRows>(a, runs, dp, bf16, st);
 }

@@ -36,7 +36,7 @@ struct Args {
     int64_t q_ts, q_hs, o_ts, o_hs;
     const uint8_t *k, *v;
     const float *ks, *vs;
-    int64_t page_stride, head_stride, token_stride;  // elements
+    uint32_t page_stride, head_stride, token_stride;  // in 16-byte pieces
     int64_t sps, shs, sts;
     const int32_t *lens, *table, *q_off;
     int64_t table_stride;
@@ -44,6 +44,10 @@ struct Args {
     int seqs, tokens, each;
     int heads, group, kv_heads, dim;
     int page_size, pages;
+    // quotients of numbers below 2^31: n / page_size = (n * page_mul) >> (32 + page_shift),
+    // and by `group` likewise; a factor of 0 for a divisor of 1
+    uint32_t page_mul, group_mul;
+    int page_shift, group_shift;
     int window;  // 0: none
     float scale2;  // scale * log2(e): scores are kept in powers of two
     // workspace
@@ -56,6 +60,10 @@ struct Args {
 // item's last; [1] 1 if its last part begins an item that it does not finish
 // (slot 1), whose [2] first token, [3] key head, [4] first row, [5] rows and
 // [6] first row's position, [7] new tokens follow.
+
+QM_DEV uint32_t quotient(uint32_t n, uint32_t mul, int shift) { return mul ? __umulhi(n, mul) >> shift : n; }
+// The token (of its sequence's new ones) that a row belongs to.
+QM_DEV uint32_t token_of(const Args& a, uint32_t row) { return quotient(row, a.group_mul, a.group_shift); }
 
 QM_DEV int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
@@ -94,8 +102,8 @@ QM_DEV Span tile_span(const Args& a, const Seq& s, unsigned tile) {
     Span t;
     t.rows = static_cast<int>(min(static_cast<unsigned>(R), all - r0));
     const int base = s.len - s.fresh;
-    t.p0 = base + static_cast<int>(r0 / a.group);
-    t.p1 = base + static_cast<int>((r0 + t.rows - 1) / a.group);
+    t.p0 = base + static_cast<int>(token_of(a, r0));
+    t.p1 = base + static_cast<int>(token_of(a, r0 + t.rows - 1));
     t.hi = min(a.cap, t.p1 + 1);
     t.lo = first_seen(a, t.p0);
     return t;
@@ -106,14 +114,40 @@ QM_DEV unsigned tiles_of(const Args& a, const Seq& s) {
     return (static_cast<unsigned>(s.fresh) * a.group + R - 1) / R;
 }
 
-// Units of one key head of a sequence.
+// Units of tile `t` of a sequence; 0 past its last.
 template <int R>
-QM_DEV int64_t head_units(const Args& a, const Seq& s) {
+QM_DEV int tile_units(const Args& a, const Seq& s, unsigned t, unsigned tiles) {
+    if (t >= tiles) return 0;
+    const Span p = tile_span<R>(a, s, t);
+    return p.u1() - p.u0();
+}
+
+QM_DEV Seq shfl_seq(const Seq& s, int src) {
+    Seq o;
+    o.first = __shfl_sync(0xffffffffu, s.first, src);
+    o.fresh = __shfl_sync(0xffffffffu, s.fresh, src);
+    o.len = __shfl_sync(0xffffffffu, s.len, src);
+    return o;
+}
+
+// Units of one key head of each lane's sequence (0 for a lane without one). The
+// warp goes through the tiles of a sequence of many together.
+template <int R>
+QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine) {
+    const int lane = threadIdx.x & 31;
+    const unsigned tiles = mine ? tiles_of<R>(a, s) : 0;
     int64_t n = 0;
-    const unsigned tiles = tiles_of<R>(a, s);
-    for (unsigned t = 0; t < tiles; ++t) {
-        const Span p = tile_span<R>(a, s, t);
-        n += p.u1() - p.u0();
+    if (tiles <= 2)
+        for (unsigned t = 0; t < tiles; ++t) n += tile_units<R>(a, s, t, tiles);
+    for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+        const int src = __ffs(many) - 1;
+        const Seq q = shfl_seq(s, src);
+        const unsigned all = __shfl_sync(0xffffffffu, tiles, src);
+        int64_t sum = 0;
+        for (unsigned t = lane; t < all; t += 32) sum += tile_units<R>(a, q, t, all);
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (lane == src) n = sum;
     }
     return n;
 }
@@ -160,9 +194,13 @@ template <int R>
 QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
     const int lane = threadIdx.x & 31;
     Cursor<R> k = {};
-    int64_t total = 0;
+    int64_t total = 0, units = 0;
+    Seq seq = {};
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
-        int64_t n = s0 + lane < a.seqs ? head_units<R>(a, load_seq(a, s0 + lane)) : 0;
+        const bool mine = s0 + lane < a.seqs;
+        if (mine) seq = load_seq(a, s0 + lane);
+        units = head_units<R>(a, seq, mine);
+        int64_t n = units;
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
         total += n;
@@ -174,7 +212,12 @@ QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
     k.left = to - from;
     int64_t at = 0;  // units before sequence s0
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
-        const int64_t n = s0 + lane < a.seqs ? head_units<R>(a, load_seq(a, s0 + lane)) * a.kv_heads : 0;
+        if (a.seqs > 32) {
+            const bool mine = s0 + lane < a.seqs;
+            if (mine) seq = load_seq(a, s0 + lane);
+            units = head_units<R>(a, seq, mine);
+        }
+        const int64_t n = units * a.kv_heads;
         int64_t upto = n;  // units up to and with this lane's sequence
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -185,20 +228,31 @@ QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
         if (past) {
             const int src = __ffs(past) - 1;
             const int64_t before = at + __shfl_sync(0xffffffffu, upto - n, src);
-            const int64_t each = __shfl_sync(0xffffffffu, n, src) / a.kv_heads;
+            const int64_t each = __shfl_sync(0xffffffffu, units, src);
             k.s = s0 + src;
-            k.seq = load_seq(a, k.s);
+            k.seq = shfl_seq(seq, src);
             k.tiles = tiles_of<R>(a, k.seq);
             int64_t rem = from - before;
             k.h = static_cast<int>(rem / each);
             rem -= k.h * each;
-            for (k.tile = 0;; ++k.tile) {
-                k.enter(a);
-                if (rem < k.u1 - k.u) break;
-                rem -= k.u1 - k.u;
+            for (unsigned t0 = 0;; t0 += 32) {  // the tile that unit `rem` of the head is in
+                int sum = tile_units<R>(a, k.seq, t0 + lane, k.tiles);
+                const int own = sum;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, sum, m);
+                    if (lane >= m) sum += o;
+                }
+                const unsigned beyond = __ballot_sync(0xffffffffu, sum > rem);
+                if (beyond) {
+                    const int hit = __ffs(beyond) - 1;
+                    k.tile = t0 + hit;
+                    k.enter(a);
+                    k.u += static_cast<int>(rem) - __shfl_sync(0xffffffffu, sum - own, hit);
+                    return k;
+                }
+                rem -= __shfl_sync(0xffffffffu, sum, 31);
             }
-            k.u += static_cast<int>(rem);
-            return k;
         }
         at += __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -206,24 +260,42 @@ QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
     return k;
 }
 
-// Element offset of key `key`'s row of head h, or -1 where it is not to be read.
-QM_DEV int64_t key_offset(const Args& a, int s, int h, int key, int lo, int hi, int64_t& scale_off) {
-    scale_off = 0;
-    if (key < lo || key >= hi) return -1;
-    const int p = key / a.page_size;
-    const int id = __ldg(a.table + s * a.table_stride + p);
-    if (id < 0 || id >= a.pages) return -1;
-    const int row = key - p * a.page_size;
-    scale_off = id * a.sps + h * a.shs + row * a.sts;
-    return id * a.page_stride + h * a.head_stride + row * a.token_stride;
+// Where key `key`'s row of head h lies: its offset in 16-byte pieces (a part of the
+// cache spans less than 2^32 - 1 of them, 64 GB), or kNoRow where it is not to be
+// read; and its scale's offset.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+// A lookup is begun and finished apart, so that what lies between hides the page
+// table's latency (and no branch keeps several of them from overlapping).
+struct Lookup {
+    int id, row;  // page id as the table has it, row in the page; row -1: not to be read
+};
+QM_DEV Lookup begin_lookup(const Args& a, int s, int key, int lo, int hi) {
+    Lookup l = {0, -1};
+    if (lo >= hi) return l;  // the same for the whole warp
+    const int k = clampi(key, lo, hi - 1);
+    const int p = static_cast<int>(quotient(k, a.page_mul, a.page_shift));
+    l.id = __ldg(a.table + s * a.table_stride + p);
+    l.row = k == key ? k - p * a.page_size : -1;
+    return l;
+}
+template <bool I8>
+QM_DEV uint32_t finish_lookup(const Args& a, const Lookup& l, int h, int64_t& scale_off) {
+    const bool there = l.row >= 0 && static_cast<unsigned>(l.id) < static_cast<unsigned>(a.pages);
+    if constexpr (I8) scale_off = l.id * a.sps + h * a.shs + l.row * a.sts;
+    const uint32_t at = l.id * a.page_stride + h * a.head_stride + l.row * a.token_stride;
+    return there ? at : kNoRow;
 }
 
 QM_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+QM_DEV void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 QM_DEV void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+QM_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 QM_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 QM_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -289,7 +361,7 @@ QM_DEV bool nonfinite2(uint32_t v) {
 
 // Where row r of an item goes: its token and query head.
 QM_DEV uint16_t* out_row(const Args& a, int first, int h, unsigned r, int64_t& lse_at) {
-    const unsigned i = r / a.group, g = r - i * a.group;
+    const unsigned i = token_of(a, r), g = r - i * a.group;
     const int head = h * a.group + static_cast<int>(g);
     const int64_t t = first + static_cast<int64_t>(i);
     lse_at = t * a.heads + head;
@@ -308,7 +380,7 @@ QM_DEV float log_total(float top, float total) {
 }
 
 // attend_tiles_kernel (qm_attend_tc.cu).
-cudaError_t launch_tiles(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st);
+cudaError_t launch_tiles(const Args& a, const qm_cache& c, int runs, bool bf16, cudaStream_t st);
 
 }  // namespace attend
 }  // namespace qm

@@ -17,13 +17,17 @@
 //  * warp 8: issues the products: Q and K from shared memory (128-byte swizzle, K
 //    major), P from tensor memory, V from shared memory as it lies in the cache
 //    (rows of keys: MN major); S and O of both tiles fill the 512 tensor-memory columns.
-//  * warps 9..11: fill a ring of 32 KB slots (a unit's keys, then its values) by
-//    16-byte asynchronous copies, each row's place looked up in the page table; they
-//    take any page size, stride and length, fill what is not there with zeros, and
-//    publish a slot to the tensor cores with a proxy fence. 8-bit codes pass through
-//    their registers on the way and enter the products exactly.
+//  * warps 9..11: fill a ring of 32 KB slots (a unit's keys, then its values), each
+//    row's place looked up in the page table, a unit ahead. Where pages are multiples of 32
+//    tokens that is one TMA box for each page and 64 elements, by lanes of warp 9; the
+//    units with a length's ragged end, and other page sizes, are 16-byte asynchronous
+//    copies of all three warps, zeros where there is nothing. Copies arrive on the
+//    slot's barrier as they land, so the loaders only issue; the issuer of the products
+//    orders them before its reads with a proxy fence. 8-bit codes pass through the
+//    loaders' registers on the way and enter the products exactly.
 // Every wait is bounded; a wait that gives up raises the device flag and the CTA
 // winds down with its copies and products drained.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -48,7 +52,6 @@ struct Lay {
     static constexpr int kTile = kPanel * (DP / 64);   // 128 rows of a head
     static constexpr int kQ = 2 * kTile;
     static constexpr int kSlots = I8 ? 4 : DP == 128 ? 5 : 8;
-    static constexpr int kLag = 2;                     // 16-bit slots in flight that are not yet published
     static constexpr int kScale = kQ + kSlots * kTile;  // [2][3][128] floats: key scales, value scales, their logarithms
     static constexpr int kBars = kScale + (I8 ? 2 * 3 * 512 : 0);
     static constexpr int kSmem = kBars + 256;
@@ -78,6 +81,10 @@ QM_DEV uint64_t desc_rows_of_k(uint32_t addr, uint32_t panel) {
 QM_DEV uint32_t idesc16(bool bf16, int N, bool mn) {
     const uint32_t f = bf16 ? 1u : 0u;
     return (1u << 4) | (f << 7) | (f << 10) | ((mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+
+QM_DEV void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
 QM_DEV float max3(float a, float b, float c) {
@@ -151,8 +158,15 @@ __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, ui
     }
 }
 
+struct TileArgs {
+    CUtensorMap tk, tv;  // keys and values [pages][heads][page_size][dim], boxes of 64 elements x box_rows tokens
+    Args a;
+    int box_rows;  // 0: no tensor maps
+};
+
 template <int DP, bool BF16, bool I8>
-__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_constant__ TileArgs ta) {
+    const Args& a = ta.a;
     using L = Lay<DP, I8>;
     constexpr int NS = L::kSlots;
     constexpr bool PBF = BF16 && !I8;  // type of the weights and values in their product
@@ -167,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     auto p_full = [&](int t) { return q_free + 32 + 8 * t; };
     auto o_full = [&](int t) { return q_free + 48 + 8 * t; };
     auto agreed = [&](int t) { return q_free + 64 + 8 * t; };
-    uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * (2 * NS) + 80);
+    const uint32_t q_full = q_free + 80;
+    uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * (2 * NS) + 88);
     uint32_t* tmem_slot = words;
     volatile uint32_t* skip = words + 1;  // [2]: the tile's values were added without the tensor cores
     uint32_t* odd_word = words + 3;       // [2][2]: a warp of the tile saw a value that is infinite or NaN
@@ -181,10 +196,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(kv_full(i), kLoaders);
+            mbar_init(kv_full(i), 32 * kLoaders);
             mbar_init(kv_free(i), 1);
         }
         mbar_init(q_free, 1);
+        mbar_init(q_full, 32 * kLoaders);
         mbar_init(done, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
@@ -228,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             const int rows = now.span.rows;
             const unsigned R = now.tile * kRows + 128 * t + row;
             const bool mine = 128 * t + row < rows;
-            const int pos = now.seq.len - now.seq.fresh + static_cast<int>(R / a.group);
+            const int pos = now.seq.len - now.seq.fresh + static_cast<int>(token_of(a, R));
             const int kmin = mine ? first_seen(a, pos) : 0, kmax = mine ? min(pos, a.cap - 1) : -1;
             float ref = -INFINITY, total = 0.f;
             if (128 * t < rows) {
@@ -415,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         // ------------------------------------------------------------ products
         const uint32_t id_s = idesc16(BF16, 128, false), id_o = idesc16(PBF, 16 * ksteps, true);
         int64_t i = 0;  // slots so far
-        int nth[2] = {0, 0};
+        int nth[2] = {0, 0}, parts = 0;
         bool ok = true;
         auto wait_slot = [&](int64_t k) { return mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1); };
         auto scores = [&](int t, int64_t k) {  // S of tile t over the keys in slot k
@@ -438,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         while (now.left > 0 && ok) {
             const int n = part_units(now);
             const int tiles = now.span.rows > 128 ? 2 : 1;
-            if (!(ok = wait_slot(i))) break;
+            if (!(ok = mbar_wait(q_full, parts & 1) && wait_slot(i))) break;
+            ++parts;
+            fence_proxy_async_smem();
             tc_fence_after();
             for (int t = 0; t < tiles; ++t) scores(t, i);
             commit(kv_free(static_cast<int>(i % NS)));
@@ -448,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     if (!(ok = mbar_wait(p_full(t), nth[t] & 1))) break;
                     ++nth[t];
                     if (t == 0 && !(ok = wait_slot(i + 1))) break;
+                    fence_proxy_async_smem();
                     tc_fence_after();
                     if (!skip[t] && elect_one()) {
                         const uint64_t vd = desc_rows_of_k(ring + static_cast<uint32_t>((i + 1) % NS) * L::kTile, L::kPanel);
@@ -461,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                         commit(o_full(t));
                     } else {
                         if (t == 0 && !(ok = wait_slot(i + 2))) break;
+                        fence_proxy_async_smem();
                         tc_fence_after();
                         scores(t, i + 2);
                     }
@@ -483,106 +503,163 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         constexpr int C = DP / 8;           // 16-byte pieces of a 16-bit row
         const int pieces = 2 * ksteps;      // of which the products read these
         int64_t i = 0;                      // slots so far
-        int64_t published = 0;
         int parts = 0;
         bool ok = true;
-        auto publish = [&]() {  // the next slot in order: its copies have landed
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(kv_full(static_cast<int>(published % NS)));
-            ++published;
+        auto landed = [&](uint32_t bar) {  // arrives when this thread's copies so far have landed
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         };
-        auto drain = [&]() {
-            cp_async_wait<0>();
-            while (published < i) publish();
+        auto take_slot = [&]() {  // waits until slot i is free
+            return i < NS || mbar_wait(kv_free(static_cast<int>(i % NS)), static_cast<uint32_t>((i / NS) & 1) ^ 1u);
         };
-        int64_t place[4], splace[4];  // of rows lane + 32 x of the unit
+        // A warp copies `per` rows at once, the same rows of each quarter of 32 of a
+        // slot; their places, each found by one lane, are passed round once for a
+        // unit's keys and values, and the shared-memory addresses stay the same.
+        constexpr int CB = I8 ? DP / 16 : C;  // 16-byte pieces of a row as it lies in the cache
+        constexpr int per = 32 / CB, turns = (32 / per + kLoaders - 1) / kLoaders;
+        const int pc = lane % CB;
+        uint32_t place[4], off[4][turns];  // of row 32 x + lane; of the rows that the lane copies
+        int64_t splace[4];
+        Lookup found[4];  // rows 32 x + lane of the next unit
+        int head = 0;
+        bool all_there = false;
+        // With tensor maps a unit is some boxes of box_rows tokens of one page each, one a
+        // lane: pages that are not there, and boxes outside the keys to be read, lie at
+        // page `pages`, which reads as zeros. A unit with a box partly outside is copied
+        // row by row.
+        const int box_rows = I8 ? 0 : ta.box_rows, boxes = box_rows ? kUnit / box_rows * (DP / 64) : 0;
+        const int box_i = DP == 128 ? lane >> 1 : lane, box_x = DP == 128 ? (lane & 1) * 64 : 0;
+        const uint32_t box_dst = static_cast<uint32_t>((DP == 128 ? (lane & 1) * L::kPanel : 0) + box_i * box_rows * 128);
+        bool next_boxed = false, boxed = false;
+        Lookup box_at = {0, 0};
+        int box_head = 0;
         auto look = [&](const Cursor<kRows>& c) {
+            head = c.h;
+            const int k0 = c.u * kUnit, k1 = k0 + (kUnit - 1);
+            next_boxed = box_rows && c.span.hi > c.span.lo && (k1 < c.span.hi || c.span.hi % box_rows == 0) &&
+                         (k0 >= c.span.lo || c.span.lo % box_rows == 0);
+            if (next_boxed) {
+                found[0] = begin_lookup(a, c.s, k0 + box_i * box_rows, c.span.lo, c.span.hi);
+                return;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) found[x] = begin_lookup(a, c.s, c.u * kUnit + 32 * x + lane, c.span.lo, c.span.hi);
+        };
+        auto pass_round = [&]() {
+            boxed = next_boxed;
+            if (boxed) {
+                box_at = found[0];
+                if (box_at.row < 0 || static_cast<unsigned>(box_at.id) >= static_cast<unsigned>(a.pages)) box_at = Lookup{a.pages, 0};
+                box_head = head;
+                return;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) place[x] = finish_lookup<I8>(a, found[x], head, splace[x]);
+            all_there = __all_sync(0xffffffffu, place[0] != kNoRow && place[1] != kNoRow && place[2] != kNoRow && place[3] != kNoRow);
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                place[x] = key_offset(a, c.s, c.h, c.u * kUnit + 32 * x + lane, c.span.lo, c.span.hi, splace[x]);
+#pragma unroll
+                for (int y = 0; y < turns; ++y) {
+                    off[x][y] = __shfl_sync(0xffffffffu, place[x], ((lw + kLoaders * y) * per + lane / CB) & 31);
+                    if ((I8 ? 16 : 8) * pc >= a.dim) off[x][y] = kNoRow;
+                }
         };
+        uint32_t dst16[turns];  // where the lane's piece of its row in turn y of a quarter lies in a tile
+#pragma unroll
+        for (int y = 0; y < turns; ++y) dst16[y] = at16<DP>(((lw + kLoaders * y) * per + lane / CB) & 31, I8 ? 2 * pc : pc);
+        const bool full_rows = C * 8 == a.dim;  // every piece of a row holds elements
         auto load_q = [&]() {
-            constexpr int per = 32 / C;
+            constexpr int qper = 32 / C;
             const int c = lane % C;
             const int tiles = now.span.rows > 128 ? 2 : 1;
-            for (int r = lw * per + lane / C; r < 128 * tiles; r += kLoaders * per) {
-                const unsigned R = now.tile * kRows + r, tok = R / a.group, g = R - tok * a.group;
+            for (int r = lw * qper + lane / C; r < 128 * tiles; r += kLoaders * qper) {
+                const unsigned R = now.tile * kRows + r, tok = token_of(a, R), g = R - tok * a.group;
                 const bool on = r < now.span.rows && 8 * c < a.dim;
                 const uint16_t* src = a.q;
                 if (on) src += (now.seq.first + static_cast<int64_t>(tok)) * a.q_ts + (now.h * a.group + static_cast<int>(g)) * a.q_hs + 8 * c;
                 if (c < pieces) cp_async16(sq + (r >> 7) * L::kTile + at16<DP>(r & 127, c), src, on ? 16u : 0u);
             }
+            landed(q_full);
+        };
+        Cursor<kRows> next = now;  // the unit that places are looked up for: one ahead of the copies
+        auto look_on = [&]() {
+            next.step(a);
+            if (next.left > 0) look(next);
         };
         look(now);
         while (now.left > 0 && ok) {
             const int n = part_units(now);
             if (parts > 0) {
-                drain();  // nothing may wait for what is not published
                 if (!(ok = mbar_wait(q_free, (parts - 1) & 1))) break;
             }
             ++parts;
             load_q();
             for (int j = 0; j < n && ok; ++j) {
+                pass_round();
                 if constexpr (!I8) {
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         const int slot = static_cast<int>(i % NS);
-                        if (i >= NS && !(ok = mbar_wait(kv_free(slot), ((i / NS) & 1) ^ 1))) break;
+                        if (!(ok = take_slot())) break;
                         const uint32_t dst = ring + slot * L::kTile;
-                        const uint8_t* src = v ? a.v : a.k;
-                        constexpr int per = 32 / C;
-                        const int c = lane % C;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-#pragma unroll
-                            for (int y = 0; y < (32 / per + kLoaders - 1) / kLoaders; ++y) {
-                                const int grp = lw + kLoaders * y;
-                                if (grp < 32 / per) {
-                                    const int r = grp * per + lane / C;
-                                    const int64_t off = __shfl_sync(0xffffffffu, place[x], r);
-                                    const bool on = off >= 0 && 8 * c < a.dim;
-                                    if (c < pieces)
-                                        cp_async16(dst + at16<DP>(32 * x + r, c),
-                                                   on ? src + (off + 8 * c) * 2 : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+                        const uint8_t* src = (v ? a.v : a.k) + 16 * pc;
+                        if (boxed) {
+                            if (lw == 0) {
+                                if (lane < boxes)
+                                    tma_load_4d(dst + box_dst, v ? &ta.tv : &ta.tk, box_x, box_at.row, box_head, box_at.id, kv_full(slot));
+                                __syncwarp();
+                                if (lane == 0) {
+                                    mbar_expect_tx(kv_full(slot), L::kTile);
+                                    mbar_arrive_n(kv_full(slot), 32 * kLoaders);
                                 }
                             }
-                        cp_async_commit();
-                        ++i;
-                        if (i - published > L::kLag) {
-                            cp_async_wait<L::kLag>();
-                            publish();
+                            ++i;
+                            if (v == 0) look_on();
+                            continue;
                         }
+                        if (all_there && full_rows) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                for (int y = 0; y < turns; ++y)
+                                    if (lw + kLoaders * y < 32 / per)
+                                        cp_async16(dst + dst16[y] + 32 * 128 * x, src + static_cast<uint64_t>(off[x][y]) * 16);
+                        } else if (pc < pieces) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                for (int y = 0; y < turns; ++y)
+                                    if (lw + kLoaders * y < 32 / per) {
+                                        const bool on = off[x][y] != kNoRow;
+                                        cp_async16(dst + dst16[y] + 32 * 128 * x,
+                                                   on ? src + static_cast<uint64_t>(off[x][y]) * 16 : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+                                    }
+                        }
+                        landed(kv_full(slot));
+                        ++i;
+                        if (v == 0) look_on();
                     }
                 } else {
                     // codes: through registers, as exact 16-bit values
-                    constexpr int C8 = DP / 16, per = 32 / C8, groups = 32 / per, turns = (groups + kLoaders - 1) / kLoaders;
-                    const int c = lane % C8;
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
-                        const uint8_t* src = v ? a.v : a.k;
+                        const uint8_t* src = (v ? a.v : a.k) + 16 * pc;
                         uint4 w[4][turns];
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
 #pragma unroll
                             for (int y = 0; y < turns; ++y) {
-                                const int grp = lw + kLoaders * y;
                                 w[x][y] = make_uint4(0u, 0u, 0u, 0u);
-                                if (grp < groups) {
-                                    const int64_t off = __shfl_sync(0xffffffffu, place[x], grp * per + lane / C8);
-                                    if (off >= 0 && 16 * c < a.dim) w[x][y] = *reinterpret_cast<const uint4*>(src + off + 16 * c);
-                                }
+                                if (lw + kLoaders * y < 32 / per && off[x][y] != kNoRow)
+                                    w[x][y] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(off[x][y]) * 16);
                             }
                         const int slot = static_cast<int>(i % NS);
-                        if (i >= NS && !(ok = mbar_wait(kv_free(slot), ((i / NS) & 1) ^ 1))) break;
+                        if (!(ok = take_slot())) break;
                         uint8_t* dst = smem + L::kQ + slot * L::kTile;
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
 #pragma unroll
                             for (int y = 0; y < turns; ++y) {
-                                const int grp = lw + kLoaders * y;
-                                if (grp < groups && 2 * c < pieces) {
-                                    const int r = 32 * x + grp * per + lane / C8;
+                                if (lw + kLoaders * y < 32 / per && 2 * pc < pieces) {
                                     const uint32_t ws[4] = {w[x][y].x, w[x][y].y, w[x][y].z, w[x][y].w};
                                     uint32_t o[8];
 #pragma unroll
@@ -591,8 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                                         o[2 * e] = v ? codes16<false>(lo) : codes16<BF16>(lo);
                                         o[2 * e + 1] = v ? codes16<false>(hi) : codes16<BF16>(hi);
                                     }
-                                    *reinterpret_cast<uint4*>(dst + at16<DP>(r, 2 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
-                                    *reinterpret_cast<uint4*>(dst + at16<DP>(r, 2 * c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                                    // pieces 2 pc and 2 pc + 1 of a swizzled row: the other of a pair of addresses
+                                    *reinterpret_cast<uint4*>(dst + dst16[y] + 32 * 128 * x) = make_uint4(o[0], o[1], o[2], o[3]);
+                                    *reinterpret_cast<uint4*>(dst + (dst16[y] ^ 16u) + 32 * 128 * x) = make_uint4(o[4], o[5], o[6], o[7]);
                                 }
                             }
                         if (v == 1 && lw == 0) {
@@ -600,26 +678,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                             float* sc = reinterpret_cast<float*>(smem + L::kScale) + ((i >> 1) & 1) * 384;
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
-                                const float ks = place[x] >= 0 ? __ldg(a.ks + splace[x]) : 0.f, vs = place[x] >= 0 ? __ldg(a.vs + splace[x]) : 0.f;
+                                const float ks = place[x] != kNoRow ? __ldg(a.ks + splace[x]) : 0.f, vs = place[x] != kNoRow ? __ldg(a.vs + splace[x]) : 0.f;
                                 sc[32 * x + lane] = ks * a.scale2;
                                 sc[128 + 32 * x + lane] = vs;
                                 sc[256 + 32 * x + lane] = scale_log2(vs);
                             }
                         }
-                        if (j == 0 && v == 0) {  // Q
-                            cp_async_commit();
-                            cp_async_wait<0>();
-                        }
+                        mbar_arrive(kv_full(slot));
                         ++i;
-                        publish();
+                        if (v == 1) look_on();
                     }
                 }
                 if (!ok) break;
                 now.step(a);
-                if (now.left > 0) look(now);
             }
         }
-        drain();
+        cp_async_wait_all();
+        if (lw == 0)  // boxes too have landed before the CTA ends, whoever gave up
+            for (int64_t k = i < NS ? 0 : i - NS; k < i; ++k) (void)mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1);
         if (!ok) give_up();
     }
     tc_fence_before();
@@ -631,19 +707,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 }
 
 template <int DP, bool BF16, bool I8>
-cudaError_t run_tiles(const Args& a, int runs, cudaStream_t st) {
+cudaError_t run_tiles(const TileArgs& a, int runs, cudaStream_t st) {
     auto kern = attend_tiles_kernel<DP, BF16, I8>;
     constexpr int smem = Lay<DP, I8>::kSmem;
-    static_assert(smem <= 227 * 1024 && 16 * Lay<DP, I8>::kSlots + 108 <= 256, "shared memory");
+    static_assert(smem <= 227 * 1024 && 16 * Lay<DP, I8>::kSlots + 116 <= 256, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(runs), kThreads, smem, st, a);
 }
 
+// Tensor maps of a 16-bit cache whose pages are multiples of 32 tokens (boxes of 16
+// rows, 2 KB, come slower than the loaders' own copies: 495 against 419 us for
+// a chunk of 4096 over 16384; boxes of 32 and more take 394) and whose heads
+// have at least a box's 64 elements.
+void make_maps(TileArgs& t, const qm_cache& c) {
+    if (c.dtype == QM_I8 || c.page_size % 32 != 0 || c.dim < 64 || c.pages < 1) return;
+    int rows = kUnit;
+    while (c.page_size % rows != 0) rows /= 2;
+    const uint64_t dims[4] = {static_cast<uint64_t>(c.dim), static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads),
+                              static_cast<uint64_t>(c.pages)};
+    // the stride of an axis of one never counts, but has to be one that a map can have
+    const auto stride = [](int64_t n, int64_t s) { return static_cast<uint64_t>(n > 1 ? 2 * s : 256); };
+    const uint64_t strides[3] = {stride(c.page_size, c.token_stride), stride(c.heads, c.head_stride), stride(c.pages, c.page_stride)};
+    if (make_tmap_4d_16(&t.tk, c.k, dims, strides, 64, rows) && make_tmap_4d_16(&t.tv, c.v, dims, strides, 64, rows)) t.box_rows = rows;
+}
+
 }  // namespace
 
-cudaError_t launch_tiles(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st) {
-    if (dp == 64) {
+cudaError_t launch_tiles(const Args& args, const qm_cache& c, int runs, bool bf16, cudaStream_t st) {
+    TileArgs a = {};
+    a.a = args;
+    make_maps(a, c);
+    const bool i8 = c.dtype == QM_I8;
+    if (c.dim <= 64) {
         if (i8) return bf16 ? run_tiles<64, true, true>(a, runs, st) : run_tiles<64, false, true>(a, runs, st);
         return bf16 ? run_tiles<64, true, false>(a, runs, st) : run_tiles<64, false, false>(a, runs, st);
     }

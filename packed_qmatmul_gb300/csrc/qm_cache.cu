@@ -13,6 +13,8 @@ namespace qm {
 
 static const int64_t kMaxI32 = std::numeric_limits<int32_t>::max();
 
+static const int64_t kMaxPieces = int64_t(0xFFFFFFFE) * 16;  // in bytes
+
 static bool float16ish(int32_t dt) { return dt == QM_BF16 || dt == QM_F16; }
 
 static qm_status check_heads(const qm_heads* x, const std::string& name, bool live) {
@@ -76,6 +78,12 @@ static qm_status check_cache(const qm_cache* c) {
         if (!aligned16(c->k)) return fail(QM_EINVAL, "k: base address must be 16-byte aligned");
         if (!aligned16(c->v)) return fail(QM_EINVAL, "v: base address must be 16-byte aligned");
     }
+    // the kernels count a part's 16-byte pieces in 32 bits
+    int64_t pg = 0, hd = 0, tk = 0;
+    if (c->pages > 0 && (!mul_ok(c->pages - 1, c->page_stride, &pg) || !mul_ok(c->heads - 1, c->head_stride, &hd) ||
+                         !mul_ok(c->page_size - 1, c->token_stride, &tk) || pg > kMaxPieces || hd > kMaxPieces || tk > kMaxPieces ||
+                         pg + hd + tk + c->dim > kMaxPieces / (i8 ? 1 : 2)))
+        return fail(QM_ENOTSUP, "cache: k and v may span at most 64 GB each");
     if (i8) {
         if (c->scale_page_stride < 0 || c->scale_head_stride < 0 || c->scale_token_stride < 0)
             return fail(QM_EINVAL, "k_scales: negative stride");
