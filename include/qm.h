@@ -343,8 +343,8 @@ qm_status qm_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void
 qm_status qm_cache_append(const qm_cache* cache, const qm_batch* batch, const qm_heads* k, const qm_heads* v,
                           const void* k_weight, float eps, const qm_rope* rope, qm_stream_t stream);
 
-/* Bytes of device workspace qm_cache_attend needs (a multiple of 256; 0 for
- * invalid arguments or no work). It depends on the shapes alone. */
+/* Bytes of device workspace qm_cache_attend needs (a multiple of 256, 32-byte
+ * aligned; 0 for invalid arguments or no work). It depends on the shapes alone. */
 size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, int32_t q_heads);
 
 /* cache_attend: attention of every new token over its sequence's tokens in the

@@ -221,12 +221,12 @@ bool make_tmap_2d(void* map, const void* base, uint64_t inner_bytes, uint64_t ro
 }
 
 bool make_tmap_4d_16(void* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t box_x,
-                     uint32_t box_y) {
+                     uint32_t box_y, uint32_t box_z) {
     EncodeTiledFn f = encode_tiled();
     if (!f) return false;
     const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
     const cuuint64_t s[3] = {strides[0], strides[1], strides[2]};
-    const cuuint32_t box[4] = {box_x, box_y, 1, 1};
+    const cuuint32_t box[4] = {box_x, box_y, box_z, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = f(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), d, s, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

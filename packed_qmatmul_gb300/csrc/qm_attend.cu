@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
             const uint32_t off = __shfl_sync(0xffffffffu, place, r);
             const bool on = off != kNoRow && c * step < a.dim;
             const uint64_t at = (static_cast<uint64_t>(off) + c) * 16;
-            cp_async16(base + L::k_at(r, c), on ? a.k + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
-            cp_async16(base + L::kPart + L::v_at(r, c), on ? a.v + at : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+            cp_async16(base + L::k_at(r, c), a.k + at, on, a.q);
+            cp_async16(base + L::kPart + L::v_at(r, c), a.v + at, on, a.q);
         }
         if constexpr (I8) {
             const float* s = lane < 16 ? a.ks : a.vs;
@@ -295,12 +295,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 // products are formed one by one.
                 bool odd = false;
                 if (cut && sp.p0 != sp.p1) {
-#pragma unroll 1
-                    for (int i = lane; i < 16 * L::kChunks; i += 32) {
-                        const uint4 w = lds_v4(vb + 16 * i);
-                        odd = odd || nonfinite2<BF16>(w.x) || nonfinite2<BF16>(w.y) || nonfinite2<BF16>(w.z) || nonfinite2<BF16>(w.w);
-                    }
-                    odd = __any_sync(0xffffffffu, odd);
+                    uint32_t high = 0;
+#pragma unroll
+                    for (int i = 0; i < L::kChunks / 2; ++i) high = top_exponents<BF16>(high, lds_v4(vb + 16 * (32 * i + lane)));
+                    odd = __any_sync(0xffffffffu, nonfinite<BF16>(high));
                 }
                 if (!odd) {
                     const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;

@@ -286,11 +286,12 @@ QM_DEV uint32_t finish_lookup(const Args& a, const Lookup& l, int h, int64_t& sc
     return there ? at : kNoRow;
 }
 
-QM_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 QM_DEV void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 zeros instead where not `on` (`any`: an address that is then not read).
+QM_DEV void cp_async16(uint32_t dst, const void* src, bool on, const void* any) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(on ? src : any), "r"(on ? 16u : 0u) : "memory");
 }
 QM_DEV void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -352,11 +353,24 @@ QM_DEV float scale_log2(float s) {
     return fminf(fmaxf(y, -30.f), 30.f);
 }
 
-// A pair of 16-bit values of which one is infinite or NaN.
+// Whether an infinity or NaN is among pairs of 16-bit values: the largest exponents
+// of the low and high halves so far, and the verdict on them.
 template <bool BF16>
-QM_DEV bool nonfinite2(uint32_t v) {
+QM_DEV uint32_t top_exponents(uint32_t top, const uint4& v) {
+    constexpr uint32_t kExp = BF16 ? 0x7F807F80u : 0x7C007C00u;
+    return __vmaxu2(__vmaxu2(__vmaxu2(top, v.x & kExp), __vmaxu2(v.y & kExp, v.z & kExp)), v.w & kExp);
+}
+template <bool BF16>
+QM_DEV bool nonfinite(uint32_t top) {
     constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-    return (v & kExp) == kExp || (v & (kExp << 16)) == (kExp << 16);
+    return (top & 0xFFFFu) == kExp || (top >> 16) == kExp;
+}
+
+// 32 bytes to a 32-byte aligned address in one access.
+QM_DEV void st_global_32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // Where row r of an item goes: its token and query head.

@@ -160,8 +160,10 @@ __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, ui
 
 struct TileArgs {
     CUtensorMap tk, tv;  // keys and values [pages][heads][page_size][dim], boxes of 64 elements x box_rows tokens
+    CUtensorMap tq;      // queries [1][tokens][heads][dim], boxes of 64 elements x group heads x 128 / group tokens
     Args a;
-    int box_rows;  // 0: no tensor maps
+    int box_rows;  // 0: no tensor maps of the cache
+    int q_boxes;   // the queries' map is there
 };
 
 template <int DP, bool BF16, bool I8>
@@ -258,6 +260,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     const int64_t vi = 2 * (index + j) + 1;  // the values' slot
                     const int slot = static_cast<int>(vi % NS);
                     const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
+                    bool odd = false;
+                    if constexpr (!I8) {
+                        // 0 times an infinity or NaN is NaN: where rows see different keys, a look at the
+                        // unit's values (each thread at one key's) tells whether the tensor cores may add them
+                        if (cut && differ) {
+                            if (!mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                            const uint32_t v = ring + slot * L::kTile;
+                            uint32_t high = 0;
+#pragma unroll
+                            for (int c = 0; c < DP / 8; ++c)
+                                if (c < 2 * ksteps) high = top_exponents<BF16>(high, lds_v4(v + at16<DP>(row, c)));
+                            uint32_t* word = odd_word + 2 * (checks & 1) + t;
+                            if (nonfinite<BF16>(high)) atomicOr(word, 1u);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(agreed(t));
+                            if (!mbar_wait(agreed(t), checks & 1)) { ok = false; break; }
+                            odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
+                            if (row == 0) odd_word[2 * (~checks & 1) + t] = 0;  // every warp has read it
+                            ++checks;
+                        }
+                    }
                     if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
                     if (I8 && !mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
                     tc_fence_after();
@@ -277,8 +300,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     }
                     if (cut) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i)
-                            if (i < sa || i > sb) s[i] = -INFINITY;
+                        for (int c = 0; c < 4; ++c) {  // where the warp's rows all see 32 keys, nothing is compared
+                            if (__any_sync(0xffffffffu, sb < 32 * c + 31)) {
+#pragma unroll
+                                for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i <= sb ? s[i] : -INFINITY;
+                            }
+                            if (__any_sync(0xffffffffu, sa > 32 * c)) {
+#pragma unroll
+                                for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i >= sa ? s[i] : -INFINITY;
+                            }
+                        }
                     }
                     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     if constexpr (I8) {
@@ -342,24 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_wait_st();
                     if constexpr (!I8) {
-                        bool odd = false;
-                        if (cut && differ) {
-                            if (!mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
-                            const uint32_t v = ring + slot * L::kTile;
-                            for (int c = 0; c < 2 * ksteps; ++c) {  // each thread looks at one key's values
-                                const uint4 x = lds_v4(v + at16<DP>(row, c));
-                                odd = odd || nonfinite2<BF16>(x.x) || nonfinite2<BF16>(x.y) || nonfinite2<BF16>(x.z) || nonfinite2<BF16>(x.w);
-                            }
-                            uint32_t* word = odd_word + 2 * (checks & 1) + t;
-                            if (odd) atomicOr(word, 1u);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(agreed(t));
-                            if (!mbar_wait(agreed(t), checks & 1)) { ok = false; break; }
-                            odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
-                            if (row == 0) odd_word[2 * (~checks & 1) + t] = 0;  // every warp has read it
-                            ++checks;
-                            if (odd) exact_values<DP, BF16>(ts, to, j == 0, v, sa, sb);
-                        }
+                        if (odd) exact_values<DP, BF16>(ts, to, j == 0, ring + slot * L::kTile, sa, sb);
                         if (row == 0) skip[t] = odd ? 1u : 0u;
                     }
                     tc_fence_before();
@@ -378,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     y = out_row(a, now.seq.first, now.h, R, lse_at);
                     inv = inverse_total(a, pos, total);
                 }
+                // a warp's rows lie apart, so the bytes of an access decide what the stores cost
+                const bool wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
                 float* po = a.part + (static_cast<int64_t>(part) * kRows + 128 * t + row) * DP;
 #pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
@@ -387,17 +403,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     if (!mine || !ok) continue;
                     if (done_here) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[4];
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack16<BF16>(__uint_as_float(r[8 * q + 2 * e]) * inv, __uint_as_float(r[8 * q + 2 * e + 1]) * inv);
-                            if (32 * c + 8 * q < a.dim) *reinterpret_cast<uint4*>(y + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 8; ++e)
+                                w[e] = pack16<BF16>(__uint_as_float(r[16 * q + 2 * e]) * inv, __uint_as_float(r[16 * q + 2 * e + 1]) * inv);
+                            uint16_t* to16 = y + 32 * c + 16 * q;
+                            if (wide && 32 * c + 16 * q + 16 <= a.dim) {
+                                st_global_32(to16, w);
+                            } else {
+                                if (32 * c + 16 * q < a.dim) *reinterpret_cast<uint4*>(to16) = make_uint4(w[0], w[1], w[2], w[3]);
+                                if (32 * c + 16 * q + 8 < a.dim) *reinterpret_cast<uint4*>(to16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
                         }
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<uint4*>(po + 32 * c + 4 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t w[8] = {r[8 * q], r[8 * q + 1], r[8 * q + 2], r[8 * q + 3], r[8 * q + 4], r[8 * q + 5], r[8 * q + 6], r[8 * q + 7]};
+                            st_global_32(po + 32 * c + 8 * q, w);
+                        }
                     }
                 }
                 tc_fence_before();  // the next part's products come after these reads
@@ -568,15 +592,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         for (int y = 0; y < turns; ++y) dst16[y] = at16<DP>(((lw + kLoaders * y) * per + lane / CB) & 31, I8 ? 2 * pc : pc);
         const bool full_rows = C * 8 == a.dim;  // every piece of a row holds elements
         auto load_q = [&]() {
+            if (ta.q_boxes) {  // a tile's rows are a box's: tokens, and within each the group's heads
+                const int tiles = now.span.rows > 128 ? 2 : 1, per_tile = 128 / a.group;
+                if (lw == 0) {
+                    if (lane < tiles * (DP / 64)) {
+                        const int t = DP == 128 ? lane >> 1 : lane, panel = DP == 128 ? lane & 1 : 0;
+                        tma_load_4d(sq + t * L::kTile + panel * L::kPanel, &ta.tq, 64 * panel, now.h * a.group,
+                                    now.seq.first + (2 * static_cast<int>(now.tile) + t) * per_tile, 0, q_full);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_expect_tx(q_full, tiles * L::kTile);
+                }
+                if (lane == 0) mbar_arrive_n(q_full, 32);
+                return;
+            }
             constexpr int qper = 32 / C;
             const int c = lane % C;
             const int tiles = now.span.rows > 128 ? 2 : 1;
+            const int rows = now.span.rows;
+            const uint16_t* base = a.q + now.seq.first * a.q_ts + now.h * a.group * a.q_hs + 8 * c;
+#pragma unroll 8
             for (int r = lw * qper + lane / C; r < 128 * tiles; r += kLoaders * qper) {
                 const unsigned R = now.tile * kRows + r, tok = token_of(a, R), g = R - tok * a.group;
-                const bool on = r < now.span.rows && 8 * c < a.dim;
-                const uint16_t* src = a.q;
-                if (on) src += (now.seq.first + static_cast<int64_t>(tok)) * a.q_ts + (now.h * a.group + static_cast<int>(g)) * a.q_hs + 8 * c;
-                if (c < pieces) cp_async16(sq + (r >> 7) * L::kTile + at16<DP>(r & 127, c), src, on ? 16u : 0u);
+                const bool on = r < rows && 8 * c < a.dim;
+                if (c < pieces)
+                    cp_async16(sq + (r >> 7) * L::kTile + at16<DP>(r & 127, c), base + static_cast<int64_t>(tok) * a.q_ts + static_cast<int64_t>(g) * a.q_hs, on, a.q);
             }
             landed(q_full);
         };
@@ -607,11 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                                 if (lane < boxes)
                                     tma_load_4d(dst + box_dst, v ? &ta.tv : &ta.tk, box_x, box_at.row, box_head, box_at.id, kv_full(slot));
                                 __syncwarp();
-                                if (lane == 0) {
-                                    mbar_expect_tx(kv_full(slot), L::kTile);
-                                    mbar_arrive_n(kv_full(slot), 32 * kLoaders);
-                                }
+                                if (lane == 0) mbar_expect_tx(kv_full(slot), L::kTile);
                             }
+                            // every loader arrives, so that none falls a whole turn of the ring behind
+                            if (lane == 0) mbar_arrive_n(kv_full(slot), 32);
                             ++i;
                             if (v == 0) look_on();
                             continue;
@@ -629,9 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 #pragma unroll
                                 for (int y = 0; y < turns; ++y)
                                     if (lw + kLoaders * y < 32 / per) {
-                                        const bool on = off[x][y] != kNoRow;
-                                        cp_async16(dst + dst16[y] + 32 * 128 * x,
-                                                   on ? src + static_cast<uint64_t>(off[x][y]) * 16 : reinterpret_cast<const uint8_t*>(a.q), on ? 16u : 0u);
+                                        cp_async16(dst + dst16[y] + 32 * 128 * x, src + static_cast<uint64_t>(off[x][y]) * 16,
+                                                   off[x][y] != kNoRow, a.q);
                                     }
                         }
                         landed(kv_full(slot));
@@ -694,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             }
         }
         cp_async_wait_all();
+        if (lw == 0 && parts > 0) (void)mbar_wait(q_full, (parts - 1) & 1);
         if (lw == 0)  // boxes too have landed before the CTA ends, whoever gave up
             for (int64_t k = i < NS ? 0 : i - NS; k < i; ++k) (void)mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1);
         if (!ok) give_up();
@@ -716,11 +755,18 @@ cudaError_t run_tiles(const TileArgs& a, int runs, cudaStream_t st) {
     return launch_pdl(kern, dim3(runs), kThreads, smem, st, a);
 }
 
-// Tensor maps of a 16-bit cache whose pages are multiples of 32 tokens (boxes of 16
+// Tensor maps of the queries where a tile of 128 rows is whole tokens, and
+// of a 16-bit cache whose pages are multiples of 32 tokens (boxes of 16
 // rows, 2 KB, come slower than the loaders' own copies: 495 against 419 us for
 // a chunk of 4096 over 16384; boxes of 32 and more take 394) and whose heads
 // have at least a box's 64 elements.
 void make_maps(TileArgs& t, const qm_cache& c) {
+    const Args& a = t.a;
+    if (a.dim >= 64 && 128 % a.group == 0 && a.q_ts > 0 && a.q_hs > 0) {
+        const uint64_t qd[4] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads), static_cast<uint64_t>(a.tokens), 1};
+        const uint64_t qs[3] = {static_cast<uint64_t>(2 * a.q_hs), static_cast<uint64_t>(2 * a.q_ts), 256};
+        t.q_boxes = make_tmap_4d_16(&t.tq, a.q, qd, qs, 64, a.group, 128 / a.group);
+    }
     if (c.dtype == QM_I8 || c.page_size % 32 != 0 || c.dim < 64 || c.pages < 1) return;
     int rows = kUnit;
     while (c.page_size % rows != 0) rows /= 2;

@@ -222,7 +222,7 @@ qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm
     const size_t need = attend_workspace_bytes(*cache, *batch, q->heads);
     if (!workspace || workspace_bytes < need)
         return fail(QM_EINVAL, "workspace: needs " + std::to_string(need) + " bytes");
-    if (!aligned16(workspace)) return fail(QM_EINVAL, "workspace: must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) & 31u) return fail(QM_EINVAL, "workspace: must be 32-byte aligned");
     return check_launch(launch_cache_attend(*cache, *batch, *q, *out, lse, scale, window, workspace,
                                             reinterpret_cast<cudaStream_t>(stream)),
                         "cache_attend launch");

@@ -56,9 +56,9 @@ bool make_tmap_2d(void* map, const void* base, uint64_t inner_bytes, uint64_t ro
                   int elem_bytes = 1);
 
 // The same over 16-bit elements in four dimensions (extents, strides of the last
-// three in bytes), boxes of box_x x box_y x 1 x 1, 128-byte swizzled.
+// three in bytes), boxes of box_x x box_y x box_z x 1, 128-byte swizzled.
 bool make_tmap_4d_16(void* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3], uint32_t box_x,
-                     uint32_t box_y);
+                     uint32_t box_y, uint32_t box_z = 1);
 
 // Number of SMs on the current device (cached per device).
 int num_sms();

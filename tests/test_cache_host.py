@@ -101,6 +101,7 @@ def test_append_refusals(lib, part, change):
     ("out", dict(out=heads(data=8192, n=4))), ("out", dict(out=heads(data=8192, dt=qm.QM_F16))), ("out", dict(out=heads(data=A))),
     ("out", dict(out=heads(data=8192, ts=32))), ("lse", dict(lse=A + 2)), ("scale", dict(scale=0.0)), ("scale", dict(scale=-1.0)),
     ("scale", dict(scale=math.nan)), ("window", dict(window=-1)), ("workspace", dict(ws=0)), ("workspace", dict(size=64)), ("workspace", dict(ws=A + 8)),
+    ("workspace", dict(ws=A + 16)),
 ])
 def test_attend_refusals(lib, part, change):
     a = dict(q=heads(), out=heads(data=8192), lse=None, scale=1.0, window=0, ws=A, size=1 << 40) | change
