@@ -47,6 +47,7 @@ _STATUS = {QM_EINVAL: "QM_EINVAL", QM_ECUDA: "QM_ECUDA", QM_ETIMEOUT: "QM_ETIMEO
 _FORMATS = {"affine": QM_AFFINE, "q8_0": QM_Q8_0, "mxfp4": QM_MXFP4, "mxfp4_blocks": QM_MXFP4_BLOCKS,
             "q4_k": QM_Q4_K, "q6_k": QM_Q6_K}
 _DTYPES = {torch.float32: QM_F32, torch.bfloat16: QM_BF16, torch.float16: QM_F16}
+_ITYPES = {torch.int32: QM_I32, torch.int64: QM_I64}
 _CACHE_DTYPES = {torch.bfloat16: QM_BF16, torch.float16: QM_F16, torch.int8: QM_I8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -102,7 +103,7 @@ def load_library():
             "qm_apply_experts": ([wp, vp, i32, i64, i64, vp, i64, i32, vp, vp, sz, vp], i32),
             "qm_experts_route": ([vp, i32, i64, i64, vp, vp, vp, vp, sz, vp], i32),
             "qm_apply_experts_static": ([wp, vp, i32, i64, i64, vp, i64, i32, vp, vp], i32),
-            "qm_head_norm_rope": ([vp, vp, ctypes.POINTER(vp), i32, i64, i32, ctypes.c_float, vp, vp, i32, vp], i32),
+            "qm_head_norm_rope": ([vp, vp, vp, i32, i64, i32, ctypes.c_float, vp, vp, i32, vp], i32),
             "qm_cache_append": ([vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i32),
             "qm_cache_attend_workspace": ([vp, vp, i32], sz),
             "qm_cache_attend": ([vp, vp, vp, vp, vp, ctypes.c_float, i64, vp, sz, vp], i32),
@@ -132,8 +133,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (0.3 against 2.9 us of a call's host time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -236,6 +243,7 @@ _HEADS = struct.Struct("Pqqii").pack
 _ROPE = struct.Struct("Pqii").pack
 _CACHE = struct.Struct("4P7q4i").pack
 _BATCH = struct.Struct("3P3q2i").pack
+_POINTERS = [struct.Struct(f"{i}P").pack for i in range(QM_MAX_HEAD_SETS + 1)]
 
 
 def _refuse(message: str):
@@ -250,6 +258,22 @@ def _heads(x: torch.Tensor, tokens: int, heads: int, dim: int, name: str) -> byt
     if es != 1 and dim > 1:
         _refuse(f"{name}: the elements of a head must be contiguous")
     return _HEADS(x.data_ptr(), ts, hs, heads, _DTYPES.get(x.dtype, -1))
+
+
+def _heads_and_like(x: torch.Tensor, tokens: int, dim: int, name: str):
+    """x's descriptor, a new contiguous tensor of its shape and type, and that one's descriptor."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+        _refuse(f"{name}: shape {tuple(shape)}, expected {(tokens, 'heads', dim)}")
+    heads = shape[1]
+    ts, hs, es = x.stride()
+    if es != 1 and dim > 1:
+        _refuse(f"{name}: the elements of a head must be contiguous")
+    dtype = x.dtype
+    code = _DTYPES.get(dtype, -1)
+    row = heads * dim
+    y = torch.empty_like(x) if hs == dim and ts == row else torch.empty(shape, dtype=dtype, device=x.device)
+    return _HEADS(x.data_ptr(), ts, hs, heads, code), y, _HEADS(y.data_ptr(), row, dim, heads, code)
 
 
 def _i32(t: torch.Tensor, name: str) -> int:
@@ -430,31 +454,49 @@ def qm_experts_route(ids: torch.Tensor, E: int, counts: torch.Tensor, offsets: t
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
-def qm_head_norm_rope(xs: Sequence[torch.Tensor], outs: Sequence[torch.Tensor], positions: Optional[torch.Tensor] = None,
-                      rope: Optional[Rope] = None, weights: Optional[Sequence[Optional[torch.Tensor]]] = None,
-                      eps: float = 1e-6, stream=None) -> None:
-    """outs[i] [tokens, heads_i, dim] = the heads of xs[i] normed by weights[i] and rotated by `positions`."""
+def _norm_rope(xs, outs, positions, rope, weights, eps, stream) -> list:
+    """The call; outs None: new tensors. Returns the outputs."""
     n = len(xs)
-    if not 1 <= n <= QM_MAX_HEAD_SETS or len(outs) != n or (weights is not None and len(weights) != n):
+    if not 1 <= n <= QM_MAX_HEAD_SETS or (outs is not None and len(outs) != n) or (weights is not None and len(weights) != n):
         _refuse(f"count: 1 .. {QM_MAX_HEAD_SETS} row sets, as many outputs and weights")
     if xs[0].dim() != 3:
         _refuse("x: must be [tokens, heads, dim]")
     T, _, D = xs[0].shape
-    xd = b"".join([_heads(x, T, x.shape[1], D, "x") for x in xs])
-    od = b"".join([_heads(y, T, x.shape[1], D, "out") for x, y in zip(xs, outs)])
+    xd, od, made = [], [], []
+    if outs is None:
+        for x in xs:
+            c, y, o = _heads_and_like(x, T, D, "x")
+            xd.append(c)
+            od.append(o)
+            made.append(y)
+    else:
+        for x, y in zip(xs, outs):
+            H = x.shape[1]
+            xd.append(_heads(x, T, H, D, "x"))
+            od.append(_heads(y, T, H, D, "out"))
     warr = None
     if weights is not None:
-        for w, x in zip(weights, xs):
-            if w is not None and (w.shape != (D,) or w.dtype != x.dtype):
+        shape, dtype = (D,), xs[0].dtype
+        for w in weights:
+            if w is not None and (w.shape != shape or w.dtype != dtype):
                 _refuse("weights: must be [dim] of x's dtype")
-        warr = _PARR[n](*[_ptr(w) for w in weights])
+        warr = _POINTERS[n](*[0 if w is None else _ptr(w) for w in weights])
     pos, ptype = None, QM_I32
     if positions is not None:
-        if positions.shape != (T,) or positions.dtype not in (torch.int32, torch.int64):
+        ptype = _ITYPES.get(positions.dtype)
+        if ptype is None or positions.shape != (T,):
             _refuse("positions: must be int32 or int64 [tokens]")
-        pos, ptype = _ptr(positions), QM_I64 if positions.dtype == torch.int64 else QM_I32
-    _check(load_library().qm_head_norm_rope(xd, od, warr, n, T, D, eps, None if rope is None else rope._c, pos, ptype,
-                                            _stream(stream)))
+        pos = _ptr(positions)
+    _check(load_library().qm_head_norm_rope(b"".join(xd), b"".join(od), warr, n, T, D, eps, None if rope is None else rope._c,
+                                            pos, ptype, _stream(stream)))
+    return made
+
+
+def qm_head_norm_rope(xs: Sequence[torch.Tensor], outs: Sequence[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                      rope: Optional[Rope] = None, weights: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                      eps: float = 1e-6, stream=None) -> None:
+    """outs[i] [tokens, heads_i, dim] = the heads of xs[i] normed by weights[i] and rotated by `positions`."""
+    _norm_rope(xs, outs, positions, rope, weights, eps, stream)
 
 
 def qm_cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
@@ -568,9 +610,7 @@ def head_norm_rope(xs: Sequence[torch.Tensor], positions: Optional[torch.Tensor]
                    weights: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6, stream=None) -> list:
     """Every head of xs[i] [tokens, heads_i, dim] (queries, keys: any strided rows) normed by weights[i] [dim] and
     rotated by its token's position."""
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-    qm_head_norm_rope(xs, outs, positions, rope, weights, eps, stream)
-    return outs
+    return _norm_rope(xs, None, positions, rope, weights, eps, stream)
 
 
 def cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
@@ -583,10 +623,13 @@ def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[fl
                  lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of the new tokens' queries [tokens, heads, dim] over their sequences in the cache; with lse, (out,
     the scores' log-sum-exp [tokens, heads])."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    total = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if lse else None
+    qd, out, od = _heads_and_like(q, batch.tokens, cache.dim, "q")
+    heads = q.shape[1]
+    total = torch.empty((batch.tokens, heads), dtype=torch.float32, device=q.device) if lse else None
     if workspace is None:
-        need = qm_cache_attend_workspace(cache, batch, q.shape[1])
+        need = qm_cache_attend_workspace(cache, batch, heads)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    qm_cache_attend(cache, batch, q, out, cache.dim ** -0.5 if scale is None else scale, workspace, window, total, stream)
+    _check(load_library().qm_cache_attend(
+        cache._c, batch._c, qd, od, _ptr(total), cache.dim ** -0.5 if scale is None else scale, window, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
     return (out, total) if lse else out

@@ -564,7 +564,8 @@ qm_status qm_device_status(qm_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
     uint32_t flags = elementwise_read_clear_error() | gemv_read_clear_error() |
-                     gemm_read_clear_error() | experts_read_clear_error() | attend_read_clear_error();
+                     gemm_read_clear_error() | experts_read_clear_error() | attend_read_clear_error() |
+                     attend_rows_read_clear_error();
     if (flags) return fail(QM_ETIMEOUT, "device: a device-side wait gave up");
     return QM_OK;
 }

@@ -27,6 +27,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 
 #include "qm_attend.cuh"
 
@@ -72,6 +74,25 @@ QM_DEV void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
 
+__device__ uint32_t g_err_rows = 0;
+
+QM_DEV void store_release(unsigned long long* p, unsigned long long v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+QM_DEV unsigned long long load_acquire(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// An item whose last part this CTA has.
+struct Join {
+    int owner;  // the CTA with its first part; -1: there is no such item
+    int first, h;
+    unsigned row0;
+    int rows, base;
+};
+
 template <int DP, bool BF16, bool I8>
 __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __grid_constant__ Args a) {
     using L = Lay<DP, I8>;
@@ -88,14 +109,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 
     grid_launch_dependents();
     grid_dependency_wait();
-    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x);
+    Cut split = {};
+    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x, split);
     Cursor<kRows> ahead = now;
-    const bool idle = now.left == 0;
-    int first_part = 0;
-    if (idle) {
-        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
-        return;
-    }
+    if (now.left == 0) return;
+    const int64_t run_units = now.left;
+    Join join = {-1, 0, 0, 0, 0, 0};
 
     // ---- copies: the place of key row (lane & 15) of the step `ahead` is at
     Lookup found = {0, -1};
@@ -425,30 +444,65 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 }
                 __syncthreads();
             }
-            if (!done && threadIdx.x == 0) {
-                int* d = a.desc + blockIdx.x * 8;
-                if (whole_start) {
-                    d[1] = 1;
-                    d[2] = now.seq.first;
-                    d[3] = now.h;
-                    d[4] = static_cast<int>(now.tile * kRows);
-                    d[5] = rows;
-                    d[6] = now.seq.len - now.seq.fresh;
+            if (!done) {
+                const int64_t at = split.from + run_units - now.left;  // this unit
+                if (ends) {  // the item's last part: the CTA joins the item when its run is done
+                    const int owner = split.run_of(at - (now.u - now.span.u0()));
+                    join = Join{owner, now.seq.first, now.h, now.tile * kRows, rows, now.seq.len - now.seq.fresh};
+                } else {  // the run's last part, for a later CTA to join
+                    __threadfence();
+                    __syncthreads();
+                    if (threadIdx.x == 0) store_release(a.done + blockIdx.x, a.call);
                 }
-            }
-            if (!whole_start) first_part = ends ? 2 : 1;
-            if (now.left == 1 && threadIdx.x == 0) {
-                a.desc[blockIdx.x * 8] = first_part;
-                if (!(whole_start && !ends)) a.desc[blockIdx.x * 8 + 1] = 0;
             }
             begin = true;
         }
         now.step(a);
     }
     cp_async_wait<0>();
+    if (join.owner < 0) return;
+    // ---- the parts of the item that this CTA's first part ended: all but its own are
+    // the last of the runs before, which end when this one does
+    const int parts = static_cast<int>(blockIdx.x) - join.owner + 1;
+    bool there = true;
+    if (threadIdx.x < parts - 1) {
+        unsigned long long* flag = a.done + join.owner + threadIdx.x;
+        const uint64_t t0 = globaltimer();
+        for (uint64_t round = 0; load_acquire(flag) != a.call; ++round)
+            if (globaltimer() - t0 > kWaitLimitNs || round > kWaitLimitNs) {
+                atomicOr(&g_err_rows, DEV_ERR_TIMEOUT);
+                there = false;
+                break;
+            }
+        *flag = 0;  // so that the next call, or this one's replay, starts over
+    }
+    if (!__syncthreads_and(there)) return;
+    // groups of DP / 4 threads: as many rows at once as there are, the rest of the groups over the parts
+    constexpr int C4 = DP / 4, G = kWarps * 32 / C4;
+    int side = 1;  // rows at once
+    while (side < join.rows && side < G) side *= 2;
+    const int grp = threadIdx.x / C4, c4 = threadIdx.x % C4, per = G / side;
+    for (int r0 = 0; r0 < join.rows; r0 += side) {
+        const int row = r0 + grp / per;
+        Sum4 s = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (row < join.rows) s = sum_parts<kRows, DP>(a, join.owner, parts, row, c4, grp % per, per);
+        float* mine = red + (grp * C4 + c4) * 8;
+        *reinterpret_cast<float4*>(mine) = s.o;
+        *reinterpret_cast<float2*>(mine + 4) = make_float2(s.m, s.total);
+        __syncthreads();
+        if (grp % per == 0 && row < join.rows) {
+            for (int k = 1; k < per; ++k) {
+                const float* other = red + ((grp + k) * C4 + c4) * 8;
+                const float2 e = *reinterpret_cast<const float2*>(other + 4);
+                s.add(e.x, e.y, *reinterpret_cast<const float4*>(other));
+            }
+            write_row4<BF16>(a, join.first, join.h, join.row0 + row, join.base, c4, s);
+        }
+        __syncthreads();
+    }
 }
 
-// Joins the parts of one item: block x of a CTA whose last part begins an item
+// Joins the parts of one item of attend_tiles_kernel: block x of a CTA whose last part begins an item
 // adds that part and the first parts of the CTAs after it, up to the item's last.
 template <int R, int DP, bool BF16>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Args a, int runs) {
@@ -466,43 +520,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int parts = last - c + 1;
     const int grp = threadIdx.x / C4, c4 = threadIdx.x % C4;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        float m = kNegInf, total = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = grp; i < parts; i += G) {
-            const int part = 2 * (c + i) + (i == 0 ? 1 : 0);
-            const float2 e = a.ml[part * R + row];
-            const float4 v = *reinterpret_cast<const float4*>(a.part + (static_cast<int64_t>(part) * R + row) * DP + 4 * c4);
-            const float mn = fmaxf(m, e.x), ref = mn == kNegInf ? 0.f : mn;
-            const float f = ex2(m - ref), fe = ex2(e.x - ref);
-            total = total * f + e.y * fe;
-            o.x = o.x * f + v.x * fe; o.y = o.y * f + v.y * fe;
-            o.z = o.z * f + v.z * fe; o.w = o.w * f + v.w * fe;
-            m = mn;
-        }
-        so[grp][c4] = o;
-        if (c4 == 0) sm[grp] = make_float2(m, total);
+        Sum4 s = sum_parts<R, DP>(a, c, parts, row, c4, grp, G);
+        so[grp][c4] = s.o;
+        if (c4 == 0) sm[grp] = make_float2(s.m, s.total);
         __syncthreads();
         if (grp == 0) {
-            float mm = kNegInf;
-#pragma unroll
-            for (int w = 0; w < G; ++w) mm = fmaxf(mm, sm[w].x);
-            const float ref = mm == kNegInf ? 0.f : mm;
-            float tt = 0.f;
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < G; ++w) {
-                const float f = ex2(sm[w].x - ref);
-                const float4 v = so[w][c4];
-                tt += sm[w].y * f;
-                o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
-            }
-            int64_t lse_at;
-            uint16_t* y = out_row(a, first, h, static_cast<unsigned>(r0) + row, lse_at);
-            const int at = base + static_cast<int>(token_of(a, static_cast<unsigned>(r0) + row));
-            const float inv = inverse_total(a, at, tt);
-            if (4 * c4 < a.dim)
-                *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(o.x * inv, o.y * inv), pack16<BF16>(o.z * inv, o.w * inv));
-            if (a.lse && c4 == 0) a.lse[lse_at] = log_total(mm, tt);
+            for (int w = 1; w < G; ++w) s.add(sm[w].x, sm[w].y, so[w][c4]);
+            write_row4<BF16>(a, first, h, static_cast<unsigned>(r0) + row, base, c4, s);
         }
         __syncthreads();
     }
@@ -527,17 +551,24 @@ cudaError_t launch_rows(const Args& a, int runs, int dp, bool bf16, bool i8, cud
     return bf16 ? run_rows<128, true, false>(a, runs, st) : run_rows<128, false, false>(a, runs, st);
 }
 
-template <int R>
 cudaError_t launch_join(const Args& a, int runs, int dp, bool bf16, cudaStream_t st) {
     const dim3 grid(runs, 16);
     if (dp == 64)
-        return bf16 ? launch_pdl(attend_join_kernel<R, 64, true>, grid, 256, 0, st, a, runs)
-                    : launch_pdl(attend_join_kernel<R, 64, false>, grid, 256, 0, st, a, runs);
-    return bf16 ? launch_pdl(attend_join_kernel<R, 128, true>, grid, 256, 0, st, a, runs)
-                : launch_pdl(attend_join_kernel<R, 128, false>, grid, 256, 0, st, a, runs);
+        return bf16 ? launch_pdl(attend_join_kernel<kTileRows, 64, true>, grid, 256, 0, st, a, runs)
+                    : launch_pdl(attend_join_kernel<kTileRows, 64, false>, grid, 256, 0, st, a, runs);
+    return bf16 ? launch_pdl(attend_join_kernel<kTileRows, 128, true>, grid, 256, 0, st, a, runs)
+                : launch_pdl(attend_join_kernel<kTileRows, 128, false>, grid, 256, 0, st, a, runs);
 }
 
-// Workspace: [runs][8] int, [runs][2][R] float2, [runs][2][R][DP] float.
+// Marks calls apart in the parts' flags: 64 scattered bits, never 0, so that what a
+// workspace happens to hold is not taken for one.
+unsigned long long next_call() {
+    static std::atomic<unsigned long long> next{static_cast<unsigned long long>(
+        std::chrono::system_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ull};
+    return next.fetch_add(0x9E3779B97F4A7C15ull, std::memory_order_relaxed) | 1ull;
+}
+
+// Workspace: [runs][8] int or [runs] flags, [runs][2][R] float2, [runs][2][R][DP] float.
 struct Ws {
     size_t ml, part, all;
 };
@@ -572,6 +603,13 @@ bool few_rows(const qm_batch& b, int group) {
 }  // namespace attend
 
 using namespace attend;
+
+uint32_t attend_rows_read_clear_error() {
+    uint32_t v = 0, z = 0;
+    cudaMemcpyFromSymbol(&v, g_err_rows, sizeof(v));
+    cudaMemcpyToSymbol(g_err_rows, &z, sizeof(z));
+    return v;
+}
 
 size_t attend_workspace_bytes(const qm_cache& c, const qm_batch& b, int q_heads) {
     return workspace_layout(num_sms(), few_rows(b, q_heads / c.heads) ? kRows : kTileRows, c.dim <= 64 ? 64 : 128).all;
@@ -623,12 +661,14 @@ cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_h
     a.window = static_cast<int>(std::min<int64_t>(window, INT_MAX));
     a.scale2 = scale * 1.4426950408889634f;
     a.desc = reinterpret_cast<int*>(wb);
+    a.done = reinterpret_cast<unsigned long long*>(wb);
+    a.call = few ? next_call() : 0;
     a.ml = reinterpret_cast<float2*>(wb + ws.ml);
     a.part = reinterpret_cast<float*>(wb + ws.part);
     const bool bf16 = q.dtype == QM_BF16, i8 = c.dtype == QM_I8;
     const cudaError_t e = few ? launch_rows(a, runs, dp, bf16, i8, st) : launch_tiles(a, c, runs, bf16, st);
     if (e != cudaSuccess) return e;
-    return few ? launch_join<kRows>(a, runs, dp, bf16, st) : launch_join<kTileRows>(a, runs, dp, bf16, st);
+    return few ? cudaSuccess : launch_join(a, runs, dp, bf16, st);
 }
 
 }  // namespace qm

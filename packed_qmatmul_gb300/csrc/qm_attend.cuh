@@ -12,8 +12,12 @@
 // and the host needs to know none of them. Each CTA finds its run from the
 // lengths itself. A CTA that has all of an item writes its rows; one that has a
 // part leaves its unnormalised sums, with their maximum and total, in the
-// workspace, and attend_join_kernel adds an item's parts in order of key. The
-// cut depends on the lengths alone, so the same call gives the same bits.
+// workspace. An item's parts are then added in order of key: in attend_rows_kernel
+// by the CTA with its last part, once its own run is done (it waits for flags of the
+// CTAs before it, whose runs are as long; a second launch costs more), after
+// attend_tiles_kernel, whose parts are up to 128 KB each, by attend_join_kernel. The
+// cut depends on the lengths alone, and so does the order of every sum: the same
+// call gives the same bits.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,7 +55,9 @@ struct Args {
     int window;  // 0: none
     float scale2;  // scale * log2(e): scores are kept in powers of two
     // workspace
-    int* desc;     // [grid][8], see Piece
+    int* desc;     // [grid][8], see below (attend_tiles_kernel)
+    unsigned long long* done;  // [grid] (attend_rows_kernel): `call` once the CTA's part of an item that goes on is there
+    unsigned long long call;   // marks this call
     float2* ml;    // [grid][2][R]: maximum and total of each row
     float* part;   // [grid][2][R][DP]
 };
@@ -188,10 +194,18 @@ struct Cursor {
     }
 };
 
+// How the units are cut.
+struct Cut {
+    int64_t total, from;  // units in all, and before this CTA's run
+    int runs;             // that have units
+    // The run that holds unit g.
+    QM_DEV int run_of(int64_t g) const { return static_cast<int>(((g + 1) * runs - 1) / total); }
+};
+
 // The calling warp's cursor at the start of run `c` of `runs` (left = 0: the run
 // is empty). Every lane returns the same.
 template <int R>
-QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
+QM_DEV Cursor<R> find_run(const Args& a, int c, int runs, Cut& cut) {
     const int lane = threadIdx.x & 31;
     Cursor<R> k = {};
     int64_t total = 0, units = 0;
@@ -210,6 +224,7 @@ QM_DEV Cursor<R> find_run(const Args& a, int c, int runs) {
     if (c >= runs) return k;
     const int64_t from = total * c / runs, to = total * (c + 1) / runs;
     k.left = to - from;
+    cut = Cut{total, from, runs};
     int64_t at = 0;  // units before sequence s0
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
         if (a.seqs > 32) {
@@ -389,8 +404,46 @@ QM_DEV float inverse_total(const Args& a, int pos, float total) {
     return 1.0f / total;
 }
 
+// The sum of an item's parts, four elements to a thread, against a reference m.
+struct Sum4 {
+    float m, total;
+    float4 o;
+    QM_DEV void add(float em, float et, const float4& v) {
+        const float mn = fmaxf(m, em), ref = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - ref), fe = ex2(em - ref);
+        total = total * f + et * fe;
+        o.x = o.x * f + v.x * fe; o.y = o.y * f + v.y * fe;
+        o.z = o.z * f + v.z * fe; o.w = o.w * f + v.w * fe;
+        m = mn;
+    }
+};
+// Parts i0, i0 + di, ... of a row: the item's first part lies at slot 2 c + 1, part i
+// after it at slot 2 (c + i).
+template <int R, int DP>
+QM_DEV Sum4 sum_parts(const Args& a, int c, int parts, int row, int c4, int i0, int di) {
+    Sum4 s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int i = i0; i < parts; i += di) {
+        const int64_t at = static_cast<int64_t>(2 * (c + i) + (i == 0 ? 1 : 0)) * R + row;
+        const float2 e = __ldcg(a.ml + at);
+        s.add(e.x, e.y, __ldcg(reinterpret_cast<const float4*>(a.part + at * DP + 4 * c4)));
+    }
+    return s;
+}
+
 QM_DEV float log_total(float top, float total) {
     return total == 0.f ? __int_as_float(0xff800000) : (top + log2f(total)) * 0.69314718055994531f;
+}
+
+// Writes four elements of row r of an item from its whole sum.
+template <bool BF16>
+QM_DEV void write_row4(const Args& a, int first, int h, unsigned r, int p0, int c4, const Sum4& s) {
+    int64_t lse_at;
+    uint16_t* y = out_row(a, first, h, r, lse_at);
+    const float inv = inverse_total(a, p0 + static_cast<int>(token_of(a, r)), s.total);
+    if (4 * c4 < a.dim)
+        *reinterpret_cast<uint2*>(y + 4 * c4) = make_uint2(pack16<BF16>(s.o.x * inv, s.o.y * inv), pack16<BF16>(s.o.z * inv, s.o.w * inv));
+    if (a.lse && c4 == 0) a.lse[lse_at] = log_total(s.m, s.total);
 }
 
 // attend_tiles_kernel (qm_attend_tc.cu).

@@ -105,6 +105,25 @@ QM_DEV uint32_t at16(int r, int c) {
     return (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// Four lanes with pieces 0..3 of a row each: afterwards lane l of the quad has piece
+// l of the rows of lanes 0..3.
+QM_DEV void quad_transpose(uint32_t (&w)[4][8]) {
+    const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int p = 0; p < 4; p += 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b0 ? w[p][e] : w[p + 1][e], 1);
+            (b0 ? w[p][e] : w[p + 1][e]) = got;
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? w[p][e] : w[p + 2][e], 2);
+            (b1 ? w[p][e] : w[p + 2][e]) = got;
+        }
+    }
+}
+
 // O[row] += P[row] V over the unit's keys that the row sees, product by product:
 // for a unit in which rows see different keys and a value is infinite or NaN (0
 // times it would be NaN in rows that do not see it). p: the row's weights in tensor
@@ -187,11 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     uint32_t* words = reinterpret_cast<uint32_t*>(smem + L::kBars + 8 * (2 * NS) + 88);
     uint32_t* tmem_slot = words;
     volatile uint32_t* skip = words + 1;  // [2]: the tile's values were added without the tensor cores
-    uint32_t* odd_word = words + 3;       // [2][2]: a warp of the tile saw a value that is infinite or NaN
+    uint32_t* odd_word = words + 3;       // [3][2]: a warp of the tile saw a value that is infinite or NaN
 
     grid_launch_dependents();
     grid_dependency_wait();
-    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x);
+    Cut split = {};
+    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x, split);
     if (now.left == 0) {
         if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
         return;
@@ -209,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             mbar_init(p_full(t), 4);
             mbar_init(o_full(t), 1);
             mbar_init(agreed(t), 4);
-            skip[t] = odd_word[t] = odd_word[2 + t] = 0;
+            skip[t] = odd_word[t] = odd_word[2 + t] = odd_word[4 + t] = 0;
         }
         fence_mbar_init();
     }
@@ -260,6 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     const int64_t vi = 2 * (index + j) + 1;  // the values' slot
                     const int slot = static_cast<int>(vi % NS);
                     const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
+                    // (only then is the unit's slot in turn: a tile that sat out an item runs ahead of the copies)
+                    if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
                     bool odd = false;
                     if constexpr (!I8) {
                         // 0 times an infinity or NaN is NaN: where rows see different keys, a look at the
@@ -271,17 +293,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 #pragma unroll
                             for (int c = 0; c < DP / 8; ++c)
                                 if (c < 2 * ksteps) high = top_exponents<BF16>(high, lds_v4(v + at16<DP>(row, c)));
-                            uint32_t* word = odd_word + 2 * (checks & 1) + t;
+                            uint32_t* word = odd_word + 2 * (checks % 3) + t;
+                            // the next check's word, which every warp read two checks ago
+                            if (row == 0) odd_word[2 * ((checks + 1) % 3) + t] = 0;
                             if (nonfinite<BF16>(high)) atomicOr(word, 1u);
                             __syncwarp();
                             if (lane == 0) mbar_arrive(agreed(t));
                             if (!mbar_wait(agreed(t), checks & 1)) { ok = false; break; }
                             odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
-                            if (row == 0) odd_word[2 * (~checks & 1) + t] = 0;  // every warp has read it
                             ++checks;
                         }
                     }
-                    if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
                     if (I8 && !mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
                     tc_fence_after();
                     uint32_t raw[4][32];
@@ -392,36 +414,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     y = out_row(a, now.seq.first, now.h, R, lse_at);
                     inv = inverse_total(a, pos, total);
                 }
-                // a warp's rows lie apart, so the bytes of an access decide what the stores cost
-                const bool wide = (reinterpret_cast<uintptr_t>(y) & 31) == 0;
-                float* po = a.part + (static_cast<int64_t>(part) * kRows + 128 * t + row) * DP;
+                // A warp's rows lie apart in memory: quads of lanes exchange pieces of 32 bytes so
+                // that each store of a quad is 128 bytes of one row (row by row from its own
+                // lane, an item's 64 KB took some 8000 clocks of the SM's memory path).
+                const int l4 = lane & 3;
+                uint16_t* yrow[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    yrow[k] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(y), (lane & ~3) + k));
+                if (done_here) {
 #pragma unroll 1
-                for (int c = 0; c < DP / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32(to + 32 * c, r);
-                    tmem_wait_ld();
-                    if (!mine || !ok) continue;
-                    if (done_here) {
+                    for (int c = 0; c < DP / 64; ++c) {
+                        uint32_t w[4][8];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t w[8];
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t r[32];
+                            tmem_ld32(to + 64 * c + 32 * h, r);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                w[e] = pack16<BF16>(__uint_as_float(r[16 * q + 2 * e]) * inv, __uint_as_float(r[16 * q + 2 * e + 1]) * inv);
-                            uint16_t* to16 = y + 32 * c + 16 * q;
-                            if (wide && 32 * c + 16 * q + 16 <= a.dim) {
-                                st_global_32(to16, w);
+                            for (int e = 0; e < 16; ++e)
+                                w[2 * h + (e >> 3)][e & 7] = pack16<BF16>(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+                        }
+                        quad_transpose(w);
+                        const int col = 64 * c + 16 * l4;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (!yrow[k] || !ok) continue;
+                            uint16_t* to16 = yrow[k] + col;
+                            if (col + 16 <= a.dim && (reinterpret_cast<uintptr_t>(to16) & 31) == 0) {
+                                st_global_32(to16, w[k]);
                             } else {
-                                if (32 * c + 16 * q < a.dim) *reinterpret_cast<uint4*>(to16) = make_uint4(w[0], w[1], w[2], w[3]);
-                                if (32 * c + 16 * q + 8 < a.dim) *reinterpret_cast<uint4*>(to16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                                if (col < a.dim) *reinterpret_cast<uint4*>(to16) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                                if (col + 8 < a.dim) *reinterpret_cast<uint4*>(to16 + 8) = make_uint4(w[k][4], w[k][5], w[k][6], w[k][7]);
                             }
                         }
-                    } else {
+                    }
+                } else {
+                    float* po = a.part + (static_cast<int64_t>(part) * kRows + 128 * t + 32 * (warp & 3) + (lane & ~3)) * DP + 8 * l4;
+                    const int left = rows - (128 * t + 32 * (warp & 3) + (lane & ~3));  // of the quad's rows, those that are
+#pragma unroll 1
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t r[32], w[4][8];
+                        tmem_ld32(to + 32 * c, r);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t w[8] = {r[8 * q], r[8 * q + 1], r[8 * q + 2], r[8 * q + 3], r[8 * q + 4], r[8 * q + 5], r[8 * q + 6], r[8 * q + 7]};
-                            st_global_32(po + 32 * c + 8 * q, w);
-                        }
+                        for (int e = 0; e < 32; ++e) w[e >> 3][e & 7] = r[e];
+                        quad_transpose(w);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left && ok) st_global_32(po + k * DP + 32 * c, w[k]);
                     }
                 }
                 tc_fence_before();  // the next part's products come after these reads
@@ -550,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         // lane: pages that are not there, and boxes outside the keys to be read, lie at
         // page `pages`, which reads as zeros. A unit with a box partly outside is copied
         // row by row.
-        const int box_rows = I8 ? 0 : ta.box_rows, boxes = box_rows ? kUnit / box_rows * (DP / 64) : 0;
+        const int box_rows = ta.box_rows, boxes = box_rows ? kUnit / box_rows * (DP / 64) : 0;
         const int box_i = DP == 128 ? lane >> 1 : lane, box_x = DP == 128 ? (lane & 1) * 64 : 0;
         const uint32_t box_dst = static_cast<uint32_t>((DP == 128 ? (lane & 1) * L::kPanel : 0) + box_i * box_rows * 128);
         bool next_boxed = false, boxed = false;
@@ -749,7 +790,7 @@ template <int DP, bool BF16, bool I8>
 cudaError_t run_tiles(const TileArgs& a, int runs, cudaStream_t st) {
     auto kern = attend_tiles_kernel<DP, BF16, I8>;
     constexpr int smem = Lay<DP, I8>::kSmem;
-    static_assert(smem <= 227 * 1024 && 16 * Lay<DP, I8>::kSlots + 116 <= 256, "shared memory");
+    static_assert(smem <= 227 * 1024 && 16 * Lay<DP, I8>::kSlots + 124 <= 256, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(runs), kThreads, smem, st, a);

@@ -174,5 +174,6 @@ uint32_t gemv_read_clear_error();
 uint32_t gemm_read_clear_error();
 uint32_t experts_read_clear_error();
 uint32_t attend_read_clear_error();
+uint32_t attend_rows_read_clear_error();
 
 }  // namespace qm
