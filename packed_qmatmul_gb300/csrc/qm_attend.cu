@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     grid_launch_dependents();
     grid_dependency_wait();
     Cut split = {};
-    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x, split);
+    Cursor<kRows> now = find_run<kRows, false>(a, blockIdx.x, gridDim.x, split);
     Cursor<kRows> ahead = now;
     if (now.left == 0) return;
     const int64_t run_units = now.left;

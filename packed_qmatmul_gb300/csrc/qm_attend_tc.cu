@@ -54,7 +54,8 @@ struct Lay {
     static constexpr int kSlots = I8 ? 4 : DP == 128 ? 5 : 8;
     static constexpr int kScale = kQ + kSlots * kTile;  // [2][3][128] floats: key scales, value scales, their logarithms
     static constexpr int kBars = kScale + (I8 ? 2 * 3 * 512 : 0);
-    static constexpr int kSmem = kBars + 256;
+    static constexpr int kCursors = kBars + 256;       // of the warps that form weights: they are out of registers
+    static constexpr int kSmem = kCursors + 8 * 96;
 };
 
 QM_DEV bool elect_one() {
@@ -211,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     grid_launch_dependents();
     grid_dependency_wait();
     Cut split = {};
-    Cursor<kRows> now = find_run<kRows>(a, blockIdx.x, gridDim.x, split);
-    if (now.left == 0) {
+    const Cursor<kRows> start = find_run<kRows, true>(a, blockIdx.x, gridDim.x, split);
+    if (start.left == 0) {
         if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
         return;
     }
@@ -257,28 +258,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
         int nth = 0, parts = 0, checks = 0;  // units, parts and value checks of this tile so far
-        int64_t index = 0;       // units of the CTA so far
+        uint32_t index = 0;      // units of the CTA so far
         int first_part = 0;
         bool ok = true;
-        while (now.left > 0 && ok) {
-            const int n = part_units(now);
-            const bool starts = now.first(), ends = now.u + n == now.u1, done_here = starts && ends;
-            const int rows = now.span.rows;
-            const unsigned R = now.tile * kRows + 128 * t + row;
+        static_assert(sizeof(Cursor<kRows>) <= 96, "cursor");
+        Cursor<kRows>* now = reinterpret_cast<Cursor<kRows>*>(smem + L::kCursors + 96 * warp);
+        if (lane == 0) *now = start;
+        __syncwarp();
+        while (now->left > 0 && ok) {
+            const int n = part_units(*now);
+            const bool starts = now->first(), ends = now->u + n == now->u1, done_here = starts && ends;
+            const int rows = now->span.rows;
+            const unsigned R = now->tile * kRows + 128 * t + row;
             const bool mine = 128 * t + row < rows;
-            const int pos = now.seq.len - now.seq.fresh + static_cast<int>(token_of(a, R));
+            const int pos = now->seq.len - now->seq.fresh + static_cast<int>(token_of(a, R));
             const int kmin = mine ? first_seen(a, pos) : 0, kmax = mine ? min(pos, a.cap - 1) : -1;
             float ref = -INFINITY, total = 0.f;
             if (128 * t < rows) {
                 // keys that every row of the item sees lie within [all_lo, all_hi]
-                const int all_hi = min(now.span.p0, a.cap - 1), all_lo = first_seen(a, now.span.p1);
-                const bool differ = now.span.p0 != now.span.p1;
+                const int all_hi = min(now->span.p0, a.cap - 1), all_lo = first_seen(a, now->span.p1);
+                const bool differ = now->span.p0 != now->span.p1;
                 for (int j = 0; j < n; ++j, ++nth) {
-                    const int key0 = (now.u + j) * kUnit;
+                    const int key0 = (now->u + j) * kUnit;
                     const bool cut = key0 + kUnit - 1 > all_hi || key0 < all_lo;
                     const int sa = max(kmin - key0, 0), sb = min(kmax - key0, kUnit - 1);  // the unit's keys that the row sees
-                    const int64_t vi = 2 * (index + j) + 1;  // the values' slot
-                    const int slot = static_cast<int>(vi % NS);
+                    const uint32_t vi = 2 * (index + j) + 1;  // the values' slot
+                    const int slot = vi % NS;
                     const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
                     // (only then is the unit's slot in turn: a tile that sat out an item runs ahead of the copies)
                     if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                 int64_t lse_at = 0;
                 float inv = 1.f;
                 if (mine && done_here) {
-                    y = out_row(a, now.seq.first, now.h, R, lse_at);
+                    y = out_row(a, now->seq.first, now->h, R, lse_at);
                     inv = inverse_total(a, pos, total);
                 }
                 // A warp's rows lie apart in memory: quads of lanes exchange pieces of 32 bytes so
@@ -477,31 +482,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             if (threadIdx.x == 0 && !done_here && starts) {
                 int* d = a.desc + blockIdx.x * 8;
                 d[1] = 1;
-                d[2] = now.seq.first;
-                d[3] = now.h;
-                d[4] = static_cast<int>(now.tile * kRows);
+                d[2] = now->seq.first;
+                d[3] = now->h;
+                d[4] = static_cast<int>(now->tile * kRows);
                 d[5] = rows;
-                d[6] = now.seq.len - now.seq.fresh;
+                d[6] = now->seq.len - now->seq.fresh;
             }
             if (!starts) first_part = ends ? 2 : 1;
-            if (now.left == n && threadIdx.x == 0) {
+            if (now->left == n && threadIdx.x == 0) {
                 a.desc[blockIdx.x * 8] = first_part;
                 if (!(starts && !ends)) a.desc[blockIdx.x * 8 + 1] = 0;
             }
             index += n;
-            skip_part(now, n);
+            Cursor<kRows> then = *now;
+            skip_part(then, n);
+            __syncwarp();
+            if (lane == 0) *now = then;
+            __syncwarp();
         }
         if (!ok) give_up();
     } else if (warp == 8) {
         // ------------------------------------------------------------ products
         const uint32_t id_s = idesc16(BF16, 128, false), id_o = idesc16(PBF, 16 * ksteps, true);
-        int64_t i = 0;  // slots so far
+        uint32_t i = 0;  // slots so far
         int nth[2] = {0, 0}, parts = 0;
         bool ok = true;
-        auto wait_slot = [&](int64_t k) { return mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1); };
-        auto scores = [&](int t, int64_t k) {  // S of tile t over the keys in slot k
+        auto wait_slot = [&](uint32_t k) { return mbar_wait(kv_full(k % NS), (k / NS) & 1); };
+        auto scores = [&](int t, uint32_t k) {  // S of tile t over the keys in slot k
             if (elect_one()) {
-                const uint64_t qd = umma_desc_sw128(sq + t * L::kTile), kd = umma_desc_sw128(ring + static_cast<uint32_t>(k % NS) * L::kTile);
+                const uint64_t qd = umma_desc_sw128(sq + t * L::kTile), kd = umma_desc_sw128(ring + (k % NS) * L::kTile);
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk)
                     if (kk < ksteps) {
@@ -516,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             if (elect_one()) umma_commit(bar);
             __syncwarp();
         };
+        Cursor<kRows> now = start;
         while (now.left > 0 && ok) {
             const int n = part_units(now);
             const int tiles = now.span.rows > 128 ? 2 : 1;
@@ -524,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             fence_proxy_async_smem();
             tc_fence_after();
             for (int t = 0; t < tiles; ++t) scores(t, i);
-            commit(kv_free(static_cast<int>(i % NS)));
+            commit(kv_free(i % NS));
             if (n == 1) commit(q_free);
             for (int j = 0; j < n && ok; ++j) {
                 for (int t = 0; t < tiles; ++t) {
@@ -534,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     fence_proxy_async_smem();
                     tc_fence_after();
                     if (!skip[t] && elect_one()) {
-                        const uint64_t vd = desc_rows_of_k(ring + static_cast<uint32_t>((i + 1) % NS) * L::kTile, L::kPanel);
+                        const uint64_t vd = desc_rows_of_k(ring + ((i + 1) % NS) * L::kTile, L::kPanel);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + ((kk * 2048) >> 4), id_o, j > 0 || kk > 0);
                     }
                     __syncwarp();
-                    if (t == tiles - 1) commit(kv_free(static_cast<int>((i + 1) % NS)));
+                    if (t == tiles - 1) commit(kv_free((i + 1) % NS));
                     if (j == n - 1) {
                         commit(o_full(t));
                     } else {
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                 }
                 if (!ok) break;
                 if (j < n - 1) {
-                    commit(kv_free(static_cast<int>((i + 2) % NS)));
+                    commit(kv_free((i + 2) % NS));
                     if (j == n - 2) commit(q_free);
                 }
                 i += 2;
@@ -567,15 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         const int lw = warp - 9;
         constexpr int C = DP / 8;           // 16-byte pieces of a 16-bit row
         const int pieces = 2 * ksteps;      // of which the products read these
-        int64_t i = 0;                      // slots so far
+        uint32_t i = 0;                     // slots so far
         int parts = 0;
         bool ok = true;
         auto landed = [&](uint32_t bar) {  // arrives when this thread's copies so far have landed
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         };
         auto take_slot = [&]() {  // waits until slot i is free
-            return i < NS || mbar_wait(kv_free(static_cast<int>(i % NS)), static_cast<uint32_t>((i / NS) & 1) ^ 1u);
+            return i < NS || mbar_wait(kv_free(i % NS), ((i / NS) & 1) ^ 1u);
         };
+        Cursor<kRows> now = start;
         // A warp copies `per` rows at once, the same rows of each quarter of 32 of a
         // slot; their places, each found by one lane, are passed round once for a
         // unit's keys and values, and the shared-memory addresses stay the same.
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                 if constexpr (!I8) {
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
-                        const int slot = static_cast<int>(i % NS);
+                        const int slot = i % NS;
                         if (!(ok = take_slot())) break;
                         const uint32_t dst = ring + slot * L::kTile;
                         const uint8_t* src = (v ? a.v : a.k) + 16 * pc;
@@ -731,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                                 if (lw + kLoaders * y < 32 / per && off[x][y] != kNoRow)
                                     w[x][y] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(off[x][y]) * 16);
                             }
-                        const int slot = static_cast<int>(i % NS);
+                        const int slot = i % NS;
                         if (!(ok = take_slot())) break;
                         uint8_t* dst = smem + L::kQ + slot * L::kTile;
 #pragma unroll
@@ -775,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         cp_async_wait_all();
         if (lw == 0 && parts > 0) (void)mbar_wait(q_full, (parts - 1) & 1);
         if (lw == 0)  // boxes too have landed before the CTA ends, whoever gave up
-            for (int64_t k = i < NS ? 0 : i - NS; k < i; ++k) (void)mbar_wait(kv_full(static_cast<int>(k % NS)), (k / NS) & 1);
+            for (uint32_t k = i < NS ? 0 : i - NS; k < i; ++k) (void)mbar_wait(kv_full(k % NS), (k / NS) & 1);
         if (!ok) give_up();
     }
     tc_fence_before();
