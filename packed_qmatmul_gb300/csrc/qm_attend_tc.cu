@@ -70,12 +70,38 @@ QM_DEV bool elect_one() {
     return p != 0;
 }
 
-// Descriptor of values as they lie: rows of keys (the product's K), 64 elements (its
-// N) to a 128-byte swizzled row; 8-row groups 1024 bytes apart, panels of 64
-// elements kPanel bytes apart.
-QM_DEV uint64_t desc_rows_of_k(uint32_t addr, uint32_t panel) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | static_cast<uint64_t>(panel >> 4) << 16 |
-           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+// Descriptors of operands in shared memory, 128-byte swizzled, 8-row groups 1024
+// bytes apart: their constant high words, and the low words at an address. The
+// issuer adds steps to low words alone: it has some 60 clocks for each product.
+// Keys and queries (rows of 64 elements of the product's K) ...
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+QM_DEV uint32_t desc_k_major(uint32_t addr) { return ((addr >> 4) & 0x3FFFu) | 1u << 16; }
+// ... and values as they lie: rows of keys (the product's K), 64 elements (its N) to a
+// row, panels of 64 elements `panel` bytes apart.
+QM_DEV uint32_t desc_rows_of_k(uint32_t addr, uint32_t panel) { return ((addr >> 4) & 0x3FFFu) | (panel >> 4) << 16; }
+
+QM_DEV void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        ".reg .b64 da, db;\n"
+        "mov.b64 da, {%1, %5};\n"
+        "mov.b64 db, {%2, %5};\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "n"(kDescHigh)
+        : "memory");
+}
+QM_DEV void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        ".reg .b64 db;\n"
+        "mov.b64 db, {%2, %5};\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "n"(kDescHigh)
+        : "memory");
 }
 
 // Instruction descriptor, kind::f16, f32 sums, 128 x N; B K-major or (mn) MN-major.
@@ -243,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     auto give_up = [&]() { atomicOr(&g_err_attend, DEV_ERR_TIMEOUT); };
+    // every wait is a whole warp's, and so is its verdict
+    auto wait = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
     const int ksteps = (a.dim + 15) / 16;
     // units of the run's part that `now` is in
     auto part_units = [](const Cursor<kRows>& c) { return static_cast<int>(min(static_cast<int64_t>(c.u1 - c.u), c.left)); };
@@ -286,13 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     const int slot = vi % NS;
                     const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
                     // (only then is the unit's slot in turn: a tile that sat out an item runs ahead of the copies)
-                    if (!mbar_wait(s_full(t), nth & 1)) { ok = false; break; }
+                    if (!wait(s_full(t), nth & 1)) { ok = false; break; }
                     bool odd = false;
                     if constexpr (!I8) {
                         // 0 times an infinity or NaN is NaN: where rows see different keys, a look at the
                         // unit's values (each thread at one key's) tells whether the tensor cores may add them
                         if (cut && differ) {
-                            if (!mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                            if (!wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
                             const uint32_t v = ring + slot * L::kTile;
                             uint32_t high = 0;
 #pragma unroll
@@ -304,12 +332,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                             if (nonfinite<BF16>(high)) atomicOr(word, 1u);
                             __syncwarp();
                             if (lane == 0) mbar_arrive(agreed(t));
-                            if (!mbar_wait(agreed(t), checks & 1)) { ok = false; break; }
+                            if (!wait(agreed(t), checks & 1)) { ok = false; break; }
                             odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
                             ++checks;
                         }
                     }
-                    if (I8 && !mbar_wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                    if (I8 && !wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
                     tc_fence_after();
                     uint32_t raw[4][32];
 #pragma unroll
@@ -408,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     if (lane == 0) mbar_arrive(p_full(t));
                 }
                 // ---- the part's end
-                if (ok && !mbar_wait(o_full(t), parts & 1)) ok = false;
+                if (ok && !wait(o_full(t), parts & 1)) ok = false;
                 ++parts;
                 tc_fence_after();
                 const int part = 2 * blockIdx.x + (starts ? 1 : 0);
@@ -507,15 +535,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         uint32_t i = 0;  // slots so far
         int nth[2] = {0, 0}, parts = 0;
         bool ok = true;
-        auto wait_slot = [&](uint32_t k) { return mbar_wait(kv_full(k % NS), (k / NS) & 1); };
+        auto wait_slot = [&](uint32_t k) { return wait(kv_full(k % NS), (k / NS) & 1); };
         auto scores = [&](int t, uint32_t k) {  // S of tile t over the keys in slot k
             if (elect_one()) {
-                const uint64_t qd = umma_desc_sw128(sq + t * L::kTile), kd = umma_desc_sw128(ring + (k % NS) * L::kTile);
+                const uint32_t qd = desc_k_major(sq + t * L::kTile), kd = desc_k_major(ring + (k % NS) * L::kTile);
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk)
                     if (kk < ksteps) {
                         const uint32_t off = ((kk >> 2) * L::kPanel + (kk & 3) * 32) >> 4;
-                        umma_f16(tmem + 128 * t, qd + off, kd + off, id_s, kk > 0);
+                        mma_ss(tmem + 128 * t, qd + off, kd + off, id_s, kk > 0);
                     }
                 umma_commit(s_full(t));
             }
@@ -529,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         while (now.left > 0 && ok) {
             const int n = part_units(now);
             const int tiles = now.span.rows > 128 ? 2 : 1;
-            if (!(ok = mbar_wait(q_full, parts & 1) && wait_slot(i))) break;
+            if (!(ok = wait(q_full, parts & 1) && wait_slot(i))) break;
             ++parts;
             fence_proxy_async_smem();
             tc_fence_after();
@@ -538,16 +566,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             if (n == 1) commit(q_free);
             for (int j = 0; j < n && ok; ++j) {
                 for (int t = 0; t < tiles; ++t) {
-                    if (!(ok = mbar_wait(p_full(t), nth[t] & 1))) break;
+                    if (!(ok = wait(p_full(t), nth[t] & 1))) break;
                     ++nth[t];
                     if (t == 0 && !(ok = wait_slot(i + 1))) break;
                     fence_proxy_async_smem();
                     tc_fence_after();
                     if (!skip[t] && elect_one()) {
-                        const uint64_t vd = desc_rows_of_k(ring + ((i + 1) % NS) * L::kTile, L::kPanel);
+                        const uint32_t vd = desc_rows_of_k(ring + ((i + 1) % NS) * L::kTile, L::kPanel);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            umma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + ((kk * 2048) >> 4), id_o, j > 0 || kk > 0);
+                            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + ((kk * 2048) >> 4), id_o, j > 0 || kk > 0);
                     }
                     __syncwarp();
                     if (t == tiles - 1) commit(kv_free((i + 1) % NS));
@@ -584,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
         };
         auto take_slot = [&]() {  // waits until slot i is free
-            return i < NS || mbar_wait(kv_free(i % NS), ((i / NS) & 1) ^ 1u);
+            return i < NS || wait(kv_free(i % NS), ((i / NS) & 1) ^ 1u);
         };
         Cursor<kRows> now = start;
         // A warp copies `per` rows at once, the same rows of each quarter of 32 of a
@@ -681,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         while (now.left > 0 && ok) {
             const int n = part_units(now);
             if (parts > 0) {
-                if (!(ok = mbar_wait(q_free, (parts - 1) & 1))) break;
+                if (!(ok = wait(q_free, (parts - 1) & 1))) break;
             }
             ++parts;
             load_q();
