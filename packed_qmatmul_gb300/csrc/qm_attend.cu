@@ -36,19 +36,19 @@ namespace qm {
 namespace attend {
 namespace {
 
-constexpr int kRows = 16;
 constexpr int kWarps = 8;
 constexpr float kNegInf = -INFINITY;
 
 // Stage and shared-memory layout of a kernel variant.
-template <int DP, bool I8>
+template <int DP, bool I8, int MT>
 struct Lay {
+    static constexpr int kRows = 16 * MT;
     static constexpr int kRowBytes = I8 ? DP : 2 * DP;
     static constexpr int kPart = 16 * kRowBytes;                   // 16 keys, or values
     static constexpr int kStage = 2 * kPart + (I8 ? 128 : 0);      // and 16 + 16 scales
     static constexpr int kStages = I8 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
     static constexpr int kChunks = kRowBytes / 16;
-    static constexpr int kRed = kWarps * 8 * DP * 4;
+    static constexpr int kRed = kWarps * 8 * DP * 4;               // sums of eight rows; between, the queries of several tiles
     static constexpr int kMl = kWarps * kRows * 8;
     static constexpr int kSmem = kWarps * kStages * kStage + kRed + kMl;
     // where 16-byte piece c of row r lies: rows that one access reads together
@@ -63,6 +63,7 @@ struct Lay {
         else if constexpr (DP == 128) return r * kRowBytes + ((c ^ (((r >> 1) & 3) << 1)) << 4);
         else return r * kRowBytes + ((c ^ (((r >> 1) & 1) << 1)) << 4);
     }
+    static QM_DEV uint32_t q_at(int r, int c) { return r * 2 * DP + ((c ^ (r & 7)) << 4); }
 };
 
 QM_DEV void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -93,9 +94,10 @@ struct Join {
     int rows, base;
 };
 
-template <int DP, bool BF16, bool I8>
+template <int DP, bool BF16, bool I8, int MT>
 __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __grid_constant__ Args a) {
-    using L = Lay<DP, I8>;
+    using L = Lay<DP, I8, MT>;
+    constexpr int kRows = L::kRows;
     constexpr int ST = L::kStages;
     constexpr int KK = DP / 16;
     constexpr bool PBF = BF16 && !I8;           // type of the weights and values in their product
@@ -158,10 +160,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         cp_async_commit();
     }
 
-    uint32_t qa[KK][4];
-    float acc[DP / 8][4];
-    float top[2], sum[2];
-    int pos[2], kmin[2], kmax[2];  // of rows g and g + 8: the keys they see, [kmin, kmax]
+    uint32_t qa[MT == 1 ? KK : 1][4];
+    const uint32_t sq = smem_u32(red);
+    float acc[MT][DP / 8][4];
+    float top[MT][2], sum[MT][2];
+    int kmin[MT][2], kmax[MT][2];  // of rows 16 mt + g and + 8: the keys they see, [kmin, kmax]
     bool begin = true;             // the next step begins a part of an item
     bool whole_start = false;
     int slot = 0;
@@ -169,33 +172,47 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         if (begin) {
             begin = false;
             whole_start = now.first();
+            const auto query = [&](int r) -> const uint16_t* {  // row r of the item; null past its last
+                if (r >= now.span.rows) return nullptr;
+                const unsigned R = now.tile * kRows + r, i = token_of(a, R), gg = R - i * a.group;
+                return a.q + (now.seq.first + static_cast<int64_t>(i)) * a.q_ts + (now.h * a.group + static_cast<int>(gg)) * a.q_hs;
+            };
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = g + 8 * x;
-                top[x] = kNegInf;
-                sum[x] = 0.f;
-                pos[x] = -1;
-                kmin[x] = 0;
-                kmax[x] = -1;
-                const uint16_t* qrow = nullptr;
-                if (r < now.span.rows) {
-                    const unsigned R = now.tile * kRows + r, i = token_of(a, R), gg = R - i * a.group;
-                    pos[x] = now.seq.len - now.seq.fresh + static_cast<int>(i);
-                    kmin[x] = first_seen(a, pos[x]);
-                    kmax[x] = min(pos[x], a.cap - 1);
-                    qrow = a.q + (now.seq.first + static_cast<int64_t>(i)) * a.q_ts + (now.h * a.group + static_cast<int>(gg)) * a.q_hs;
-                }
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int kk = 0; kk < KK; ++kk)
+                for (int x = 0; x < 2; ++x) {
+                    const int r = 16 * mt + g + 8 * x;
+                    const int at = now.seq.len - now.seq.fresh + static_cast<int>(token_of(a, now.tile * kRows + r));
+                    top[mt][x] = kNegInf;
+                    sum[mt][x] = 0.f;
+                    kmin[mt][x] = r < now.span.rows ? first_seen(a, at) : 0;
+                    kmax[mt][x] = r < now.span.rows ? min(at, a.cap - 1) : -1;
+                    if constexpr (MT == 1) {
+                        const uint16_t* qrow = query(r);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        // codes come four to a lane: their products take the head's elements in that order
-                        const int d = I8 ? 64 * (kk / 4) + 16 * t + 4 * (kk % 4) + 2 * y : 16 * kk + 8 * y + 2 * t;
-                        qa[kk][2 * y + x] = qrow && d < a.dim ? *reinterpret_cast<const uint32_t*>(qrow + d) : 0u;
+                        for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                // codes come four to a lane: their products take the head's elements in that order
+                                const int d = I8 ? 64 * (kk / 4) + 16 * t + 4 * (kk % 4) + 2 * y : 16 * kk + 8 * y + 2 * t;
+                                qa[kk][2 * y + x] = qrow && d < a.dim ? *reinterpret_cast<const uint32_t*>(qrow + d) : 0u;
+                            }
                     }
+                }
+            if constexpr (MT > 1) {  // kept where the warps' sums meet at a part's end
+                for (int i = threadIdx.x; i < kRows * (DP / 8); i += kWarps * 32) {
+                    const int r = i / (DP / 8), c = i % (DP / 8);
+                    const uint16_t* qrow = query(r);
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (qrow && 8 * c < a.dim) v = *reinterpret_cast<const uint4*>(qrow + 8 * c);
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(red) + L::q_at(r, c)) = v;
+                }
+                __syncthreads();
             }
 #pragma unroll
-            for (int j = 0; j < DP / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j) acc[mt][j][0] = acc[mt][j][1] = acc[mt][j][2] = acc[mt][j][3] = 0.f;
         }
         cp_async_wait<ST - 2>();
         __syncwarp();  // the stage is whole, and its predecessor is free in every lane
@@ -210,51 +227,94 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         const Span& sp = now.span;
         if (key0 < sp.hi && key0 + 15 >= sp.lo) {
             const uint32_t kb = ring + slot * L::kStage, vb = kb + L::kPart;
-            float s[2][4] = {};
+            float s[MT][2][4] = {};
+            // queries of tile mt, step kk
+            const auto queries = [&](int mt, int kk, uint32_t (&q)[4]) {
+                if constexpr (MT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q[i] = qa[kk][i];
+                } else if constexpr (!I8) {
+                    ldsm4(sq + L::q_at(16 * mt + (lane & 15), 2 * kk + (lane >> 4)), q);
+                } else {
+                    const int d = 64 * (kk / 4) + 16 * t + 4 * (kk % 4);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint2 v = lds_v2(sq + L::q_at(16 * mt + g + 8 * x, d / 8) + 2 * (d % 8));
+                        q[x] = v.x;
+                        q[2 + x] = v.y;
+                    }
+                }
+            };
             if constexpr (!I8) {
                 const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
                     uint32_t b[4];
                     ldsm4(kb + L::k_at(r, 2 * kk + c), b);
-                    mma16<BF16>(s[0], qa[kk], b[0], b[1]);
-                    mma16<BF16>(s[1], qa[kk], b[2], b[3]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t q[4];
+                        queries(mt, kk, q);
+                        mma16<BF16>(s[mt][0], q, b[0], b[1]);
+                        mma16<BF16>(s[mt][1], q, b[2], b[3]);
+                    }
                 }
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][e] *= a.scale2;
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][n][e] *= a.scale2;
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int h = 0; h < KK / 4; ++h) {
+                    uint4 w[2];
 #pragma unroll
-                    for (int h = 0; h < KK / 4; ++h) {
-                        const uint4 w = lds_v4(kb + L::k_at(8 * n + g, 4 * h + t));
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    for (int n = 0; n < 2; ++n) w[n] = lds_v4(kb + L::k_at(8 * n + g, 4 * h + t));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma16<BF16>(s[n], qa[4 * h + i], codes16<BF16>(prmt(ws[i], 0u, 0x4140)),
-                                        codes16<BF16>(prmt(ws[i], 0u, 0x4342)));
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t b[2][2];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const uint32_t word = i == 0 ? w[n].x : i == 1 ? w[n].y : i == 2 ? w[n].z : w[n].w;
+                            b[n][0] = codes16<BF16>(prmt(word, 0u, 0x4140));
+                            b[n][1] = codes16<BF16>(prmt(word, 0u, 0x4342));
+                        }
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            uint32_t q[4];
+                            queries(mt, 4 * h + i, q);
+                            mma16<BF16>(s[mt][0], q, b[0][0], b[0][1]);
+                            mma16<BF16>(s[mt][1], q, b[1][0], b[1][1]);
+                        }
                     }
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
                     const uint2 sc = lds_v2(kb + 2 * L::kPart + 4 * (8 * n + 2 * t));
                     const float s0 = __uint_as_float(sc.x) * a.scale2, s1 = __uint_as_float(sc.y) * a.scale2;
-                    s[n][0] *= s0; s[n][1] *= s1; s[n][2] *= s0; s[n][3] *= s1;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        s[mt][n][0] *= s0; s[mt][n][1] *= s1; s[mt][n][2] *= s0; s[mt][n][3] *= s1;
+                    }
                 }
             }
             // rows differ in what they see, or the step's keys end or begin in between
             const bool cut = key0 + 15 > min(sp.p0, a.cap - 1) || (a.window && key0 < first_seen(a, sp.p1));
-            uint32_t hidden = 0;  // bit 4n + e
+            uint32_t hidden[MT] = {};  // bit 4n + e
             if (cut) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 8 * n + 2 * t + (e & 1), x = e >> 1;
-                        if (key < kmin[x] || key > kmax[x]) {
-                            s[n][e] = kNegInf;
-                            hidden |= 1u << (4 * n + e);
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + 8 * n + 2 * t + (e & 1), x = e >> 1;
+                            if (key < kmin[mt][x] || key > kmax[mt][x]) {
+                                s[mt][n][e] = kNegInf;
+                                hidden[mt] |= 1u << (4 * n + e);
+                            }
                         }
-                    }
             }
             float vs[2][2], lv[2][2];  // value scales of keys 8n + 2t + e, and their logarithms
             if constexpr (I8) {
@@ -267,47 +327,52 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     lv[n][1] = scale_log2(vs[n][1]);
                 }
             }
-            float from[2];
-            bool grown = false;
+            uint32_t pa[MT][4];
+            float p[MT][2][4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float m = top[x];
+            for (int mt = 0; mt < MT; ++mt) {
+                float from[2];
+                bool grown = false;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float m = top[mt][x];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) m = fmaxf(m, I8 ? s[mt][n][2 * x + e] + lv[n][e] : s[mt][n][2 * x + e]);
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    grown = grown || m > top[mt][x];
+                    from[x] = top[mt][x];
+                    top[mt][x] = m;
+                }
+                if (__any_sync(0xffffffffu, grown)) {
+                    float f[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        f[x] = ex2(from[x] - (top[mt][x] == kNegInf ? 0.f : top[mt][x]));
+                        sum[mt][x] *= f[x];
+                    }
+#pragma unroll
+                    for (int j = 0; j < DP / 8; ++j) {
+                        acc[mt][j][0] *= f[0]; acc[mt][j][1] *= f[0];
+                        acc[mt][j][2] *= f[1]; acc[mt][j][3] *= f[1];
+                    }
+                }
+                const float ref[2] = {top[mt][0] == kNegInf ? 0.f : top[mt][0] - kLift, top[mt][1] == kNegInf ? 0.f : top[mt][1] - kLift};
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        m = fmaxf(m, I8 ? s[n][2 * x + e] + lv[n][e] : s[n][2 * x + e]);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                grown = grown || m > top[x];
-                from[x] = top[x];
-                top[x] = m;
+                    for (int e = 0; e < 4; ++e) {
+                        p[mt][n][e] = ex2(s[mt][n][e] - ref[e >> 1]);
+                        sum[mt][e >> 1] += p[mt][n][e];
+                        if constexpr (I8) p[mt][n][e] = (hidden[mt] >> (4 * n + e)) & 1 ? 0.f : p[mt][n][e] * vs[n][e & 1];
+                    }
+                pa[mt][0] = pack16<PBF>(p[mt][0][0], p[mt][0][1]);
+                pa[mt][1] = pack16<PBF>(p[mt][0][2], p[mt][0][3]);
+                pa[mt][2] = pack16<PBF>(p[mt][1][0], p[mt][1][1]);
+                pa[mt][3] = pack16<PBF>(p[mt][1][2], p[mt][1][3]);
             }
-            if (__any_sync(0xffffffffu, grown)) {
-                float f[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    f[x] = ex2(from[x] - (top[x] == kNegInf ? 0.f : top[x]));
-                    sum[x] *= f[x];
-                }
-#pragma unroll
-                for (int j = 0; j < DP / 8; ++j) {
-                    acc[j][0] *= f[0]; acc[j][1] *= f[0];
-                    acc[j][2] *= f[1]; acc[j][3] *= f[1];
-                }
-            }
-            const float ref[2] = {top[0] == kNegInf ? 0.f : top[0] - kLift, top[1] == kNegInf ? 0.f : top[1] - kLift};
-            float p[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[n][e] = ex2(s[n][e] - ref[e >> 1]);
-                    sum[e >> 1] += p[n][e];
-                    if constexpr (I8) p[n][e] = (hidden >> (4 * n + e)) & 1 ? 0.f : p[n][e] * vs[n][e & 1];
-                }
-            const uint32_t pa[4] = {pack16<PBF>(p[0][0], p[0][1]), pack16<PBF>(p[0][2], p[0][3]),
-                                    pack16<PBF>(p[1][0], p[1][1]), pack16<PBF>(p[1][2], p[1][3])};
             if constexpr (!I8) {
                 // A value that only some of the rows see must not reach the others: 0 times an
                 // infinity or NaN is NaN. Where the rows differ and such a value is there, the
@@ -325,32 +390,38 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     for (int j = 0; j < DP / 16; ++j) {
                         uint32_t b[4];
                         ldsm4_t(vb + L::v_at(r, 2 * j + c), b);
-                        mma16<BF16>(acc[2 * j], pa, b[0], b[1]);
-                        mma16<BF16>(acc[2 * j + 1], pa, b[2], b[3]);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma16<BF16>(acc[mt][2 * j], pa[mt], b[0], b[1]);
+                            mma16<BF16>(acc[mt][2 * j + 1], pa[mt], b[2], b[3]);
+                        }
                     }
                 } else {
 #pragma unroll 1
                     for (int k = 0; k < 16; ++k) {
                         // p[row g + 8x][key k] is in lane 4g + (k % 8) / 2, entry [k / 8][2x + k % 2]
                         const int src = 4 * g + ((k & 7) >> 1);
-                        float pk[2];
+                        float pk[MT][2];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float mine = k < 8 ? ((k & 1) ? p[0][2 * x + 1] : p[0][2 * x]) : ((k & 1) ? p[1][2 * x + 1] : p[1][2 * x]);
-                            pk[x] = __shfl_sync(0xffffffffu, mine, src);
-                        }
-                        const bool see[2] = {key0 + k >= kmin[0] && key0 + k <= kmax[0], key0 + k >= kmin[1] && key0 + k <= kmax[1]};
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float mine = k < 8 ? ((k & 1) ? p[mt][0][2 * x + 1] : p[mt][0][2 * x]) : ((k & 1) ? p[mt][1][2 * x + 1] : p[mt][1][2 * x]);
+                                pk[mt][x] = __shfl_sync(0xffffffffu, mine, src);
+                            }
 #pragma unroll
                         for (int j = 0; j < DP / 8; ++j) {
                             const uint32_t w = lds_u32(vb + L::v_at(k, j) + 4 * t);
                             const float v0 = BF16 ? __uint_as_float(w << 16) : f16_bits_to_f32(w & 0xFFFFu);
                             const float v1 = BF16 ? __uint_as_float(w & 0xFFFF0000u) : f16_bits_to_f32(w >> 16);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                if (see[x]) {
-                                    acc[j][2 * x] = fmaf(pk[x], v0, acc[j][2 * x]);
-                                    acc[j][2 * x + 1] = fmaf(pk[x], v1, acc[j][2 * x + 1]);
-                                }
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    if (key0 + k >= kmin[mt][x] && key0 + k <= kmax[mt][x]) {
+                                        acc[mt][j][2 * x] = fmaf(pk[mt][x], v0, acc[mt][j][2 * x]);
+                                        acc[mt][j][2 * x + 1] = fmaf(pk[mt][x], v1, acc[mt][j][2 * x + 1]);
+                                    }
                         }
                     }
                 }
@@ -367,7 +438,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t pick = 0x0400u + 0x0101u * i;  // byte i of the two keys, to bytes 0 and 2
-                        mma16<PBF>(acc[4 * jb + i], pa, codes16<PBF>(prmt(w[0], w[1], pick)), codes16<PBF>(prmt(w[2], w[3], pick)));
+                        const uint32_t b0 = codes16<PBF>(prmt(w[0], w[1], pick)), b1 = codes16<PBF>(prmt(w[2], w[3], pick));
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) mma16<PBF>(acc[mt][4 * jb + i], pa[mt], b0, b1);
                     }
                 }
             }
@@ -378,10 +451,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         if (ends || now.left == 1) {
             // ---- the part's end: add the warps' sums
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
-                sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-                if (t == 0) ml[warp * kRows + g + 8 * x] = make_float2(top[x], sum[x]);
+            for (int x = 0; x < 2 * MT; ++x) {
+                float total = sum[x >> 1][x & 1];
+                total += __shfl_xor_sync(0xffffffffu, total, 1);
+                total += __shfl_xor_sync(0xffffffffu, total, 2);
+                if (t == 0) ml[warp * kRows + g + 8 * x] = make_float2(top[x >> 1][x & 1], total);
             }
             __syncthreads();
             const int rows = now.span.rows;
@@ -390,26 +464,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
             // swaps 16-byte pieces of row g of `red` so that the rows' writes differ in bank
             auto piece = [](int row, int c4) { return c4 ^ (2 * (row & 3) | (row >> 2)); };
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 2 * MT; ++x) {
                 if (8 * x >= rows) break;
+                const int mt = x >> 1, y = x & 1;
                 float m = kNegInf;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kRows + g + 8 * x].x);
-                const float f = ex2(top[x] - (m == kNegInf ? 0.f : m));
+                const float f = ex2(top[mt][y] - (m == kNegInf ? 0.f : m));
                 float* mine = red + (warp * 8 + g) * DP;
                 if constexpr (!I8) {
 #pragma unroll
                     for (int j = 0; j < DP / 8; ++j)
                         *reinterpret_cast<float2*>(mine + 4 * piece(g, 2 * j + (t >> 1)) + 2 * (t & 1)) =
-                            make_float2(acc[j][2 * x] * f, acc[j][2 * x + 1] * f);
+                            make_float2(acc[mt][j][2 * y] * f, acc[mt][j][2 * y + 1] * f);
                 } else {
 #pragma unroll
                     for (int jb = 0; jb < DP / 32; ++jb)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            *reinterpret_cast<float4*>(mine + 4 * piece(g, 8 * jb + 2 * t + y)) =
-                                make_float4(acc[4 * jb][2 * x + y] * f, acc[4 * jb + 1][2 * x + y] * f,
-                                            acc[4 * jb + 2][2 * x + y] * f, acc[4 * jb + 3][2 * x + y] * f);
+                        for (int z = 0; z < 2; ++z)
+                            *reinterpret_cast<float4*>(mine + 4 * piece(g, 8 * jb + 2 * t + z)) =
+                                make_float4(acc[mt][4 * jb][2 * y + z] * f, acc[mt][4 * jb + 1][2 * y + z] * f,
+                                            acc[mt][4 * jb + 2][2 * y + z] * f, acc[mt][4 * jb + 3][2 * y + z] * f);
                 }
                 __syncthreads();
                 const int rr = threadIdx.x / (DP / 4), c4 = threadIdx.x % (DP / 4);
@@ -532,23 +607,26 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     }
 }
 
-template <int DP, bool BF16, bool I8>
+template <int DP, bool BF16, bool I8, int MT>
 cudaError_t run_rows(const Args& a, int runs, cudaStream_t st) {
-    auto kern = attend_rows_kernel<DP, BF16, I8>;
-    constexpr int smem = Lay<DP, I8>::kSmem;
+    auto kern = attend_rows_kernel<DP, BF16, I8, MT>;
+    constexpr int smem = Lay<DP, I8, MT>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(Lay<DP, I8, MT>::kRows * DP * 2 <= Lay<DP, I8, MT>::kRed, "queries");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(runs), kWarps * 32, smem, st, a);
 }
 
-cudaError_t launch_rows(const Args& a, int runs, int dp, bool bf16, bool i8, cudaStream_t st) {
-    if (dp == 64) {
-        if (i8) return bf16 ? run_rows<64, true, true>(a, runs, st) : run_rows<64, false, true>(a, runs, st);
-        return bf16 ? run_rows<64, true, false>(a, runs, st) : run_rows<64, false, false>(a, runs, st);
-    }
-    if (i8) return bf16 ? run_rows<128, true, true>(a, runs, st) : run_rows<128, false, true>(a, runs, st);
-    return bf16 ? run_rows<128, true, false>(a, runs, st) : run_rows<128, false, false>(a, runs, st);
+template <int DP, int MT>
+cudaError_t rows_of_type(const Args& a, int runs, bool bf16, bool i8, cudaStream_t st) {
+    if (i8) return bf16 ? run_rows<DP, true, true, MT>(a, runs, st) : run_rows<DP, false, true, MT>(a, runs, st);
+    return bf16 ? run_rows<DP, true, false, MT>(a, runs, st) : run_rows<DP, false, false, MT>(a, runs, st);
+}
+
+cudaError_t launch_rows(const Args& a, int runs, int dp, int rows, bool bf16, bool i8, cudaStream_t st) {
+    if (dp == 64) return rows == 16 ? rows_of_type<64, 1>(a, runs, bf16, i8, st) : rows_of_type<64, 3>(a, runs, bf16, i8, st);
+    return rows == 16 ? rows_of_type<128, 1>(a, runs, bf16, i8, st) : rows_of_type<128, 2>(a, runs, bf16, i8, st);
 }
 
 cudaError_t launch_join(const Args& a, int runs, int dp, bool bf16, cudaStream_t st) {
@@ -592,11 +670,14 @@ void set_quotient(int d, uint32_t* mul, int* shift) {
     *shift = l - 1;
 }
 
-// Whether the rows that share a key head (the most of any sequence, if the caller
-// said; else the average) are few.
-bool few_rows(const qm_batch& b, int group) {
+// Rows of an item: by the rows that share a key head (the most of any sequence, if
+// the caller said; else the average). Up to 16, and up to 32 of heads over 64
+// elements or 48 of others, go to attend_rows_kernel, more to attend_tiles_kernel.
+int item_rows(const qm_batch& b, int group, int dp) {
     const int64_t most = b.max_new > 0 ? std::min<int64_t>(b.max_new, b.tokens) : (b.tokens + b.seqs - 1) / b.seqs;
-    return most * group <= kRows;
+    const int64_t rows = most * group;
+    const int several = dp == 64 ? 48 : 32;
+    return rows <= 16 ? 16 : rows <= several ? several : kTileRows;
 }
 
 }  // namespace
@@ -612,15 +693,17 @@ uint32_t attend_rows_read_clear_error() {
 }
 
 size_t attend_workspace_bytes(const qm_cache& c, const qm_batch& b, int q_heads) {
-    return workspace_layout(num_sms(), few_rows(b, q_heads / c.heads) ? kRows : kTileRows, c.dim <= 64 ? 64 : 128).all;
+    const int dp = c.dim <= 64 ? 64 : 128;
+    return workspace_layout(num_sms(), item_rows(b, q_heads / c.heads, dp), dp).all;
 }
 
 cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_heads& q, const qm_heads& out,
                                 float* lse, float scale, int64_t window, void* workspace, cudaStream_t st) {
     const int dp = c.dim <= 64 ? 64 : 128;
     const int runs = num_sms();
-    const bool few = few_rows(b, q.heads / c.heads);
-    const Ws ws = workspace_layout(runs, few ? kRows : kTileRows, dp);
+    const int rows = item_rows(b, q.heads / c.heads, dp);
+    const bool few = rows != kTileRows;
+    const Ws ws = workspace_layout(runs, rows, dp);
     uint8_t* wb = static_cast<uint8_t*>(workspace);
     Args a = {};
     a.q = static_cast<const uint16_t*>(q.data);
@@ -666,7 +749,7 @@ cudaError_t launch_cache_attend(const qm_cache& c, const qm_batch& b, const qm_h
     a.ml = reinterpret_cast<float2*>(wb + ws.ml);
     a.part = reinterpret_cast<float*>(wb + ws.part);
     const bool bf16 = q.dtype == QM_BF16, i8 = c.dtype == QM_I8;
-    const cudaError_t e = few ? launch_rows(a, runs, dp, bf16, i8, st) : launch_tiles(a, c, runs, bf16, st);
+    const cudaError_t e = few ? launch_rows(a, runs, dp, rows, bf16, i8, st) : launch_tiles(a, c, runs, bf16, st);
     if (e != cudaSuccess) return e;
     return few ? cudaSuccess : launch_join(a, runs, dp, bf16, st);
 }
