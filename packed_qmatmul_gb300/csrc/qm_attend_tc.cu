@@ -204,27 +204,6 @@ __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, ui
     }
 }
 
-// Codes of the rows that a lane copies, as 16-bit values in a slot: 16 codes are
-// two neighbouring 16-byte pieces, whose swizzled addresses differ in one bit.
-template <bool BF16, int TURNS, int GROUPS>
-QM_DEV void store_codes(uint8_t* slot, const uint32_t (&at)[TURNS], const uint4 (&w)[4][TURNS], int lw, bool on) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-        for (int y = 0; y < TURNS; ++y)
-            if (lw + kLoaders * y < GROUPS && on) {
-                const uint32_t ws[4] = {w[x][y].x, w[x][y].y, w[x][y].z, w[x][y].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[2 * e] = codes16<BF16>(prmt(ws[e], 0u, 0x4140));
-                    o[2 * e + 1] = codes16<BF16>(prmt(ws[e], 0u, 0x4342));
-                }
-                *reinterpret_cast<uint4*>(slot + at[y] + 32 * 128 * x) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(slot + (at[y] ^ 16u) + 32 * 128 * x) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-}
-
 struct TileArgs {
     CUtensorMap tk, tv;  // keys and values [pages][heads][page_size][dim], boxes of 64 elements x box_rows tokens
     CUtensorMap tq;      // queries [1][tokens][heads][dim], boxes of 64 elements x group heads x 128 / group tokens
@@ -726,78 +705,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
             next.step(a);
             if (next.left > 0) look(next);
         };
-        const auto start_part = [&]() {  // waits until the queries' place is free and loads them
-            if (parts > 0 && !wait(q_free, (parts - 1) & 1)) return false;
+        look(now);
+        while (now.left > 0 && ok) {
+            const int n = part_units(now);
+            if (parts > 0) {
+                if (!(ok = wait(q_free, (parts - 1) & 1))) break;
+            }
             ++parts;
             load_q();
-            return true;
-        };
-        look(now);
-        if constexpr (I8) {
-            // Codes pass through registers and become exact 16-bit values. While a slot's codes are
-            // turned and stored the next slot's are under way: a unit's keys and values by turns.
-            uint4 wk[4][turns], wv[4][turns];
-            const auto load = [&](const uint8_t* part, uint4 (&w)[4][turns]) {
-                const uint8_t* src = part + 16 * pc;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int y = 0; y < turns; ++y) {
-                        w[x][y] = make_uint4(0u, 0u, 0u, 0u);
-                        if (lw + kLoaders * y < 32 / per && off[x][y] != kNoRow)
-                            w[x][y] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(off[x][y]) * 16);
-                    }
-            };
-            const auto publish = [&]() {
-                mbar_arrive(kv_full(i % NS));
-                ++i;
-            };
-            pass_round();
-            look_on();
-            load(a.k, wk);
-            while (now.left > 0 && ok) {
-                const int n = part_units(now);
-                if (!(ok = start_part())) break;
-                for (int j = 0; j < n; ++j) {
-                    load(a.v, wv);
-                    float ks[4], vs[4];
-                    if (lw == 0) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            ks[x] = place[x] != kNoRow ? __ldg(a.ks + splace[x]) : 0.f;
-                            vs[x] = place[x] != kNoRow ? __ldg(a.vs + splace[x]) : 0.f;
-                        }
-                    }
-                    if (!(ok = take_slot())) break;
-                    store_codes<BF16, turns, 32 / per>(smem + L::kQ + (i % NS) * L::kTile, dst16, wk, lw, 2 * pc < pieces);
-                    publish();
-                    if (now.left > 1) {
-                        pass_round();
-                        look_on();
-                        load(a.k, wk);
-                    }
-                    if (!(ok = take_slot())) break;
-                    store_codes<false, turns, 32 / per>(smem + L::kQ + (i % NS) * L::kTile, dst16, wv, lw, 2 * pc < pieces);
-                    if (lw == 0) {
-                        // the values two units back have been used, so their scales have been read
-                        float* sc = reinterpret_cast<float*>(smem + L::kScale) + ((i >> 1) & 1) * 384;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            sc[32 * x + lane] = ks[x] * a.scale2;
-                            sc[128 + 32 * x + lane] = vs[x];
-                            sc[256 + 32 * x + lane] = scale_log2(vs[x]);
-                        }
-                    }
-                    publish();
-                    now.step(a);
-                }
-            }
-        } else {
-            while (now.left > 0 && ok) {
-                const int n = part_units(now);
-                if (!(ok = start_part())) break;
-                for (int j = 0; j < n && ok; ++j) {
-                    pass_round();
+            for (int j = 0; j < n && ok; ++j) {
+                pass_round();
+                if constexpr (!I8) {
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         const int slot = i % NS;
@@ -838,9 +756,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                         ++i;
                         if (v == 0) look_on();
                     }
-                    if (!ok) break;
-                    now.step(a);
+                } else {
+                    // codes: through registers, as exact 16-bit values
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const uint8_t* src = (v ? a.v : a.k) + 16 * pc;
+                        uint4 w[4][turns];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < turns; ++y) {
+                                w[x][y] = make_uint4(0u, 0u, 0u, 0u);
+                                if (lw + kLoaders * y < 32 / per && off[x][y] != kNoRow)
+                                    w[x][y] = *reinterpret_cast<const uint4*>(src + static_cast<uint64_t>(off[x][y]) * 16);
+                            }
+                        const int slot = i % NS;
+                        if (!(ok = take_slot())) break;
+                        uint8_t* dst = smem + L::kQ + slot * L::kTile;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < turns; ++y) {
+                                if (lw + kLoaders * y < 32 / per && 2 * pc < pieces) {
+                                    const uint32_t ws[4] = {w[x][y].x, w[x][y].y, w[x][y].z, w[x][y].w};
+                                    uint32_t o[8];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t lo = prmt(ws[e], 0u, 0x4140), hi = prmt(ws[e], 0u, 0x4342);
+                                        o[2 * e] = v ? codes16<false>(lo) : codes16<BF16>(lo);
+                                        o[2 * e + 1] = v ? codes16<false>(hi) : codes16<BF16>(hi);
+                                    }
+                                    // pieces 2 pc and 2 pc + 1 of a swizzled row: the other of a pair of addresses
+                                    *reinterpret_cast<uint4*>(dst + dst16[y] + 32 * 128 * x) = make_uint4(o[0], o[1], o[2], o[3]);
+                                    *reinterpret_cast<uint4*>(dst + (dst16[y] ^ 16u) + 32 * 128 * x) = make_uint4(o[4], o[5], o[6], o[7]);
+                                }
+                            }
+                        if (v == 1 && lw == 0) {
+                            // the values two units back have been used, so their scales have been read
+                            float* sc = reinterpret_cast<float*>(smem + L::kScale) + ((i >> 1) & 1) * 384;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float ks = place[x] != kNoRow ? __ldg(a.ks + splace[x]) : 0.f, vs = place[x] != kNoRow ? __ldg(a.vs + splace[x]) : 0.f;
+                                sc[32 * x + lane] = ks * a.scale2;
+                                sc[128 + 32 * x + lane] = vs;
+                                sc[256 + 32 * x + lane] = scale_log2(vs);
+                            }
+                        }
+                        mbar_arrive(kv_full(slot));
+                        ++i;
+                        if (v == 1) look_on();
+                    }
                 }
+                if (!ok) break;
+                now.step(a);
             }
         }
         cp_async_wait_all();
