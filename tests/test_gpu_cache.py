@@ -585,3 +585,15 @@ def test_nothing_to_do():
     out = qm.cache_attend(cache, batch, torch.zeros(3, 2, 64, dtype=BF, device="cuda"))
     assert out.shape == (3, 2, 64)
     qm.qm_device_status()
+
+
+def test_norm_rope_more_tokens_than_one_launch_takes():
+    T = 65535 * 16 + 37  # heads of 64 elements or fewer: 16 tokens to a block
+    g = gen(20)
+    x = randn(g, T, 1, 8, dtype=BF)
+    w = randn(g, 8, dtype=BF)
+    table = angles(32, 8)
+    pos = torch.arange(T) % 32
+    (y,) = qm.head_norm_rope([x.cuda()], pos.cuda(), qm.Rope(table.cuda()), [w.cuda()])
+    want, size = norm_rope_def(x, w, 1e-6, table, pos, "half")
+    assert rounded_within(y.cpu(), want, 2.0 ** -18 * size).all()
