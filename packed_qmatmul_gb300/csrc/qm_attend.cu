@@ -17,13 +17,21 @@
 // some 130 KB in flight. The products are m16n8k16 tensor-core instructions on 16
 // rows (rows that the item lacks are zeros: the tensor pipe has time to spare). At the
 // end of an item the warps' sums are added through shared memory in warp order while
-// the next item's copies are already under way.
+// the next item's copies are already under way. Up to 32 rows (48 of heads of 64
+// elements: the sums fit in registers) take two or three such tiles of rows at once, their queries
+// in shared memory; against attend_tiles_kernel 114 to 121 us for 32 x 8 tokens of 4 query
+// heads to a key head over 4096, and 141 to 361 over 8-bit codes.
+// Measured: one token of 64 ragged sequences of up to 8192 (16 / 8 heads of 128,
+// 1.08 GB) 178 us, 6.05 TB/s, 0.91 of the copy rate; of one sequence of 1500 8.4 us, of one of
+// 32768 30 us (4.4 TB/s).
 //
 // 8-bit codes are exact in both 16-bit types, so they enter the products as they
 // are: a key's scale multiplies its score, a value's scale its weight. Scaled weights
 // and value codes are float16 whatever q's type (three bits more than bfloat16, whose
 // range they do not need: the running maximum includes the values' scales, which
-// keeps them within [0, 2^8]).
+// keeps them within [0, 2^8]). Turning them takes some 220 of a step's 770
+// instructions, and instructions are what bounds it: 4 sequences of 65 to 131 thousand tokens
+// (32 / 8 heads) 238 us, 3.4 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
