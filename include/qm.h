@@ -254,8 +254,8 @@ qm_status qm_experts_route(const void* ids, int32_t id_type, int64_t P, int64_t 
  * All arithmetic is float32, each result rounded once to its type. */
 
 /* Rows of heads: element i of head h of token t at
- * data[t*token_stride + h*head_stride + i] (strides in elements, multiples of 8,
- * not negative; the address 16-byte aligned), such as a part of the rows that a
+ * data[t*token_stride + h*head_stride + i] (strides in elements, multiples of 8
+ * where their axis has more than one, not negative; the address 16-byte aligned), such as a part of the rows that a
  * fused q/k/v product leaves. dtype QM_BF16 or QM_F16. */
 typedef struct qm_heads {
     void* data;

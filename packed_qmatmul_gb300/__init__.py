@@ -12,6 +12,7 @@ per byte, plus e8m0 scales per 32 values).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -145,6 +146,17 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on(stream):
+    """Where a call's own tensors are allocated: on the stream that uses them (the caching allocator hands
+    out again what is freed on a stream as soon as that stream's earlier work is enqueued)."""
+    if stream is None:
+        return _HERE_NOW
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+_HERE_NOW = contextlib.nullcontext()
 
 
 # ---------------------------------------------------------------- weights
@@ -610,7 +622,8 @@ def head_norm_rope(xs: Sequence[torch.Tensor], positions: Optional[torch.Tensor]
                    weights: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6, stream=None) -> list:
     """Every head of xs[i] [tokens, heads_i, dim] (queries, keys: any strided rows) normed by weights[i] [dim] and
     rotated by its token's position."""
-    return _norm_rope(xs, None, positions, rope, weights, eps, stream)
+    with _on(stream):
+        return _norm_rope(xs, None, positions, rope, weights, eps, stream)
 
 
 def cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, rope: Optional[Rope] = None,
@@ -623,13 +636,14 @@ def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[fl
                  lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of the new tokens' queries [tokens, heads, dim] over their sequences in the cache; with lse, (out,
     the scores' log-sum-exp [tokens, heads])."""
-    qd, out, od = _heads_and_like(q, batch.tokens, cache.dim, "q")
-    heads = q.shape[1]
-    total = torch.empty((batch.tokens, heads), dtype=torch.float32, device=q.device) if lse else None
-    if workspace is None:
-        need = qm_cache_attend_workspace(cache, batch, heads)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(load_library().qm_cache_attend(
-        cache._c, batch._c, qd, od, _ptr(total), cache.dim ** -0.5 if scale is None else scale, window, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
-    return (out, total) if lse else out
+    with _on(stream):
+        qd, out, od = _heads_and_like(q, batch.tokens, cache.dim, "q")
+        heads = q.shape[1]
+        total = torch.empty((batch.tokens, heads), dtype=torch.float32, device=q.device) if lse else None
+        if workspace is None:
+            need = qm_cache_attend_workspace(cache, batch, heads)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        _check(load_library().qm_cache_attend(
+            cache._c, batch._c, qd, od, _ptr(total), cache.dim ** -0.5 if scale is None else scale, window, _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        return (out, total) if lse else out

@@ -848,9 +848,11 @@ cudaError_t run_tiles(const TileArgs& a, int runs, cudaStream_t st) {
 // have at least a box's 64 elements.
 void make_maps(TileArgs& t, const qm_cache& c) {
     const Args& a = t.a;
-    if (a.dim >= 64 && 128 % a.group == 0 && a.q_ts > 0 && a.q_hs > 0) {
+    // the stride of an axis of one never counts, but has to be one that a map can have
+    const auto stride = [](int64_t n, int64_t s) { return static_cast<uint64_t>(n > 1 ? 2 * s : 256); };
+    if (a.dim >= 64 && 128 % a.group == 0 && (a.tokens == 1 || a.q_ts > 0) && (a.heads == 1 || a.q_hs > 0)) {
         const uint64_t qd[4] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads), static_cast<uint64_t>(a.tokens), 1};
-        const uint64_t qs[3] = {static_cast<uint64_t>(2 * a.q_hs), static_cast<uint64_t>(2 * a.q_ts), 256};
+        const uint64_t qs[3] = {stride(a.heads, a.q_hs), stride(a.tokens, a.q_ts), 256};
         t.q_boxes = make_tmap_4d_16(&t.tq, a.q, qd, qs, 64, a.group, 128 / a.group);
     }
     if (c.dtype == QM_I8 || c.page_size % 32 != 0 || c.dim < 64 || c.pages < 1) return;
@@ -858,8 +860,6 @@ void make_maps(TileArgs& t, const qm_cache& c) {
     while (c.page_size % rows != 0) rows /= 2;
     const uint64_t dims[4] = {static_cast<uint64_t>(c.dim), static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.heads),
                               static_cast<uint64_t>(c.pages)};
-    // the stride of an axis of one never counts, but has to be one that a map can have
-    const auto stride = [](int64_t n, int64_t s) { return static_cast<uint64_t>(n > 1 ? 2 * s : 256); };
     const uint64_t strides[3] = {stride(c.page_size, c.token_stride), stride(c.heads, c.head_stride), stride(c.pages, c.page_stride)};
     if (make_tmap_4d_16(&t.tk, c.k, dims, strides, 64, rows) && make_tmap_4d_16(&t.tv, c.v, dims, strides, 64, rows)) t.box_rows = rows;
 }

@@ -17,12 +17,13 @@ static const int64_t kMaxPieces = int64_t(0xFFFFFFFE) * 16;  // in bytes
 
 static bool float16ish(int32_t dt) { return dt == QM_BF16 || dt == QM_F16; }
 
-static qm_status check_heads(const qm_heads* x, const std::string& name, bool live) {
+static qm_status check_heads(const qm_heads* x, const std::string& name, int64_t tokens) {
+    const bool live = tokens > 0;
     if (!x) return fail(QM_EINVAL, name + ": NULL");
     if (x->heads < 1) return fail(QM_EINVAL, name + ": needs at least one head");
     if (!float16ish(x->dtype)) return fail(QM_EINVAL, name + ": dtype must be QM_BF16 or QM_F16");
     if (x->token_stride < 0 || x->head_stride < 0) return fail(QM_EINVAL, name + ": negative stride");
-    if (x->token_stride % 8 != 0 || x->head_stride % 8 != 0)
+    if ((tokens > 1 && x->token_stride % 8 != 0) || (x->heads > 1 && x->head_stride % 8 != 0))  // an axis of one has none
         return fail(QM_EINVAL, name + ": strides must be multiples of 8 elements");
     if (live && !x->data) return fail(QM_EINVAL, name + ": NULL");
     if (live && !aligned16(x->data)) return fail(QM_EINVAL, name + ": base address must be 16-byte aligned");
@@ -67,7 +68,8 @@ static qm_status check_cache(const qm_cache* c) {
     if (c->pages < 0 || c->pages > kMaxI32) return fail(QM_EINVAL, "cache: pages must be 0 .. 2^31-1");
     if (c->page_stride < 0 || c->head_stride < 0 || c->token_stride < 0)
         return fail(QM_EINVAL, "cache: negative stride");
-    if (c->page_stride % step != 0 || c->head_stride % step != 0 || c->token_stride % step != 0)
+    if ((c->pages > 1 && c->page_stride % step != 0) || (c->heads > 1 && c->head_stride % step != 0) ||
+        (c->page_size > 1 && c->token_stride % step != 0))
         return fail(QM_EINVAL, "cache: strides must be multiples of " + std::to_string(step) + " elements");
     if ((c->pages > 1 && c->page_stride < c->dim) || (c->heads > 1 && c->head_stride < c->dim) ||
         (c->page_size > 1 && c->token_stride < c->dim))
@@ -140,8 +142,8 @@ qm_status qm_head_norm_rope(const qm_heads* xs, const qm_heads* outs, const void
     if (s != QM_OK) return s;
     for (int i = 0; i < count; ++i) {
         const std::string at = "[" + std::to_string(i) + "]";
-        if ((s = check_heads(&xs[i], "x" + at, tokens > 0)) != QM_OK) return s;
-        if ((s = check_heads(&outs[i], "out" + at, tokens > 0)) != QM_OK) return s;
+        if ((s = check_heads(&xs[i], "x" + at, tokens)) != QM_OK) return s;
+        if ((s = check_heads(&outs[i], "out" + at, tokens)) != QM_OK) return s;
         if ((s = check_written(outs[i], "out" + at, tokens, dim)) != QM_OK) return s;
         if (xs[i].dtype != xs[0].dtype) return fail(QM_EINVAL, "x" + at + ": dtype differs from x[0]");
         if (outs[i].dtype != xs[i].dtype) return fail(QM_EINVAL, "out" + at + ": dtype differs from x" + at);
@@ -174,8 +176,8 @@ qm_status qm_cache_append(const qm_cache* cache, const qm_batch* batch, const qm
     if ((s = check_eps(eps)) != QM_OK) return s;
     if ((s = check_rope(rope, cache->dim)) != QM_OK) return s;
     const bool live = batch->tokens > 0 && batch->seqs > 0;
-    if ((s = check_heads(k, "k", live)) != QM_OK) return s;
-    if ((s = check_heads(v, "v", live)) != QM_OK) return s;
+    if ((s = check_heads(k, "k", live ? batch->tokens : 0)) != QM_OK) return s;
+    if ((s = check_heads(v, "v", live ? batch->tokens : 0)) != QM_OK) return s;
     if (k->heads != cache->heads) return fail(QM_EINVAL, "k: heads differ from the cache's");
     if (v->heads != cache->heads) return fail(QM_EINVAL, "v: heads differ from the cache's");
     if (v->dtype != k->dtype) return fail(QM_EINVAL, "v: dtype differs from k's");
@@ -203,8 +205,8 @@ qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm
     if (s != QM_OK) return s;
     if ((s = check_batch(batch)) != QM_OK) return s;
     const bool live = batch->tokens > 0 && batch->seqs > 0;
-    if ((s = check_heads(q, "q", live)) != QM_OK) return s;
-    if ((s = check_heads(out, "out", live)) != QM_OK) return s;
+    if ((s = check_heads(q, "q", live ? batch->tokens : 0)) != QM_OK) return s;
+    if ((s = check_heads(out, "out", live ? batch->tokens : 0)) != QM_OK) return s;
     if (q->heads % cache->heads != 0) return fail(QM_EINVAL, "q: heads must be a multiple of the cache's");
     if (q->heads / cache->heads > 32768) return fail(QM_ENOTSUP, "q: at most 32768 query heads to a key head");
     if (cache->dtype != QM_I8 && q->dtype != cache->dtype) return fail(QM_EINVAL, "q: dtype differs from the cache's");

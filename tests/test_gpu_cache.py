@@ -495,34 +495,40 @@ def test_rows_of_no_sequence_are_not_written():
     check_attend(P, q, out[:43].cpu(), None, 0.125)
 
 
-def test_offsets_past_32_bits():
+@pytest.mark.parametrize("codes", [True, False])
+def test_offsets_past_32_bits(codes):
     """A cache of more than 2^31 elements a part, used at both of its ends."""
     g = gen(15)
     kv, page, dim = 2, 128, 128
     pages = (1 << 31) // (kv * page * dim) + 40
-    k = torch.empty(pages, kv, page, dim, dtype=torch.int8, device="cuda")
+    k = torch.empty(pages, kv, page, dim, dtype=torch.int8 if codes else BF, device="cuda")
     v = torch.empty_like(k)
-    ks, vs = (torch.full((pages, kv, page), math.nan, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((pages, kv, page), math.nan, device="cuda") if codes else None for _ in range(2))
     ids = [pages - 1, 0, pages - 30, 5]
     seqs = [(1, 400), (60, 100)]
     table = torch.tensor([ids, [pages - 2, -1, -1, -1]], dtype=torch.int32)
-    small = Paged(g, seqs, kv, dim, page, BF, codes=True)
+    small = Paged(g, seqs, kv, dim, page, BF, codes=codes)
     for i in range(2):
         for j in range(-(-seqs[i][1] // page)):
             src, dst = int(small.table[i, j]), int(table[i, j])
             k[dst], v[dst] = small.k[src].cuda(), small.v[src].cuda()
-            ks[dst], vs[dst] = small.ks[src].cuda(), small.vs[src].cuda()
+            if codes:
+                ks[dst], vs[dst] = small.ks[src].cuda(), small.vs[src].cuda()
     cache = qm.Cache(k, v, ks, vs)
     off = torch.tensor([0, 1, 61], dtype=torch.int32).cuda()
-    batch = qm.Batch(torch.tensor([400, 100], dtype=torch.int32).cuda(), table.cuda(), off, tokens=61, max_new=60)
+    lens = torch.tensor([400, 100], dtype=torch.int32).cuda()
     q = randn(g, 61, 4, dim, dtype=BF)
-    out = qm.cache_attend(cache, batch, q.cuda(), scale=0.1)
-    check_attend(small, q, out.cpu(), None, 0.1)
+    for most in (60, 1):  # either kernel
+        batch = qm.Batch(lens, table.cuda(), off, tokens=61, max_new=most)
+        out = qm.cache_attend(cache, batch, q.cuda(), scale=0.1)
+        check_attend(small, q, out.cpu(), None, 0.1)
     new = randn(g, 61, kv, dim, dtype=BF)
     qm.cache_append(cache, batch, new.cuda(), new.cuda())
-    r = 399 - 3 * page
-    assert (cache.v[5, :, r].cpu().double() * cache.v_scales[5, :, r].cpu().double()[:, None] - new[0].double()).abs().max() < 0.05
-    assert (cache.v[pages - 2, :, 99].cpu().double() * cache.v_scales[pages - 2, :, 99].cpu().double()[:, None] - new[60].double()).abs().max() < 0.05
+    for p, r, i in ((5, 399 - 3 * page, 0), (pages - 2, 99, 60)):
+        got = cache.v[p, :, r].cpu().double()
+        if codes:
+            got = got * cache.v_scales[p, :, r].cpu().double()[:, None]
+        assert (got - new[i].double()).abs().max() < (0.05 if codes else 1e-30)
 
 
 def test_another_stream_and_a_captured_graph():
@@ -597,3 +603,33 @@ def test_norm_rope_more_tokens_than_one_launch_takes():
     (y,) = qm.head_norm_rope([x.cuda()], pos.cuda(), qm.Rope(table.cuda()), [w.cuda()])
     want, size = norm_rope_def(x, w, 1e-6, table, pos, "half")
     assert rounded_within(y.cpu(), want, 2.0 ** -18 * size).all()
+
+
+def test_calls_on_a_side_stream_own_their_tensors():
+    g = gen(21)
+    P = Paged(g, [(1, 5000), (1, 700)], 2, 128, 16, BF)
+    q = randn(g, 2, 4, 128, dtype=BF).cuda()
+    cache, batch = P.cache(), P.batch()
+    s = torch.cuda.Stream()
+    want = qm.cache_attend(cache, batch, q)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        got = []
+        for _ in range(20):
+            got.append(qm.cache_attend(cache, batch, q, stream=stream))
+            torch.full((1 << 20,), 7, dtype=torch.int32, device="cuda")  # would take the workspace's memory, were it this stream's
+        torch.cuda.synchronize()
+        for o in got:
+            assert torch.equal(o, want)
+
+
+def test_strides_of_axes_of_one_do_not_count():
+    g = gen(22)
+    P = Paged(g, [(1, 90)], 1, 64, 16, BF)
+    q = randn(g, 1, 1, 64, dtype=BF)
+    odd = q.cuda().as_strided((1, 1, 64), (3, 5, 1))
+    out = qm.cache_attend(P.cache(), P.batch(), odd, scale=0.125)
+    check_attend(P, q, out.cpu(), None, 0.125)
+    (a,) = qm.head_norm_rope([odd], weights=[torch.ones(64, dtype=BF, device="cuda")])
+    (b,) = qm.head_norm_rope([q.cuda()], weights=[torch.ones(64, dtype=BF, device="cuda")])
+    assert torch.equal(a, b)
