@@ -119,11 +119,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 
     grid_launch_dependents();
     grid_dependency_wait();
-    Cut split = {};
-    Cursor<kRows> now = find_run<kRows, false>(a, blockIdx.x, gridDim.x, split);
+    const Load work = measure<kRows>(a, gridDim.x);
+    int64_t run_from;
+    Cursor<kRows> now = run_start<kRows, false>(a, work, blockIdx.x, run_from);
+    const int64_t run_units = (static_cast<int>(blockIdx.x) + 1 < work.runs ? share(work.total, blockIdx.x + 1, work.runs) : work.total) - run_from;
+    if (run_units <= 0) return;
+    now.left = run_units;
     Cursor<kRows> ahead = now;
-    if (now.left == 0) return;
-    const int64_t run_units = now.left;
     Join join = {-1, 0, 0, 0, 0, 0};
 
     // ---- copies: the place of key row (lane & 15) of the step `ahead` is at
@@ -528,9 +530,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 __syncthreads();
             }
             if (!done) {
-                const int64_t at = split.from + run_units - now.left;  // this unit
+                const int64_t at = run_from + run_units - now.left;  // this unit
                 if (ends) {  // the item's last part: the CTA joins the item when its run is done
-                    const int owner = split.run_of(at - (now.u - now.span.u0()));
+                    const int64_t first_unit = at - (now.u - now.span.u0());
+                    const int owner = static_cast<int>(((first_unit + 1) * work.runs - 1) / work.total);  // the run that holds it
                     join = Join{owner, now.seq.first, now.h, now.tile * kRows, rows, now.seq.len - now.seq.fresh};
                 } else {  // the run's last part, for a later CTA to join
                     __threadfence();

@@ -143,9 +143,10 @@ QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine) {
     const int lane = threadIdx.x & 31;
     const unsigned tiles = mine ? tiles_of<R>(a, s) : 0;
     int64_t n = 0;
-    if (tiles <= 2)
+    constexpr unsigned kAlone = 12;
+    if (tiles <= kAlone)
         for (unsigned t = 0; t < tiles; ++t) n += tile_units<R>(a, s, t, tiles);
-    for (unsigned many = __ballot_sync(0xffffffffu, tiles > 2); many; many &= many - 1) {
+    for (unsigned many = __ballot_sync(0xffffffffu, tiles > kAlone); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq q = shfl_seq(s, src);
         const unsigned all = __shfl_sync(0xffffffffu, tiles, src);
@@ -192,14 +193,6 @@ struct Cursor {
         --left;
         if (++u == u1 && left > 0) next_item(a);
     }
-};
-
-// How the units are cut.
-struct Cut {
-    int64_t total, from;  // units in all, and before this CTA's run
-    int runs;             // that have units
-    // The run that holds unit g.
-    QM_DEV int run_of(int64_t g) const { return static_cast<int>(((g + 1) * runs - 1) / total); }
 };
 
 // total * c / runs, in 32 bits where they hold it.
@@ -265,58 +258,63 @@ QM_DEV Cursor<R> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
     return k;
 }
 
-// The calling warp's cursor at the start of run `c` of `runs` (left = 0: the run
-// is empty). Every lane returns the same. WHOLE: the ends of runs are moved to an
-// end of the item they fall in where splitting it would cost more than the uneven
-// runs: a split's parts (written and joined) cost about 8 units of an item of two
-// tiles and 5 of one of a single tile; whole items of s units leave the longest run of those that
-// should have L each with s where s > L, and with up to s more than L else.
-// Ragged chunks in a window 127 -> 87 us, 16 chunks of 512 90 -> 59.
-template <int R, bool WHOLE>
-QM_DEV Cursor<R> find_run(const Args& a, int c, int runs, Cut& cut) {
+// The units in all, and those of one key head of the lane's sequence among the first 32.
+struct Load {
+    int64_t total, units0;
+    Seq seq0;
+    int runs;  // that have units
+};
+template <int R>
+QM_DEV Load measure(const Args& a, int runs) {
     const int lane = threadIdx.x & 31;
-    int64_t total = 0, units0 = 0;
-    Seq seq0 = {};
+    Load w = {};
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
         Seq seq = {};
         const bool mine = s0 + lane < a.seqs;
         if (mine) seq = load_seq(a, s0 + lane);
-        const int64_t units = head_units<R>(a, seq, mine);
+        int64_t n = head_units<R>(a, seq, mine);
         if (s0 == 0) {
-            seq0 = seq;
-            units0 = units;
+            w.seq0 = seq;
+            w.units0 = n;
         }
-        int64_t n = units;
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
-        total += n;
+        w.total += n;
     }
-    total *= a.kv_heads;
-    if (total < runs) runs = static_cast<int>(total);  // the CTAs past the last unit have nothing
+    w.total *= a.kv_heads;
+    w.runs = w.total < runs ? static_cast<int>(w.total) : runs;  // the CTAs past the last unit have nothing
+    return w;
+}
+
+// Where run `c` begins: unit `at`, and the cursor there (the calling warp's; every
+// lane returns the same, left is not set); the last one's end for c = runs. WHOLE: moved to an
+// end of the item it falls in where splitting that would cost more than uneven runs: a split's
+// parts (written and joined) cost about 8 units of an item of two
+// tiles and 5 of one of a single tile; whole items of s units leave the longest run of those that
+// should have L each with s where s > L, and with up to s more than L else.
+// Ragged chunks in a window 127 -> 87 us, 16 chunks of 512 90 -> 59.
+template <int R, bool WHOLE>
+QM_DEV Cursor<R> run_start(const Args& a, const Load& w, int c, int64_t& at) {
     Cursor<R> k = {};
-    if (c >= runs) return k;
-    int64_t from = share(total, c, runs), to = c + 1 == runs ? total : share(total, c + 1, runs);
-    k = locate<R>(a, from, seq0, units0);
+    at = w.total;
+    if (c >= w.runs) return k;
+    at = share(w.total, c, w.runs);
+    k = locate<R>(a, at, w.seq0, w.units0);
     if constexpr (WHOLE) {
-        const int64_t even = share(total, 1, runs);
-        const auto move = [&](int64_t g, const Cursor<R>& at) -> int64_t {
-            const int span = at.span.u1() - at.span.u0(), in = at.u - at.span.u0();
-            const int cost = at.span.rows > R / 2 ? 8 : 5;
-            const bool whole = span <= cost || (span > even && span <= even + cost);
-            return in == 0 || !whole ? g : 2 * in < span ? g - in : g + span - in;
-        };
-        if (to < total) to = move(to, locate<R>(a, to, seq0, units0));
-        const int64_t moved = move(from, k);
-        if (moved < from) {
-            k.u = k.span.u0();
-        } else if (moved > from) {
-            k.left = 1;  // not the last: there are units after the item
-            if (moved < total) k.next_item(a);
+        const int64_t even = share(w.total, 1, w.runs);
+        const int span = k.span.u1() - k.span.u0(), in = k.u - k.span.u0();
+        const int cost = k.span.rows > R / 2 ? 8 : 5;
+        if (in > 0 && (span <= cost || (span > even && span <= even + cost))) {
+            if (2 * in < span) {
+                at -= in;
+                k.u = k.span.u0();
+            } else {
+                at += span - in;
+                k.left = 1;  // only so that next_item looks at what follows
+                if (at < w.total) k.next_item(a);
+            }
         }
-        from = moved;
     }
-    k.left = to - from;
-    cut = Cut{total, from, runs};
     return k;
 }
 

@@ -243,37 +243,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 
     grid_launch_dependents();
     grid_dependency_wait();
-    Cut split = {};
-    const Cursor<kRows> start = find_run<kRows, true>(a, blockIdx.x, gridDim.x, split);
-    if (start.left == 0) {
-        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
-        return;
-    }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(kv_full(i), 32 * kLoaders);
-            mbar_init(kv_free(i), 1);
+    // the run's start, its end, the barriers and the tensor memory, a warp each
+    struct Run {
+        Cursor<kRows> start;
+        int64_t from, to;
+    };
+    static_assert(sizeof(Run) <= 8 * 96, "run");
+    Run* run = reinterpret_cast<Run*>(smem + L::kCursors);
+    if (warp < 2) {
+        const Load work = measure<kRows>(a, gridDim.x);
+        int64_t at;
+        const Cursor<kRows> k = run_start<kRows, true>(a, work, blockIdx.x + warp, at);
+        if (lane == 0) {
+            if (warp == 0) {
+                run->start = k;
+                run->from = at;
+            } else {
+                run->to = at;
+            }
         }
-        mbar_init(q_free, 1);
-        mbar_init(q_full, 32 * kLoaders);
-        mbar_init(done, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
-            mbar_init(o_full(t), 1);
-            mbar_init(agreed(t), 4);
-            skip[t] = odd_word[t] = odd_word[2 + t] = odd_word[4 + t] = 0;
+    } else if (warp == 9) {
+        if (lane == 0) {
+            for (int i = 0; i < NS; ++i) {
+                mbar_init(kv_full(i), 32 * kLoaders);
+                mbar_init(kv_free(i), 1);
+            }
+            mbar_init(q_free, 1);
+            mbar_init(q_full, 32 * kLoaders);
+            mbar_init(done, 1);
+            for (int t = 0; t < 2; ++t) {
+                mbar_init(s_full(t), 1);
+                mbar_init(p_full(t), 4);
+                mbar_init(o_full(t), 1);
+                mbar_init(agreed(t), 4);
+                skip[t] = odd_word[t] = odd_word[2 + t] = odd_word[4 + t] = 0;
+            }
+            fence_mbar_init();
         }
-        fence_mbar_init();
-    }
-    if (warp == 8) {
+    } else if (warp == 8) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    Cursor<kRows> start = run->start;
+    start.left = run->to - run->from;
+    __syncthreads();  // the cursors of the warps that form weights lie there from here on
     const uint32_t tmem = *tmem_slot;
+    if (start.left <= 0) {
+        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
+        if (warp == 8) tmem_dealloc(tmem, 512);
+        return;
+    }
     auto give_up = [&]() { atomicOr(&g_err_attend, DEV_ERR_TIMEOUT); };
     // every wait is a whole warp's, and so is its verdict
     auto wait = [](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0; };
@@ -301,14 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         __syncwarp();
         while (now->left > 0 && ok) {
             const int n = part_units(*now);
-            const bool starts = now->first(), ends = now->u + n == now->u1, done_here = starts && ends;
-            const int rows = now->span.rows;
-            const unsigned R = now->tile * kRows + 128 * t + row;
-            const bool mine = 128 * t + row < rows;
-            const int pos = now->seq.len - now->seq.fresh + static_cast<int>(token_of(a, R));
-            const int kmin = mine ? first_seen(a, pos) : 0, kmax = mine ? min(pos, a.cap - 1) : -1;
+            // (what only the part's end needs is read again there: the units' loop has no register to spare)
+            int kmin = 0, kmax = -1;
+            if (128 * t + row < now->span.rows) {
+                const int at = now->seq.len - now->seq.fresh + static_cast<int>(token_of(a, now->tile * kRows + 128 * t + row));
+                kmin = first_seen(a, at);
+                kmax = min(at, a.cap - 1);
+            }
             float ref = -INFINITY, total = 0.f;
-            if (128 * t < rows) {
+            if (128 * t < now->span.rows) {
                 // keys that every row of the item sees lie within [all_lo, all_hi]
                 const int all_hi = min(now->span.p0, a.cap - 1), all_lo = first_seen(a, now->span.p1);
                 const bool differ = now->span.p0 != now->span.p1;
@@ -442,6 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     if (lane == 0) mbar_arrive(p_full(t));
                 }
                 // ---- the part's end
+                const bool starts = now->first(), done_here = starts && now->u + n == now->u1;
+                const int rows = now->span.rows;
+                const unsigned R = now->tile * kRows + 128 * t + row;
+                const bool mine = 128 * t + row < rows;
+                const int pos = now->seq.len - now->seq.fresh + static_cast<int>(token_of(a, R));
                 if (ok && !wait(o_full(t), parts & 1)) ok = false;
                 ++parts;
                 tc_fence_after();
@@ -513,13 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                     }
                 }
             }
-            if (threadIdx.x == 0 && !done_here && starts) {
+            const bool starts = now->first(), ends = now->u + n == now->u1;
+            if (threadIdx.x == 0 && starts && !ends) {
                 int* d = a.desc + blockIdx.x * 8;
                 d[1] = 1;
                 d[2] = now->seq.first;
                 d[3] = now->h;
                 d[4] = static_cast<int>(now->tile * kRows);
-                d[5] = rows;
+                d[5] = now->span.rows;
                 d[6] = now->seq.len - now->seq.fresh;
             }
             if (!starts) first_part = ends ? 2 : 1;
