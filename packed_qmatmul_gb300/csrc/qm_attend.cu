@@ -58,7 +58,8 @@ struct Lay {
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRed = kWarps * 8 * DP * 4;               // sums of eight rows; between, the queries of several tiles
     static constexpr int kMl = kWarps * kRows * 8;
-    static constexpr int kSmem = kWarps * kStages * kStage + kRed + kMl;
+    static constexpr int kRun = kWarps * kStages * kStage + kRed + kMl;  // the CTA's run
+    static constexpr int kSmem = kRun + 128;
     // where 16-byte piece c of row r lies: rows that one access reads together
     // must differ in bank group
     static QM_DEV uint32_t k_at(int r, int c) {
@@ -119,12 +120,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 
     grid_launch_dependents();
     grid_dependency_wait();
-    const Load work = measure<kRows>(a, gridDim.x);
-    int64_t run_from;
-    Cursor<kRows> now = run_start<kRows, false>(a, work, blockIdx.x, run_from);
-    const int64_t run_units = (static_cast<int>(blockIdx.x) + 1 < work.runs ? share(work.total, blockIdx.x + 1, work.runs) : work.total) - run_from;
-    if (run_units <= 0) return;
-    now.left = run_units;
+    struct Run {
+        Cursor<kRows> start;
+        int64_t to, total;  // the unit after the run, units in all
+        int runs;
+    };
+    static_assert(sizeof(Run) <= 128, "run");
+    Run* run = reinterpret_cast<Run*>(smem + L::kRun);
+    if (warp == 0) {
+        const Load work = measure<kRows>(a, gridDim.x);
+        int64_t from;
+        Cursor<kRows> k = run_start<kRows, false>(a, work, blockIdx.x, from);
+        if (lane == 0) {
+            run->to = static_cast<int>(blockIdx.x) + 1 < work.runs ? share(work.total, blockIdx.x + 1, work.runs) : work.total;
+            run->total = work.total;
+            run->runs = work.runs;
+            k.left = run->to - from;
+            run->start = k;
+        }
+    }
+    __syncthreads();
+    Cursor<kRows> now = run->start;
+    if (now.left <= 0) return;
     Cursor<kRows> ahead = now;
     Join join = {-1, 0, 0, 0, 0, 0};
 
@@ -530,10 +547,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 __syncthreads();
             }
             if (!done) {
-                const int64_t at = run_from + run_units - now.left;  // this unit
+                const int64_t at = run->to - now.left;  // this unit
                 if (ends) {  // the item's last part: the CTA joins the item when its run is done
                     const int64_t first_unit = at - (now.u - now.span.u0());
-                    const int owner = static_cast<int>(((first_unit + 1) * work.runs - 1) / work.total);  // the run that holds it
+                    const int owner = static_cast<int>(((first_unit + 1) * run->runs - 1) / run->total);  // the run that holds it
                     join = Join{owner, now.seq.first, now.h, now.tile * kRows, rows, now.seq.len - now.seq.fresh};
                 } else {  // the run's last part, for a later CTA to join
                     __threadfence();
