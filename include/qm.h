@@ -356,7 +356,9 @@ size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, i
  * receives the natural logarithm of the sum of exp(scale * (q . k_j)). A token
  * that sees nothing gets zeros and -infinity; values and scores at positions that
  * a token does not see never reach its results, whatever they hold. q's dtype is
- * the cache's, or either 16-bit type over QM_I8; out's is q's. Rows of no
+ * the cache's, or either 16-bit type over QM_I8; out's is q's. Weights are rounded
+ * to the cache's type before they meet values (over codes: with the value's scale, to
+ * float16); in float16 one below 2^-22 of its row's largest loses bits, below 2^-33 all. Rows of no
  * sequence are not written. out shares no element with q or the cache. The
  * results are the same bits in every run of the same arguments. */
 qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm_heads* q, const qm_heads* out,

@@ -19,19 +19,24 @@
 // end of an item the warps' sums are added through shared memory in warp order while
 // the next item's copies are already under way. Up to 32 rows (48 of heads of 64
 // elements: the sums fit in registers) take two or three such tiles of rows at once, their queries
-// in shared memory; against attend_tiles_kernel 114 to 121 us for 32 x 8 tokens of 4 query
-// heads to a key head over 4096, and 141 to 361 over 8-bit codes.
+// in shared memory; against attend_tiles_kernel 112 to 121 us for 32 x 8 tokens of 4 query
+// heads to a key head over 4096, and 137 to 361 over 8-bit codes.
 // Measured: one token of 64 ragged sequences of up to 8192 (16 / 8 heads of 128,
 // 1.08 GB) 178 us, 6.05 TB/s, 0.91 of the copy rate; of one sequence of 1500 8.4 us, of one of
 // 32768 30 us (4.4 TB/s).
 //
 // 8-bit codes are exact in both 16-bit types, so they enter the products as they
-// are: a key's scale multiplies its score, a value's scale its weight. Scaled weights
-// and value codes are float16 whatever q's type (three bits more than bfloat16, whose
-// range they do not need: the running maximum includes the values' scales, which
-// keeps them within [0, 2^8]). Turning them takes some 220 of a step's 770
-// instructions, and instructions are what bounds it: 4 sequences of 65 to 131 thousand tokens
-// (32 / 8 heads) 238 us, 3.4 TB/s.
+// are: a key's scale multiplies its score, a value's scale its weight. All operands
+// are float16 whatever q's type: a code takes fewer instructions to become one than to become
+// bfloat16, bfloat16 queries fit after an exact power of two for each row, and scaled weights
+// have three bits more (the running maximum includes the values' scales, which
+// keeps them within [0, 2^8]). Instructions, not bytes, are what bounds it: 4 sequences
+// of 65 to 131 thousand tokens (32 / 8 heads) 205 us, 4.0 TB/s (238 with keys turned into
+// bfloat16); 16 x 2 tokens of 8 query heads to a key head over 8192 84 us (93).
+//
+// Float16 weights, here and over a float16 cache: lifted by 2^8, a weight (times its value's scale)
+// keeps all its bits down to 2^-22 of the row's largest, fewer below, and none past 2^-33.
+// It shows where the values of a row's large weights are zero in an element.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -59,7 +64,7 @@ struct Lay {
     static constexpr int kRed = kWarps * 8 * DP * 4;               // sums of eight rows; between, the queries of several tiles
     static constexpr int kMl = kWarps * kRows * 8;
     static constexpr int kRun = kWarps * kStages * kStage + kRed + kMl;  // the CTA's run
-    static constexpr int kSmem = kRun + 128;
+    static constexpr int kSmem = kRun + 384;
     // where 16-byte piece c of row r lies: rows that one access reads together
     // must differ in bank group
     static QM_DEV uint32_t k_at(int r, int c) {
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     constexpr int kRows = L::kRows;
     constexpr int ST = L::kStages;
     constexpr int KK = DP / 16;
-    constexpr bool PBF = BF16 && !I8;           // type of the weights and values in their product
+    constexpr bool PBF = BF16 && !I8;           // type of the operands
     constexpr float kLift = PBF ? 0.f : 8.f;    // float16 weights in [0, 2^8]: the small ones keep their bits
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -124,8 +129,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         Cursor<kRows> start;
         int64_t to, total;  // the unit after the run, units in all
         int runs;
+        float back[kRows];  // see below
     };
-    static_assert(sizeof(Run) <= 128, "run");
+    static_assert(sizeof(Run) <= 384, "run");
     Run* run = reinterpret_cast<Run*>(smem + L::kRun);
     if (warp == 0) {
         const Load work = measure<kRows>(a, gridDim.x);
@@ -191,6 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     const uint32_t sq = smem_u32(red);
     float acc[MT][DP / 8][4];
     float top[MT][2], sum[MT][2];
+    float back[MT][2];             // bfloat16 queries over codes: what their scores are still to be multiplied by
     int kmin[MT][2], kmax[MT][2];  // of rows 16 mt + g and + 8: the keys they see, [kmin, kmax]
     bool begin = true;             // the next step begins a part of an item
     bool whole_start = false;
@@ -224,6 +231,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                                 const int d = I8 ? 64 * (kk / 4) + 16 * t + 4 * (kk % 4) + 2 * y : 16 * kk + 8 * y + 2 * t;
                                 qa[kk][2 * y + x] = qrow && d < a.dim ? *reinterpret_cast<const uint32_t*>(qrow + d) : 0u;
                             }
+                        if constexpr (I8 && BF16) {
+                            float big = 0.f;
+#pragma unroll
+                            for (int kk = 0; kk < KK; ++kk) big = larger(big, larger(largest2(qa[kk][x]), largest2(qa[kk][2 + x])));
+                            big = larger(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                            big = larger(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                            const RowScale rs = row_scale(big);
+                            back[mt][x] = rs.back;
+#pragma unroll
+                            for (int kk = 0; kk < KK; ++kk) {
+                                qa[kk][x] = to_f16x2(qa[kk][x], rs.by);
+                                qa[kk][2 + x] = to_f16x2(qa[kk][2 + x], rs.by);
+                            }
+                        }
                     }
                 }
             if constexpr (MT > 1) {  // kept where the warps' sums meet at a part's end
@@ -232,9 +253,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     const uint16_t* qrow = query(r);
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
                     if (qrow && 8 * c < a.dim) v = *reinterpret_cast<const uint4*>(qrow + 8 * c);
+                    if constexpr (I8 && BF16) {  // the lanes of a row agree on its scale
+                        float big = larger(larger(largest2(v.x), largest2(v.y)), larger(largest2(v.z), largest2(v.w)));
+#pragma unroll
+                        for (int m = 1; m < DP / 8; m <<= 1) big = larger(big, __shfl_xor_sync(0xffffffffu, big, m));
+                        const RowScale rs = row_scale(big);
+                        v = make_uint4(to_f16x2(v.x, rs.by), to_f16x2(v.y, rs.by), to_f16x2(v.z, rs.by), to_f16x2(v.w, rs.by));
+                        if (c == 0) run->back[r] = rs.back;
+                    }
                     *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(red) + L::q_at(r, c)) = v;
                 }
                 __syncthreads();
+                if constexpr (I8 && BF16) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) back[mt][x] = run->back[16 * mt + g + 8 * x];
+                }
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -304,15 +339,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const uint32_t word = i == 0 ? w[n].x : i == 1 ? w[n].y : i == 2 ? w[n].z : w[n].w;
-                            b[n][0] = codes16<BF16>(prmt(word, 0u, 0x4140));
-                            b[n][1] = codes16<BF16>(prmt(word, 0u, 0x4342));
+                            codes4(word, b[n][0], b[n][1]);
                         }
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
                             uint32_t q[4];
                             queries(mt, 4 * h + i, q);
-                            mma16<BF16>(s[mt][0], q, b[0][0], b[0][1]);
-                            mma16<BF16>(s[mt][1], q, b[1][0], b[1][1]);
+                            mma16<false>(s[mt][0], q, b[0][0], b[0][1]);
+                            mma16<false>(s[mt][1], q, b[1][0], b[1][1]);
                         }
                     }
                 }
@@ -322,6 +356,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     const float s0 = __uint_as_float(sc.x) * a.scale2, s1 = __uint_as_float(sc.y) * a.scale2;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
+                        if constexpr (BF16) {
+                            s[mt][n][0] *= back[mt][0]; s[mt][n][1] *= back[mt][0]; s[mt][n][2] *= back[mt][1]; s[mt][n][3] *= back[mt][1];
+                        }
                         s[mt][n][0] *= s0; s[mt][n][1] *= s1; s[mt][n][2] *= s0; s[mt][n][3] *= s1;
                     }
                 }

@@ -404,6 +404,35 @@ QM_DEV uint32_t codes16(uint32_t x) {
     }
 }
 
+// The four codes of a word as two pairs of float16.
+QM_DEV void codes4(uint32_t word, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = word ^ 0x80808080u, b = 0x64806480u;
+    const uint32_t x = prmt(u, 0x64646464u, 0x4140), y = prmt(u, 0x64646464u, 0x4342);
+    const __half2 c = *reinterpret_cast<const __half2*>(&b);
+    const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&x), c), q = __hsub2(*reinterpret_cast<const __half2*>(&y), c);
+    lo = *reinterpret_cast<const uint32_t*>(&p);
+    hi = *reinterpret_cast<const uint32_t*>(&q);
+}
+
+// A row of bfloat16 as float16: the power of two that brings its largest magnitude
+// to 2^14 .. 2^15, and its inverse; beside an infinity or NaN the finite elements stay
+// finite. The eight bits of every element above 2^-31 of the largest stay whole.
+struct RowScale {
+    float by, back;
+};
+QM_DEV RowScale row_scale(float largest) {
+    const uint32_t e0 = (__float_as_uint(largest) >> 23) & 255u;
+    const uint32_t e = min(max(e0, 15u), 254u);
+    return RowScale{__uint_as_float((268u - e) << 23), __uint_as_float((e - 14u) << 23)};
+}
+QM_DEV float largest2(uint32_t pair) {  // of two bfloat16 magnitudes (a NaN as an integer above infinity)
+    return __uint_as_float(max((pair << 16) & 0x7FFF0000u, pair & 0x7FFF0000u));
+}
+QM_DEV float larger(float a, float b) { return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))); }
+QM_DEV uint32_t to_f16x2(uint32_t pair, float by) {
+    return pack_f16x2(__uint_as_float(pair << 16) * by, __uint_as_float(pair & 0xFFFF0000u) * by);
+}
+
 // log2 of a value scale, held within 2^+-30 (zero and NaN: the low end).
 QM_DEV float scale_log2(float s) {
     float y;

@@ -13,7 +13,8 @@
 //    registers, weights P = 2^(t - ref) rounded to 16 bits back over it. ref follows
 //    the running maximum lazily: only when it has grown by kSlack (a factor of 2^8
 //    or 2^4) is O rescaled, which is exact in float32 whenever it happens; weights stay
-//    below 2^8 (bfloat16) or 2^12 (float16).
+//    below 2^8 (bfloat16) or 2^12 (float16, lifted by 2^8: all bits down to 2^-22 of the
+//    row's largest, none past 2^-33).
 //  * warp 8: issues the products: Q and K from shared memory (128-byte swizzle, K
 //    major), P from tensor memory, V from shared memory as it lies in the cache
 //    (rows of keys: MN major); S and O of both tiles fill the 512 tensor-memory columns.

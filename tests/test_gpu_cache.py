@@ -482,6 +482,45 @@ def test_large_and_infinite_scores(new):
     check_attend(P, q, out.cpu(), lse.cpu(), 1.0)
 
 
+@pytest.mark.parametrize("new,heads,dim", [(1, 4, 128), (5, 8, 128), (9, 8, 64), (3, 4, 96), (70, 8, 128)])
+@pytest.mark.parametrize("e", [-100, -60, 14, 60, 96])
+def test_queries_of_any_size_over_codes(new, heads, dim, e):
+    """Rows from 2^(e-12) to 2^e, one with an element 2^12 above the rest: a power of two is exact
+    throughout, so the bits are those of e = 0, and the scores' log-sum-exp keeps its bound."""
+    g = gen(31)
+    P = Paged(g, [(new, 300), (1, 20)], 1, dim, 32, BF, True)
+    q = (randn(g, new + 1, heads, dim, sigma=16.0).round() / 16).clamp(-3.5, 3.5)
+    q *= 2.0 ** -(torch.arange(heads) % 5 * 3.0)[None, :, None]
+    q[:, 1, 3] *= 2.0 ** 12
+    q = q.to(BF)
+    cache, batch = P.cache(), P.batch()
+    got, want = (qm.cache_attend(cache, batch, (q.double() * 2.0 ** x).to(BF).cuda(), scale=2.0 ** -x / 8, lse=True) for x in (e, 0))
+    qm.qm_device_status()
+    assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16))
+    assert torch.equal(got[1].view(torch.int32), want[1].view(torch.int32))
+    at, lse = 0, want[1].cpu().double()
+    for i, (n, length) in enumerate(P.seqs):
+        _, wl, _, size = attend_def(q[at: at + n], P.keys[i], P.vals[i], n, length, heads, 0.125, 0, P.width * P.page)
+        ds = size * (dim + 4) * 2.0 ** -23
+        assert ((lse[at: at + n] - wl).abs() <= ds + 2.0 ** -20 * (1 + wl.abs())).all()
+        at += n
+
+
+@pytest.mark.parametrize("new", [1, 5, 40])
+def test_infinite_queries_over_codes(new):
+    g = gen(29)
+    P = Paged(g, [(new, 260)], 1, 64, 16, BF, True)
+    P.k[..., 0] = P.k[..., 0].abs().clamp(min=1)  # the infinity meets codes above zero alone
+    q = randn(g, new, 3, 64, dtype=BF)
+    q[:, 0, 0] = -math.inf  # every score -inf, whatever the rest of the row holds
+    q[:, 0, 1:] = q[:, 0, 1:].sign() * 2.0 ** 100
+    q[:, 1, 0] = math.nan
+    out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=1.0, lse=True)
+    assert torch.isneginf(lse[:, 0]).all() and torch.isnan(out[:, 0]).all()
+    assert torch.isnan(lse[:, 1]).all() and torch.isnan(out[:, 1]).all()
+    assert torch.isfinite(out[:, 2]).all() and torch.isfinite(lse[:, 2]).all()
+
+
 def test_rows_of_no_sequence_are_not_written():
     g = gen(14)
     P = Paged(g, [(3, 50), (40, 60)], 2, 64, 16, BF)
