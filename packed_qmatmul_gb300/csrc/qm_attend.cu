@@ -22,7 +22,7 @@
 // in shared memory; against attend_tiles_kernel 112 to 121 us for 32 x 8 tokens of 4 query
 // heads to a key head over 4096, and 137 to 361 over 8-bit codes.
 // Measured: one token of 64 ragged sequences of up to 8192 (16 / 8 heads of 128,
-// 1.08 GB) 178 us, 6.05 TB/s, 0.91 of the copy rate; of one sequence of 1500 8.4 us, of one of
+// 1.08 GB) 175 to 180 us, 6.0 to 6.2 TB/s, 0.9 of the copy rate; of one sequence of 1500 8.4 us, of one of
 // 32768 30 us (4.4 TB/s).
 //
 // 8-bit codes are exact in both 16-bit types, so they enter the products as they
