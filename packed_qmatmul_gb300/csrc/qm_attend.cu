@@ -10,17 +10,20 @@
 // 2^-9 or 2^-12 that does not add up over keys, as the output's own rounding).
 //
 // Every key and value is read once for up to 16 rows, 2 flops a byte and row: what
-// bounds it is HBM. One CTA per SM, eight warps; a warp takes 16 of a unit's 128 keys and
+// bounds it is HBM. One CTA per SM, eight warps; a warp takes an eighth of a unit's keys and
 // streams them through its own ring of shared-memory stages with 16-byte
 // asynchronous copies (whole 2 * DP-byte rows; the pages' places are looked up one
 // step ahead), so that warps wait for nothing but their own copies and an SM keeps
-// some 130 KB in flight. The products are m16n8k16 tensor-core instructions on 16
+// 64 to 139 KB in flight. A step is 16 keys of 256-byte rows and 32 of shorter ones: with 16 the
+// step's own latency and its fixed instructions (place, maxima, rescaling) are what bounds those (8-bit
+// codes, below; 32 x 2 tokens of 7 query heads of 64 over 8192 38.9 -> 32.5 us; ragged short
+// items lose a little to the coarser units: 32 x 5 tokens over 100 to 4000 31.4 -> 32.4). The products are m16n8k16 tensor-core instructions on 16
 // rows (rows that the item lacks are zeros: the tensor pipe has time to spare). At the
 // end of an item the warps' sums are added through shared memory in warp order while
 // the next item's copies are already under way. Up to 32 rows (48 of heads of 64
 // elements: the sums fit in registers) take two or three such tiles of rows at once, their queries
 // in shared memory; against attend_tiles_kernel 112 to 121 us for 32 x 8 tokens of 4 query
-// heads to a key head over 4096, and 137 to 361 over 8-bit codes.
+// heads to a key head over 4096, and 121 to 361 over 8-bit codes.
 // Measured: one token of 64 ragged sequences of up to 8192 (16 / 8 heads of 128,
 // 1.08 GB) 175 to 180 us, 6.0 to 6.2 TB/s, 0.9 of the copy rate; of one sequence of 1500 8.4 us, of one of
 // 32768 30 us (4.4 TB/s).
@@ -31,8 +34,8 @@
 // bfloat16, bfloat16 queries fit after an exact power of two for each row, and scaled weights
 // have three bits more (the running maximum includes the values' scales, which
 // keeps them within [0, 2^8]). Instructions, not bytes, are what bounds it: 4 sequences
-// of 65 to 131 thousand tokens (32 / 8 heads) 205 us, 4.0 TB/s (238 with keys turned into
-// bfloat16); 16 x 2 tokens of 8 query heads to a key head over 8192 84 us (93).
+// of 65 to 131 thousand tokens (32 / 8 heads) 179 us, 4.6 TB/s (205 in steps of 16 keys, 238 with keys also turned into
+// bfloat16); 16 x 2 tokens of 8 query heads to a key head over 8192 74 us (84, 93).
 //
 // Float16 weights, here and over a float16 cache: lifted by 2^8, a weight (times its value's scale)
 // keeps all its bits down to 2^-22 of the row's largest, fewer below, and none past 2^-33.
@@ -57,9 +60,10 @@ template <int DP, bool I8, int MT>
 struct Lay {
     static constexpr int kRows = 16 * MT;
     static constexpr int kRowBytes = I8 ? DP : 2 * DP;
-    static constexpr int kPart = 16 * kRowBytes;                   // 16 keys, or values
-    static constexpr int kStage = 2 * kPart + (I8 ? 128 : 0);      // and 16 + 16 scales
-    static constexpr int kStages = I8 ? (DP == 128 ? 5 : 8) : (DP == 128 ? 3 : 6);
+    static constexpr int kKeys = kRowBytes == 256 ? 16 : 32;       // of a warp's step
+    static constexpr int kPart = kKeys * kRowBytes;                // keys, or values, of a step
+    static constexpr int kStage = 2 * kPart + (I8 ? 8 * kKeys : 0);  // and their scales
+    static constexpr int kStages = I8 ? (DP == 128 ? 2 : 5) : 3;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRed = kWarps * 8 * DP * 4;               // sums of eight rows; between, the queries of several tiles
     static constexpr int kMl = kWarps * kRows * 8;
@@ -114,6 +118,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     constexpr int kRows = L::kRows;
     constexpr int ST = L::kStages;
     constexpr int KK = DP / 16;
+    constexpr int KEYS = L::kKeys, NT = KEYS / 8, KP = KEYS / 16;
+    constexpr int U = kWarps * KEYS;            // keys of a unit
     constexpr bool PBF = BF16 && !I8;           // type of the operands
     constexpr float kLift = PBF ? 0.f : 8.f;    // float16 weights in [0, 2^8]: the small ones keep their bits
     extern __shared__ __align__(128) uint8_t smem[];
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     grid_launch_dependents();
     grid_dependency_wait();
     struct Run {
-        Cursor<kRows> start;
+        Cursor<kRows, U> start;
         int64_t to, total;  // the unit after the run, units in all
         int runs;
         float back[kRows];  // see below
@@ -134,9 +140,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     static_assert(sizeof(Run) <= 384, "run");
     Run* run = reinterpret_cast<Run*>(smem + L::kRun);
     if (warp == 0) {
-        const Load work = measure<kRows>(a, gridDim.x);
+        const Load work = measure<kRows, U>(a, gridDim.x);
         int64_t from;
-        Cursor<kRows> k = run_start<kRows, false>(a, work, blockIdx.x, from);
+        Cursor<kRows, U> k = run_start<kRows, false, U>(a, work, blockIdx.x, from);
         if (lane == 0) {
             run->to = static_cast<int>(blockIdx.x) + 1 < work.runs ? share(work.total, blockIdx.x + 1, work.runs) : work.total;
             run->total = work.total;
@@ -146,18 +152,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         }
     }
     __syncthreads();
-    Cursor<kRows> now = run->start;
+    Cursor<kRows, U> now = run->start;
     if (now.left <= 0) return;
-    Cursor<kRows> ahead = now;
+    Cursor<kRows, U> ahead = now;
     Join join = {-1, 0, 0, 0, 0, 0};
 
-    // ---- copies: the place of key row (lane & 15) of the step `ahead` is at
+    // ---- copies: the place of key row lane % KEYS of the step `ahead` is at
     Lookup found = {0, -1};
     int head = 0;
     auto look = [&]() {
         if (ahead.left > 0) {
             head = ahead.h;
-            found = begin_lookup(a, ahead.s, ahead.u * kUnit + warp * 16 + (lane & 15), ahead.span.lo, ahead.span.hi);
+            found = begin_lookup(a, ahead.s, ahead.u * U + warp * KEYS + lane % KEYS, ahead.span.lo, ahead.span.hi);
         }
     };
     auto issue = [&](int slot) {
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         const int c = lane % L::kChunks;
         const int step = I8 ? 16 : 8;  // elements of a piece
 #pragma unroll
-        for (int i = 0; i < 16 / per; ++i) {
+        for (int i = 0; i < KEYS / per; ++i) {
             const int r = i * per + lane / L::kChunks;
             const uint32_t off = __shfl_sync(0xffffffffu, place, r);
             const bool on = off != kNoRow && c * step < a.dim;
@@ -177,9 +183,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
             cp_async16(base + L::kPart + L::v_at(r, c), a.v + at, on, a.q);
         }
         if constexpr (I8) {
-            const float* s = lane < 16 ? a.ks : a.vs;
-            cp_async4(base + 2 * L::kPart + 4 * lane, place != kNoRow ? s + splace : reinterpret_cast<const float*>(a.q),
-                      place != kNoRow ? 4u : 0u);
+            static_assert(KEYS == 32, "a lane for every key");
+            const bool on = place != kNoRow;
+            cp_async4(base + 2 * L::kPart + 4 * lane, on ? a.ks + splace : reinterpret_cast<const float*>(a.q), on ? 4u : 0u);
+            cp_async4(base + 2 * L::kPart + 4 * KEYS + 4 * lane, on ? a.vs + splace : reinterpret_cast<const float*>(a.q), on ? 4u : 0u);
         }
     };
     look();
@@ -285,11 +292,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         }
         cp_async_commit();
 
-        const int key0 = now.u * kUnit + warp * 16;
-        const Span& sp = now.span;
-        if (key0 < sp.hi && key0 + 15 >= sp.lo) {
+        const int key0 = now.u * U + warp * KEYS;
+        const Span<U>& sp = now.span;
+        if (key0 < sp.hi && key0 + KEYS - 1 >= sp.lo) {
             const uint32_t kb = ring + slot * L::kStage, vb = kb + L::kPart;
-            float s[MT][2][4] = {};
+            float s[MT][NT][4] = {};
             // queries of tile mt, step kk
             const auto queries = [&](int mt, int kk, uint32_t (&q)[4]) {
                 if constexpr (MT == 1) {
@@ -311,33 +318,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
                 for (int kk = 0; kk < KK; ++kk) {
-                    uint32_t b[4];
-                    ldsm4(kb + L::k_at(r, 2 * kk + c), b);
+                    uint32_t b[KP][4];
+#pragma unroll
+                    for (int h = 0; h < KP; ++h) ldsm4(kb + L::k_at(16 * h + r, 2 * kk + c), b[h]);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t q[4];
                         queries(mt, kk, q);
-                        mma16<BF16>(s[mt][0], q, b[0], b[1]);
-                        mma16<BF16>(s[mt][1], q, b[2], b[3]);
+#pragma unroll
+                        for (int h = 0; h < KP; ++h) {
+                            mma16<BF16>(s[mt][2 * h], q, b[h][0], b[h][1]);
+                            mma16<BF16>(s[mt][2 * h + 1], q, b[h][2], b[h][3]);
+                        }
                     }
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[mt][n][e] *= a.scale2;
             } else {
 #pragma unroll
                 for (int h = 0; h < KK / 4; ++h) {
-                    uint4 w[2];
+                    uint4 w[NT];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) w[n] = lds_v4(kb + L::k_at(8 * n + g, 4 * h + t));
+                    for (int n = 0; n < NT; ++n) w[n] = lds_v4(kb + L::k_at(8 * n + g, 4 * h + t));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t b[2][2];
+                        uint32_t b[NT][2];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
+                        for (int n = 0; n < NT; ++n) {
                             const uint32_t word = i == 0 ? w[n].x : i == 1 ? w[n].y : i == 2 ? w[n].z : w[n].w;
                             codes4(word, b[n][0], b[n][1]);
                         }
@@ -345,13 +356,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         for (int mt = 0; mt < MT; ++mt) {
                             uint32_t q[4];
                             queries(mt, 4 * h + i, q);
-                            mma16<false>(s[mt][0], q, b[0][0], b[0][1]);
-                            mma16<false>(s[mt][1], q, b[1][0], b[1][1]);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma16<false>(s[mt][n], q, b[n][0], b[n][1]);
                         }
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < NT; ++n) {
                     const uint2 sc = lds_v2(kb + 2 * L::kPart + 4 * (8 * n + 2 * t));
                     const float s0 = __uint_as_float(sc.x) * a.scale2, s1 = __uint_as_float(sc.y) * a.scale2;
 #pragma unroll
@@ -364,13 +375,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 }
             }
             // rows differ in what they see, or the step's keys end or begin in between
-            const bool cut = key0 + 15 > min(sp.p0, a.cap - 1) || (a.window && key0 < first_seen(a, sp.p1));
+            const bool cut = key0 + KEYS - 1 > min(sp.p0, a.cap - 1) || (a.window && key0 < first_seen(a, sp.p1));
             uint32_t hidden[MT] = {};  // bit 4n + e
             if (cut) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int key = key0 + 8 * n + 2 * t + (e & 1), x = e >> 1;
@@ -380,19 +391,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                             }
                         }
             }
-            float vs[2][2], lv[2][2];  // value scales of keys 8n + 2t + e, and their logarithms
+            float vs[NT][2], lv[NT][2];  // value scales of keys 8n + 2t + e, and their logarithms
             if constexpr (I8) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint2 sc = lds_v2(kb + 2 * L::kPart + 64 + 4 * (8 * n + 2 * t));
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 sc = lds_v2(kb + 2 * L::kPart + 4 * KEYS + 4 * (8 * n + 2 * t));
                     vs[n][0] = __uint_as_float(sc.x);
                     vs[n][1] = __uint_as_float(sc.y);
                     lv[n][0] = scale_log2(vs[n][0]);
                     lv[n][1] = scale_log2(vs[n][1]);
                 }
             }
-            uint32_t pa[MT][4];
-            float p[MT][2][4];
+            uint32_t pa[MT][KP][4];
+            float p[MT][NT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 float from[2];
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 for (int x = 0; x < 2; ++x) {
                     float m = top[mt][x];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) m = fmaxf(m, I8 ? s[mt][n][2 * x + e] + lv[n][e] : s[mt][n][2 * x + e]);
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -425,17 +436,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 }
                 const float ref[2] = {top[mt][0] == kNegInf ? 0.f : top[mt][0] - kLift, top[mt][1] == kNegInf ? 0.f : top[mt][1] - kLift};
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         p[mt][n][e] = ex2(s[mt][n][e] - ref[e >> 1]);
                         sum[mt][e >> 1] += p[mt][n][e];
                         if constexpr (I8) p[mt][n][e] = (hidden[mt] >> (4 * n + e)) & 1 ? 0.f : p[mt][n][e] * vs[n][e & 1];
                     }
-                pa[mt][0] = pack16<PBF>(p[mt][0][0], p[mt][0][1]);
-                pa[mt][1] = pack16<PBF>(p[mt][0][2], p[mt][0][3]);
-                pa[mt][2] = pack16<PBF>(p[mt][1][0], p[mt][1][1]);
-                pa[mt][3] = pack16<PBF>(p[mt][1][2], p[mt][1][3]);
+#pragma unroll
+                for (int h = 0; h < KP; ++h) {
+                    pa[mt][h][0] = pack16<PBF>(p[mt][2 * h][0], p[mt][2 * h][1]);
+                    pa[mt][h][1] = pack16<PBF>(p[mt][2 * h][2], p[mt][2 * h][3]);
+                    pa[mt][h][2] = pack16<PBF>(p[mt][2 * h + 1][0], p[mt][2 * h + 1][1]);
+                    pa[mt][h][3] = pack16<PBF>(p[mt][2 * h + 1][2], p[mt][2 * h + 1][3]);
+                }
             }
             if constexpr (!I8) {
                 // A value that only some of the rows see must not reach the others: 0 times an
@@ -445,24 +459,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 if (cut && sp.p0 != sp.p1) {
                     uint32_t high = 0;
 #pragma unroll
-                    for (int i = 0; i < L::kChunks / 2; ++i) high = top_exponents<BF16>(high, lds_v4(vb + 16 * (32 * i + lane)));
+                    for (int i = 0; i < L::kPart / 512; ++i) high = top_exponents<BF16>(high, lds_v4(vb + 16 * (32 * i + lane)));
                     odd = __any_sync(0xffffffffu, nonfinite<BF16>(high));
                 }
                 if (!odd) {
                     const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
 #pragma unroll
                     for (int j = 0; j < DP / 16; ++j) {
-                        uint32_t b[4];
-                        ldsm4_t(vb + L::v_at(r, 2 * j + c), b);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            mma16<BF16>(acc[mt][2 * j], pa[mt], b[0], b[1]);
-                            mma16<BF16>(acc[mt][2 * j + 1], pa[mt], b[2], b[3]);
+                        for (int h = 0; h < KP; ++h) {
+                            uint32_t b[4];
+                            ldsm4_t(vb + L::v_at(16 * h + r, 2 * j + c), b);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma16<BF16>(acc[mt][2 * j], pa[mt][h], b[0], b[1]);
+                                mma16<BF16>(acc[mt][2 * j + 1], pa[mt][h], b[2], b[3]);
+                            }
                         }
                     }
                 } else {
 #pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {
+                    for (int k = 0; k < KEYS; ++k) {
                         // p[row g + 8x][key k] is in lane 4g + (k % 8) / 2, entry [k / 8][2x + k % 2]
                         const int src = 4 * g + ((k & 7) >> 1);
                         float pk[MT][2];
@@ -470,8 +487,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const float mine = k < 8 ? ((k & 1) ? p[mt][0][2 * x + 1] : p[mt][0][2 * x]) : ((k & 1) ? p[mt][1][2 * x + 1] : p[mt][1][2 * x]);
-                                pk[mt][x] = __shfl_sync(0xffffffffu, mine, src);
+                                uint32_t mine = 0;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mine |= __float_as_uint((k & 1) ? p[mt][n][2 * x + 1] : p[mt][n][2 * x]) & (k >> 3 == n ? ~0u : 0u);
+                                pk[mt][x] = __uint_as_float(__shfl_sync(0xffffffffu, mine, src));
                             }
 #pragma unroll
                         for (int j = 0; j < DP / 8; ++j) {
@@ -493,18 +513,23 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 // column n of tile i of 32 elements jb: element 32 jb + 4 n + i
 #pragma unroll
                 for (int jb = 0; jb < DP / 32; ++jb) {
-                    uint32_t w[4];
+                    uint32_t w[KP][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-                        w[i] = lds_u32(vb + L::v_at(r, 2 * jb + (g >> 2)) + 4 * (g & 3));
-                    }
+                    for (int h = 0; h < KP; ++h)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 16 * h + 2 * t + (i & 1) + 8 * (i >> 1);
+                            w[h][i] = lds_u32(vb + L::v_at(r, 2 * jb + (g >> 2)) + 4 * (g & 3));
+                        }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t pick = 0x0400u + 0x0101u * i;  // byte i of the two keys, to bytes 0 and 2
-                        const uint32_t b0 = codes16<PBF>(prmt(w[0], w[1], pick)), b1 = codes16<PBF>(prmt(w[2], w[3], pick));
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) mma16<PBF>(acc[mt][4 * jb + i], pa[mt], b0, b1);
+                        for (int h = 0; h < KP; ++h) {
+                            const uint32_t b0 = codes16<PBF>(prmt(w[h][0], w[h][1], pick)), b1 = codes16<PBF>(prmt(w[h][2], w[h][3], pick));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) mma16<PBF>(acc[mt][4 * jb + i], pa[mt][h], b0, b1);
+                        }
                     }
                 }
             }

@@ -5,7 +5,7 @@
 // sequence's new tokens and its group of G query heads make new*G rows (row r:
 // token r / G, head r % G of the group), cut into tiles of R rows. An item is one
 // row tile of one key head of one sequence; its work is its span of keys in units
-// of kUnit keys, from the first key that any of its rows sees to the last (one
+// of 128 or 256 keys, from the first key that any of its rows sees to the last (one
 // unit where they see none, whose rows are then written as empty). The units of
 // all items, in order of sequence, key head, tile and key, are cut into as many
 // equal runs as there are CTAs: lengths of any mix keep every SM busy to the end,
@@ -30,7 +30,7 @@
 namespace qm {
 namespace attend {
 
-constexpr int kUnit = 128;      // keys of a unit of work
+constexpr int kUnit = 128;      // keys of a unit of work (attend_rows_kernel may take 256)
 constexpr int kTileRows = 256;  // rows of an item of attend_tiles_kernel
 
 struct Args {
@@ -96,16 +96,17 @@ QM_DEV int first_seen(const Args& a, int p) { return a.window && p >= a.window ?
 
 // The keys [lo, hi) that rows r0 .. r0 + R - 1 of a sequence see between them (hi
 // <= lo: none); p0 and p1: the first and last row's positions.
+template <int U>
 struct Span {
     int lo, hi, p0, p1, rows;
-    QM_DEV int u0() const { return hi > lo ? lo / kUnit : 0; }
-    QM_DEV int u1() const { return hi > lo ? (hi - 1) / kUnit + 1 : 1; }
+    QM_DEV int u0() const { return hi > lo ? lo / U : 0; }
+    QM_DEV int u1() const { return hi > lo ? (hi - 1) / U + 1 : 1; }
 };
 
-template <int R>
-QM_DEV Span tile_span(const Args& a, const Seq& s, unsigned tile) {
+template <int R, int U>
+QM_DEV Span<U> tile_span(const Args& a, const Seq& s, unsigned tile) {
     const unsigned r0 = tile * R, all = static_cast<unsigned>(s.fresh) * a.group;
-    Span t;
+    Span<U> t;
     t.rows = static_cast<int>(min(static_cast<unsigned>(R), all - r0));
     const int base = s.len - s.fresh;
     t.p0 = base + static_cast<int>(token_of(a, r0));
@@ -121,10 +122,10 @@ QM_DEV unsigned tiles_of(const Args& a, const Seq& s) {
 }
 
 // Units of tile `t` of a sequence; 0 past its last.
-template <int R>
+template <int R, int U>
 QM_DEV int tile_units(const Args& a, const Seq& s, unsigned t, unsigned tiles) {
     if (t >= tiles) return 0;
-    const Span p = tile_span<R>(a, s, t);
+    const Span<U> p = tile_span<R, U>(a, s, t);
     return p.u1() - p.u0();
 }
 
@@ -138,20 +139,20 @@ QM_DEV Seq shfl_seq(const Seq& s, int src) {
 
 // Units of one key head of each lane's sequence (0 for a lane without one). The
 // warp goes through the tiles of a sequence of many together.
-template <int R>
+template <int R, int U>
 QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine) {
     const int lane = threadIdx.x & 31;
     const unsigned tiles = mine ? tiles_of<R>(a, s) : 0;
     int64_t n = 0;
     constexpr unsigned kAlone = 12;
     if (tiles <= kAlone)
-        for (unsigned t = 0; t < tiles; ++t) n += tile_units<R>(a, s, t, tiles);
+        for (unsigned t = 0; t < tiles; ++t) n += tile_units<R, U>(a, s, t, tiles);
     for (unsigned many = __ballot_sync(0xffffffffu, tiles > kAlone); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq q = shfl_seq(s, src);
         const unsigned all = __shfl_sync(0xffffffffu, tiles, src);
         int64_t sum = 0;
-        for (unsigned t = lane; t < all; t += 32) sum += tile_units<R>(a, q, t, all);
+        for (unsigned t = lane; t < all; t += 32) sum += tile_units<R, U>(a, q, t, all);
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         if (lane == src) n = sum;
@@ -160,17 +161,17 @@ QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine) {
 }
 
 // A place in a CTA's run of units.
-template <int R>
+template <int R, int U = kUnit>
 struct Cursor {
     int64_t left;  // units of the run still to come, this one among them
     int s, h;
     unsigned tile, tiles;
     Seq seq;
-    Span span;
+    Span<U> span;
     int u, u1;
 
     QM_DEV void enter(const Args& a) {  // the item's first unit
-        span = tile_span<R>(a, seq, tile);
+        span = tile_span<R, U>(a, seq, tile);
         u = span.u0();
         u1 = span.u1();
     }
@@ -204,16 +205,16 @@ QM_DEV int64_t share(int64_t total, int c, int runs) {
 // The calling warp's cursor at unit g (every lane returns the same; left is not
 // set). seq and units: the lane's sequence and its units of one key head, of
 // sequences 0..31.
-template <int R>
-QM_DEV Cursor<R> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
+template <int R, int U>
+QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
     const int lane = threadIdx.x & 31;
-    Cursor<R> k = {};
+    Cursor<R, U> k = {};
     int64_t at = 0;  // units before sequence s0
     for (int s0 = 0; s0 < a.seqs; s0 += 32) {
         if (s0 > 0) {
             const bool mine = s0 + lane < a.seqs;
             if (mine) seq = load_seq(a, s0 + lane);
-            units = head_units<R>(a, seq, mine);
+            units = head_units<R, U>(a, seq, mine);
         }
         const int64_t n = units * a.kv_heads;
         int64_t upto = n;  // units up to and with this lane's sequence
@@ -235,7 +236,7 @@ QM_DEV Cursor<R> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
                                                         : static_cast<int>(rem / each);
             rem -= k.h * each;
             for (unsigned t0 = 0;; t0 += 32) {  // the tile that unit `rem` of the head is in
-                int sum = tile_units<R>(a, k.seq, t0 + lane, k.tiles);
+                int sum = tile_units<R, U>(a, k.seq, t0 + lane, k.tiles);
                 const int own = sum;
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
@@ -264,7 +265,7 @@ struct Load {
     Seq seq0;
     int runs;  // that have units
 };
-template <int R>
+template <int R, int U = kUnit>
 QM_DEV Load measure(const Args& a, int runs) {
     const int lane = threadIdx.x & 31;
     Load w = {};
@@ -272,7 +273,7 @@ QM_DEV Load measure(const Args& a, int runs) {
         Seq seq = {};
         const bool mine = s0 + lane < a.seqs;
         if (mine) seq = load_seq(a, s0 + lane);
-        int64_t n = head_units<R>(a, seq, mine);
+        int64_t n = head_units<R, U>(a, seq, mine);
         if (s0 == 0) {
             w.seq0 = seq;
             w.units0 = n;
@@ -293,13 +294,13 @@ QM_DEV Load measure(const Args& a, int runs) {
 // tiles and 5 of one of a single tile; whole items of s units leave the longest run of those that
 // should have L each with s where s > L, and with up to s more than L else.
 // Ragged chunks in a window 127 -> 87 us, 16 chunks of 512 90 -> 59.
-template <int R, bool WHOLE>
-QM_DEV Cursor<R> run_start(const Args& a, const Load& w, int c, int64_t& at) {
-    Cursor<R> k = {};
+template <int R, bool WHOLE, int U = kUnit>
+QM_DEV Cursor<R, U> run_start(const Args& a, const Load& w, int c, int64_t& at) {
+    Cursor<R, U> k = {};
     at = w.total;
     if (c >= w.runs) return k;
     at = share(w.total, c, w.runs);
-    k = locate<R>(a, at, w.seq0, w.units0);
+    k = locate<R, U>(a, at, w.seq0, w.units0);
     if constexpr (WHOLE) {
         const int64_t even = share(w.total, 1, w.runs);
         const int span = k.span.u1() - k.span.u0(), in = k.u - k.span.u0();
