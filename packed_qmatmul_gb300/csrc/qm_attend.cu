@@ -16,8 +16,7 @@
 // step ahead), so that warps wait for nothing but their own copies and an SM keeps
 // 64 to 139 KB in flight. A step is 16 keys of 256-byte rows and 32 of shorter ones: with 16 the
 // step's own latency and its fixed instructions (place, maxima, rescaling) are what bounds those (8-bit
-// codes, below; 32 x 2 tokens of 7 query heads of 64 over 8192 38.9 -> 32.5 us; ragged short
-// items lose a little to the coarser units: 32 x 5 tokens over 100 to 4000 31.4 -> 32.4). The products are m16n8k16 tensor-core instructions on 16
+// codes, below; 32 x 2 tokens of 7 query heads of 64 over 8192 38.9 -> 32.5 us). The products are m16n8k16 tensor-core instructions on 16
 // rows (rows that the item lacks are zeros: the tensor pipe has time to spare). At the
 // end of an item the warps' sums are added through shared memory in warp order while
 // the next item's copies are already under way. Up to 32 rows (48 of heads of 64
@@ -133,26 +132,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
     grid_dependency_wait();
     struct Run {
         Cursor<kRows, U> start;
-        int64_t to, total;  // the unit after the run, units in all
+        int64_t from, to, total;  // the run's first unit, the unit after it, units in all
         int runs;
         float back[kRows];  // see below
     };
     static_assert(sizeof(Run) <= 384, "run");
     Run* run = reinterpret_cast<Run*>(smem + L::kRun);
-    if (warp == 0) {
+    if (warp < 2) {  // the run's start and its end
         const Load work = measure<kRows, U>(a, gridDim.x);
-        int64_t from;
-        Cursor<kRows, U> k = run_start<kRows, false, U>(a, work, blockIdx.x, from);
-        if (lane == 0) {
-            run->to = static_cast<int>(blockIdx.x) + 1 < work.runs ? share(work.total, blockIdx.x + 1, work.runs) : work.total;
+        // Runs of one unit have one part each, and a join costs little more than a second unit;
+        // longer ones may have two, and write or join both. Against splitting everywhere: 32 x 5 tokens (7 query
+        // heads of 64 to a key head) over 100 to 4000 32.3 -> 27.9 us, over 1024 19.4 -> 15.1; 32 x 4
+        // (4 heads of 128) over 512 26.0 -> 21.9, over 1024 37.3 -> 33.3; one token over 256 7.4 -> 6.5.
+        // One token over 512 to 1024 loses 2 % to looking; left whole it would lose 20 to 60.
+        const Split split = {1024 / U, work.total <= gridDim.x ? 1 : U == 256 ? 3 : 2};
+        int64_t at;
+        const Cursor<kRows, U> k = run_start<kRows, U>(a, work, blockIdx.x + warp, split, split, at);
+        if (lane == 0 && warp == 0) {
+            run->from = at;
             run->total = work.total;
             run->runs = work.runs;
-            k.left = run->to - from;
             run->start = k;
         }
+        if (lane == 0 && warp == 1) run->to = at;
     }
     __syncthreads();
     Cursor<kRows, U> now = run->start;
+    now.left = run->to - run->from;
     if (now.left <= 0) return;
     Cursor<kRows, U> ahead = now;
     Join join = {-1, 0, 0, 0, 0, 0};

@@ -287,33 +287,37 @@ QM_DEV Load measure(const Args& a, int runs) {
     return w;
 }
 
+// The items that are not split: of up to `inside` units where runs are at least as long, else
+// of up to `beyond` more than a run.
+struct Split {
+    int inside, beyond;
+};
+
 // Where run `c` begins: unit `at`, and the cursor there (the calling warp's; every
-// lane returns the same, left is not set); the last one's end for c = runs. WHOLE: moved to an
-// end of the item it falls in where splitting that would cost more than uneven runs: a split's
-// parts (written and joined) cost about 8 units of an item of two
-// tiles and 5 of one of a single tile; whole items of s units leave the longest run of those that
-// should have L each with s where s > L, and with up to s more than L else.
-// Ragged chunks in a window 127 -> 87 us, 16 chunks of 512 90 -> 59.
-template <int R, bool WHOLE, int U = kUnit>
-QM_DEV Cursor<R, U> run_start(const Args& a, const Load& w, int c, int64_t& at) {
+// lane returns the same, left is not set); the last one's end for c = runs. Moved to an
+// end of the item it falls in where splitting that would cost more (its parts are written
+// and joined) than uneven runs: whole items of s units leave the longest of the runs that
+// should have L units each with s where s > L, and with up to s more than L else. An item's
+// span alone decides, so it is cut at all the runs' ends in it or at none. small and
+// large: for items of at most R / 2 rows and of more.
+template <int R, int U = kUnit>
+QM_DEV Cursor<R, U> run_start(const Args& a, const Load& w, int c, Split small, Split large, int64_t& at) {
     Cursor<R, U> k = {};
     at = w.total;
     if (c >= w.runs) return k;
     at = share(w.total, c, w.runs);
     k = locate<R, U>(a, at, w.seq0, w.units0);
-    if constexpr (WHOLE) {
-        const int64_t even = share(w.total, 1, w.runs);
-        const int span = k.span.u1() - k.span.u0(), in = k.u - k.span.u0();
-        const int cost = k.span.rows > R / 2 ? 8 : 5;
-        if (in > 0 && (span <= cost || (span > even && span <= even + cost))) {
-            if (2 * in < span) {
-                at -= in;
-                k.u = k.span.u0();
-            } else {
-                at += span - in;
-                k.left = 1;  // only so that next_item looks at what follows
-                if (at < w.total) k.next_item(a);
-            }
+    const int64_t even = share(w.total, 1, w.runs);
+    const int span = k.span.u1() - k.span.u0(), in = k.u - k.span.u0();
+    const Split cost = k.span.rows > R / 2 ? large : small;
+    if (in > 0 && (span <= even ? span <= cost.inside : span <= even + cost.beyond)) {
+        if (2 * in < span) {
+            at -= in;
+            k.u = k.span.u0();
+        } else {
+            at += span - in;
+            k.left = 1;  // only so that next_item looks at what follows
+            if (at < w.total) k.next_item(a);
         }
     }
     return k;
