@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
         // One token over 512 to 1024 loses 2 % to looking; left whole it would lose 20 to 60.
         const Split split = {1024 / U, work.total <= gridDim.x ? 1 : U == 256 ? 3 : 2};
         int64_t at;
-        const Cursor<kRows, U> k = run_start<kRows, U>(a, work, blockIdx.x + warp, split, split, at);
+        const Cursor<kRows, U> k = run_start<kRows, U>(a, work, blockIdx.x + warp, false, split, split, at);
         if (lane == 0 && warp == 0) {
             run->from = at;
             run->total = work.total;

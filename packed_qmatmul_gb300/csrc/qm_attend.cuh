@@ -137,22 +137,30 @@ QM_DEV Seq shfl_seq(const Seq& s, int src) {
     return o;
 }
 
-// Units of one key head of each lane's sequence (0 for a lane without one). The
-// warp goes through the tiles of a sequence of many together.
+// Units of one key head of each lane's sequence (0 for a lane without one); `most` grows
+// to those of the longest item seen. The warp goes through the tiles of a sequence of many together.
 template <int R, int U>
-QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine) {
+QM_DEV int64_t head_units(const Args& a, const Seq& s, bool mine, int& most) {
     const int lane = threadIdx.x & 31;
     const unsigned tiles = mine ? tiles_of<R>(a, s) : 0;
     int64_t n = 0;
     constexpr unsigned kAlone = 12;
     if (tiles <= kAlone)
-        for (unsigned t = 0; t < tiles; ++t) n += tile_units<R, U>(a, s, t, tiles);
+        for (unsigned t = 0; t < tiles; ++t) {
+            const int units = tile_units<R, U>(a, s, t, tiles);
+            n += units;
+            if constexpr (R == kTileRows) most = max(most, units);
+        }
     for (unsigned many = __ballot_sync(0xffffffffu, tiles > kAlone); many; many &= many - 1) {
         const int src = __ffs(many) - 1;
         const Seq q = shfl_seq(s, src);
         const unsigned all = __shfl_sync(0xffffffffu, tiles, src);
         int64_t sum = 0;
-        for (unsigned t = lane; t < all; t += 32) sum += tile_units<R, U>(a, q, t, all);
+        for (unsigned t = lane; t < all; t += 32) {
+            const int units = tile_units<R, U>(a, q, t, all);
+            sum += units;
+            if constexpr (R == kTileRows) most = max(most, units);
+        }
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         if (lane == src) n = sum;
@@ -204,9 +212,9 @@ QM_DEV int64_t share(int64_t total, int c, int runs) {
 
 // The calling warp's cursor at unit g (every lane returns the same; left is not
 // set). seq and units: the lane's sequence and its units of one key head, of
-// sequences 0..31.
+// sequences 0..31. each: g counts items, and units their row tiles.
 template <int R, int U>
-QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
+QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units, bool each) {
     const int lane = threadIdx.x & 31;
     Cursor<R, U> k = {};
     int64_t at = 0;  // units before sequence s0
@@ -214,7 +222,8 @@ QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
         if (s0 > 0) {
             const bool mine = s0 + lane < a.seqs;
             if (mine) seq = load_seq(a, s0 + lane);
-            units = head_units<R, U>(a, seq, mine);
+            int most = 0;
+            units = each ? (mine ? tiles_of<R>(a, seq) : 0) : head_units<R, U>(a, seq, mine, most);
         }
         const int64_t n = units * a.kv_heads;
         int64_t upto = n;  // units up to and with this lane's sequence
@@ -227,16 +236,17 @@ QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
         if (past) {
             const int src = __ffs(past) - 1;
             const int64_t before = at + __shfl_sync(0xffffffffu, upto - n, src);
-            const int64_t each = __shfl_sync(0xffffffffu, units, src);
+            const int64_t per_head = __shfl_sync(0xffffffffu, units, src);
             k.s = s0 + src;
             k.seq = shfl_seq(seq, src);
             k.tiles = tiles_of<R>(a, k.seq);
             int64_t rem = g - before;
-            k.h = (rem >> 31) == 0 && (each >> 31) == 0 ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(each))
-                                                        : static_cast<int>(rem / each);
-            rem -= k.h * each;
-            for (unsigned t0 = 0;; t0 += 32) {  // the tile that unit `rem` of the head is in
-                int sum = tile_units<R, U>(a, k.seq, t0 + lane, k.tiles);
+            k.h = (rem >> 31) == 0 && (per_head >> 31) == 0
+                      ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(per_head))
+                      : static_cast<int>(rem / per_head);
+            rem -= k.h * per_head;
+            for (unsigned t0 = 0; t0 < k.tiles; t0 += 32) {  // the tile that unit `rem` of the head is in
+                int sum = each ? t0 + lane < k.tiles : tile_units<R, U>(a, k.seq, t0 + lane, k.tiles);
                 const int own = sum;
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
@@ -253,6 +263,7 @@ QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
                 }
                 rem -= __shfl_sync(0xffffffffu, sum, 31);
             }
+            return k;  // not reached: the head's tiles have per_head units
         }
         at += __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -263,7 +274,10 @@ QM_DEV Cursor<R, U> locate(const Args& a, int64_t g, Seq seq, int64_t units) {
 struct Load {
     int64_t total, units0;
     Seq seq0;
-    int runs;  // that have units
+    int runs;   // that have units
+    // of attend_tiles_kernel:
+    int items;  // (2^16 stands for any more)
+    int most;   // units of the longest
 };
 template <int R, int U = kUnit>
 QM_DEV Load measure(const Args& a, int runs) {
@@ -273,7 +287,11 @@ QM_DEV Load measure(const Args& a, int runs) {
         Seq seq = {};
         const bool mine = s0 + lane < a.seqs;
         if (mine) seq = load_seq(a, s0 + lane);
-        int64_t n = head_units<R, U>(a, seq, mine);
+        int64_t n = head_units<R, U>(a, seq, mine, w.most);
+        if constexpr (R == kTileRows) {
+            const unsigned items = __reduce_add_sync(0xffffffffu, mine ? min(tiles_of<R>(a, seq), 1u << 16) : 0u);
+            w.items = min(w.items + static_cast<int>(min(items, 1u << 16)), 1 << 16);
+        }
         if (s0 == 0) {
             w.seq0 = seq;
             w.units0 = n;
@@ -281,6 +299,10 @@ QM_DEV Load measure(const Args& a, int runs) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(0xffffffffu, n, m);
         w.total += n;
+    }
+    if constexpr (R == kTileRows) {
+        w.most = __reduce_max_sync(0xffffffffu, w.most);
+        w.items = static_cast<int>(min(static_cast<int64_t>(w.items) * a.kv_heads, static_cast<int64_t>(1 << 16)));
     }
     w.total *= a.kv_heads;
     w.runs = w.total < runs ? static_cast<int>(w.total) : runs;  // the CTAs past the last unit have nothing
@@ -293,20 +315,27 @@ struct Split {
     int inside, beyond;
 };
 
+// Whether every item has a CTA to itself: there are enough of them, and no item is so long that splitting it
+// would be quicker (cost: what a split costs, in units).
+QM_DEV bool item_each(const Load& w, int runs, int cost) {
+    return w.items <= runs && w.most <= share(w.total, 1, w.runs) + cost;
+}
+
 // Where run `c` begins: unit `at`, and the cursor there (the calling warp's; every
 // lane returns the same, left is not set); the last one's end for c = runs. Moved to an
 // end of the item it falls in where splitting that would cost more (its parts are written
 // and joined) than uneven runs: whole items of s units leave the longest of the runs that
 // should have L units each with s where s > L, and with up to s more than L else. An item's
 // span alone decides, so it is cut at all the runs' ends in it or at none. small and
-// large: for items of at most R / 2 rows and of more.
+// large: for items of at most R / 2 rows and of more. each: run c is item c.
 template <int R, int U = kUnit>
-QM_DEV Cursor<R, U> run_start(const Args& a, const Load& w, int c, Split small, Split large, int64_t& at) {
+QM_DEV Cursor<R, U> run_start(const Args& a, const Load& w, int c, bool each, Split small, Split large, int64_t& at) {
     Cursor<R, U> k = {};
-    at = w.total;
-    if (c >= w.runs) return k;
-    at = share(w.total, c, w.runs);
-    k = locate<R, U>(a, at, w.seq0, w.units0);
+    at = each ? 0 : w.total;
+    if (c >= (each ? w.items : w.runs)) return k;
+    if (!each) at = share(w.total, c, w.runs);
+    k = locate<R, U>(a, each ? c : at, w.seq0, each ? tiles_of<R>(a, w.seq0) : w.units0, each);
+    if (each) return k;
     const int64_t even = share(w.total, 1, w.runs);
     const int span = k.span.u1() - k.span.u0(), in = k.u - k.span.u0();
     const Split cost = k.span.rows > R / 2 ? large : small;
