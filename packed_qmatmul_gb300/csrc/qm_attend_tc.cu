@@ -252,14 +252,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     static_assert(sizeof(Run) <= 8 * 96, "run");
     Run* run = reinterpret_cast<Run*>(smem + L::kCursors);
     if (warp < 2) {
-        // a split costs about 5 units of an item of one tile and 8 of one of two: ragged chunks
-        // in a window 127 -> 87 us, 16 chunks of 512 90 -> 59 against splitting everywhere. An item to each CTA, where
+        // a split costs some 9 units of an item of one tile and 14 of one of two: 16 chunks of 512 88 -> 54 us against
+        // splitting everywhere, 10 batches of 6 to 15 ragged chunks in a window of 2000 (16 / 4 heads of 96) 0.2 to 35 %
+        // less, the largest 222 -> 192 (220 with 5 and 8 units). An item to each CTA, where
         // there are enough, keeps runs from holding the ends of two: those chunks, 140 items of up to 17 units, 78 -> 49 us,
         // 144 items of 9 to 11 units 60 -> 34.
         const Load work = measure<kRows>(a, gridDim.x);
         int64_t at;
         const bool each = item_each(work, gridDim.x, 8);
-        const Cursor<kRows> k = run_start<kRows>(a, work, blockIdx.x + (each ? 0 : warp), each, Split{5, 5}, Split{8, 8}, at);
+        const Cursor<kRows> k = run_start<kRows>(a, work, blockIdx.x + (each ? 0 : warp), each, Split{9, 9}, Split{14, 14}, at);
         if (each) at = warp == 0 ? 0 : k.u1 - k.u;
         if (lane == 0) {
             if (warp == 0) {
