@@ -32,7 +32,7 @@
 // products' rate; of 4096 over 16384 365 us in pages of 64, 376 in pages of 16 or 20. A unit takes
 // 3300 clocks, 2048 of them products: a tile's scores wait 1700 for their weights, then
 // those 1500 for the products and the next scores, and the tiles' turns hide most but not all of it.
-// Over 8-bit codes 1172 us (4096 over 16384): the scales, broadcast from shared memory to every row,
+// Over 8-bit codes 1146 us (4096 over 16384): the scales, broadcast from shared memory to every row,
 // and the products share its bandwidth.
 #include <cuda.h>
 #include <cuda_runtime.h>
