@@ -398,6 +398,19 @@ def test_attend_split_over_many_ctas(new, length, heads, kv, codes):
     check_attend(P, q, out.cpu(), lse.cpu(), 0.1)
 
 
+@pytest.mark.parametrize("n,most,heads,kv", [(40, 90, 4, 1), (40, 90, 8, 4), (37, 5, 6, 2), (70, 1, 4, 2)])
+@pytest.mark.parametrize("codes", [False, True])
+def test_attend_more_sequences_than_a_warp_has_lanes(n, most, heads, kv, codes):
+    """An item to each CTA, items kept whole and items split, found past the 32nd sequence, idle ones between."""
+    g = gen(n + most + kv)
+    seqs = [(0 if i % 9 == 4 else 1 + (i * 37) % most, 100 + (i * 211) % 900) for i in range(n)]
+    P = Paged(g, seqs, kv, 64, 16, BF, codes)
+    q = randn(g, sum(new for new, _ in seqs), heads, 64, dtype=BF)
+    out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=0.125, lse=True)
+    qm.qm_device_status()
+    check_attend(P, q, out.cpu(), lse.cpu(), 0.125)
+
+
 @pytest.mark.parametrize("new,length", [(1, 40), (6, 200), (40, 200), (150, 400)])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_masked_values_never_reach_a_result(new, length, dtype):
