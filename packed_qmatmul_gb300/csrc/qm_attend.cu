@@ -682,12 +682,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     __shared__ float2 sm[G];
     grid_dependency_wait();
     const int c = blockIdx.x;
-    const int* d = a.desc + c * 8;
-    if (d[1] == 0) return;
+    const int last = last_part(a.desc, c, runs);
+    if (last < 0) return;
+    const int* d = a.desc + c * kDesc;
     const int first = d[2], h = d[3], r0 = d[4], rows = d[5], base = d[6];
     if (static_cast<int>(blockIdx.y) >= rows) return;
-    int last = c + 1;  // the CTA with the item's last part
-    while (last < runs && a.desc[last * 8] == 1) ++last;
     const int parts = last - c + 1;
     const int grp = threadIdx.x / C4, c4 = threadIdx.x % C4;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -742,13 +741,13 @@ unsigned long long next_call() {
     return next.fetch_add(0x9E3779B97F4A7C15ull, std::memory_order_relaxed) | 1ull;
 }
 
-// Workspace: [runs][8] int or [runs] flags, [runs][2][R] float2, [runs][2][R][DP] float.
+// Workspace: [runs][kDesc] int or [runs] flags, [runs][2][R] float2, [runs][2][R][DP] float.
 struct Ws {
     size_t ml, part, all;
 };
 Ws workspace_layout(int runs, int rows, int dp) {
     Ws w;
-    w.ml = (static_cast<size_t>(runs) * 32 + 255) / 256 * 256;
+    w.ml = (static_cast<size_t>(runs) * kDesc * 4 + 255) / 256 * 256;
     w.part = w.ml + (static_cast<size_t>(runs) * 2 * rows * 8 + 255) / 256 * 256;
     w.all = w.part + static_cast<size_t>(runs) * 2 * rows * dp * 4;
     return w;

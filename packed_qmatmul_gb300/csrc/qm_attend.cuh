@@ -24,6 +24,7 @@
 
 #include <climits>
 
+#include "qm_attend_parts.h"
 #include "qm_device.cuh"
 #include "qm_internal.h"
 
@@ -55,17 +56,12 @@ struct Args {
     int window;  // 0: none
     float scale2;  // scale * log2(e): scores are kept in powers of two
     // workspace
-    int* desc;     // [grid][8], see below (attend_tiles_kernel)
+    int* desc;     // [grid][kDesc] (attend_tiles_kernel)
     unsigned long long* done;  // [grid] (attend_rows_kernel): `call` once the CTA's part of an item that goes on is there
     unsigned long long call;   // marks this call
     float2* ml;    // [grid][2][R]: maximum and total of each row
     float* part;   // [grid][2][R][DP]
 };
-
-// desc[8] of a CTA: [0] its first part: 0 none, 1 neither end of its item, 2 its
-// item's last; [1] 1 if its last part begins an item that it does not finish
-// (slot 1), whose [2] first token, [3] key head, [4] first row, [5] rows and
-// [6] first row's position, [7] new tokens follow.
 
 QM_DEV uint32_t quotient(uint32_t n, uint32_t mul, int shift) { return mul ? __umulhi(n, mul) >> shift : n; }
 // The token (of its sequence's new ones) that a row belongs to.

@@ -244,6 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
 
     grid_launch_dependents();
     grid_dependency_wait();
+    // What the workspace held is no descriptor: one that is never published, by an empty run or one
+    // that a wait made give up, reads as a run without parts.
+    if (threadIdx.x < 2) a.desc[blockIdx.x * kDesc + threadIdx.x] = 0;
     // the run's start, its end, the barriers and the tensor memory, a warp each
     struct Run {
         Cursor<kRows> start;
@@ -300,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
     __syncthreads();  // the cursors of the warps that form weights lie there from here on
     const uint32_t tmem = *tmem_slot;
     if (start.left <= 0) {
-        if (threadIdx.x < 2) a.desc[blockIdx.x * 8 + threadIdx.x] = 0;
         if (warp == 8) tmem_dealloc(tmem, 512);
         return;
     }
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
         int nth = 0, parts = 0, checks = 0;  // units, parts and value checks of this tile so far
         uint32_t index = 0;      // units of the CTA so far
-        int first_part = 0;
+        int first_part = kNoPart;
         bool ok = true;
         static_assert(sizeof(Cursor<kRows>) <= 96, "cursor");
         Cursor<kRows>* now = reinterpret_cast<Cursor<kRows>*>(smem + L::kCursors + 96 * warp);
@@ -550,19 +552,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                 }
             }
             const bool starts = now->first(), ends = now->u + n == now->u1;
-            if (threadIdx.x == 0 && starts && !ends) {
-                int* d = a.desc + blockIdx.x * 8;
-                d[1] = 1;
-                d[2] = now->seq.first;
-                d[3] = now->h;
-                d[4] = static_cast<int>(now->tile * kRows);
-                d[5] = now->span.rows;
-                d[6] = now->seq.len - now->seq.fresh;
-            }
-            if (!starts) first_part = ends ? 2 : 1;
-            if (now->left == n && threadIdx.x == 0) {
-                a.desc[blockIdx.x * 8] = first_part;
-                if (!(starts && !ends)) a.desc[blockIdx.x * 8 + 1] = 0;
+            if (!starts) first_part = ends ? kLast : kInner;
+            if (threadIdx.x == 0 && now->left == n && ok) {  // the run's last part
+                int* desc = a.desc + blockIdx.x * kDesc;
+                desc[0] = first_part;
+                if (starts && !ends) {
+                    desc[1] = 1;
+                    desc[2] = now->seq.first;
+                    desc[3] = now->h;
+                    desc[4] = static_cast<int>(now->tile * kRows);
+                    desc[5] = now->span.rows;
+                    desc[6] = now->seq.len - now->seq.fresh;
+                }
             }
             index += n;
             Cursor<kRows> then = *now;
