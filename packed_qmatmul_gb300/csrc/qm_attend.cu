@@ -94,9 +94,15 @@ QM_DEV void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
 
 __device__ uint32_t g_err_rows = 0;
 
-QM_DEV void store_release(unsigned long long* p, unsigned long long v) {
-    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
+struct Flag {
+    unsigned long long* p;
+    QM_DEV unsigned long long swap(unsigned long long v) const {
+        unsigned long long old;
+        asm volatile("atom.acq_rel.gpu.global.exch.b64 %0, [%1], %2;" : "=l"(old) : "l"(p), "l"(v) : "memory");
+        return old;
+    }
+    QM_DEV void set(unsigned long long v) const { *reinterpret_cast<volatile unsigned long long*>(p) = v; }
+};
 QM_DEV unsigned long long load_acquire(const unsigned long long* p) {
     unsigned long long v;
     asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -614,39 +620,38 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 }
                 __syncthreads();
             }
-            if (!done) {
+            if (!done && ends) {  // the item's last part: the CTA joins the item when its run is done
                 const int64_t at = run->to - now.left;  // this unit
-                if (ends) {  // the item's last part: the CTA joins the item when its run is done
-                    const int64_t first_unit = at - (now.u - now.span.u0());
-                    const int owner = static_cast<int>(((first_unit + 1) * run->runs - 1) / run->total);  // the run that holds it
-                    join = Join{owner, now.seq.first, now.h, now.tile * kRows, rows, now.seq.len - now.seq.fresh};
-                } else {  // the run's last part, for a later CTA to join
-                    __threadfence();
-                    __syncthreads();
-                    if (threadIdx.x == 0) store_release(a.done + blockIdx.x, a.call);
-                }
+                const int64_t first_unit = at - (now.u - now.span.u0());
+                const int owner = static_cast<int>(((first_unit + 1) * run->runs - 1) / run->total);  // the run that holds it
+                join = Join{owner, now.seq.first, now.h, now.tile * kRows, rows, now.seq.len - now.seq.fresh};
             }
             begin = true;
         }
         now.step(a);
     }
     cp_async_wait<0>();
-    if (join.owner < 0) return;
+    const Flag own = {a.done + blockIdx.x};
+    unsigned long long before = 0;
+    if (now.u != now.u1) {  // the run's last part is for a later CTA to join
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) before = own.swap(a.call);
+    }
+    bool there = join.owner >= 0;
     // ---- the parts of the item that this CTA's first part ended: all but its own are
     // the last of the runs before, which end when this one does
     const int parts = static_cast<int>(blockIdx.x) - join.owner + 1;
-    bool there = true;
-    if (threadIdx.x < parts - 1) {
-        unsigned long long* flag = a.done + join.owner + threadIdx.x;
+    if (there && threadIdx.x < parts - 1) {
+        const Flag flag = {a.done + join.owner + threadIdx.x};
         const uint64_t t0 = globaltimer();
-        for (uint64_t round = 0; load_acquire(flag) != a.call; ++round)
-            if (globaltimer() - t0 > kWaitLimitNs || round > kWaitLimitNs) {
-                atomicOr(&g_err_rows, DEV_ERR_TIMEOUT);
-                there = false;
-                break;
-            }
-        *flag = 0;  // so that the next call, or this one's replay, starts over
+        uint64_t round = 0;
+        while (there && load_acquire(flag.p) != a.call)
+            there = globaltimer() - t0 <= kWaitLimitNs && ++round <= kWaitLimitNs;
+        if (there) flag.set(0);
+        else if (!(there = give_up(flag, a.call))) atomicOr(&g_err_rows, DEV_ERR_TIMEOUT);
     }
+    if (threadIdx.x == 0) take_back(own, before, a.call);
     if (!__syncthreads_and(there)) return;
     // groups of DP / 4 threads: as many rows at once as there are, the rest of the groups over the parts
     constexpr int C4 = DP / 4, G = kWarps * 32 / C4;

@@ -33,5 +33,21 @@ QM_BOTH int last_part(const int* desc, int c, int runs) {
     return -1;
 }
 
+// attend_rows_kernel: a CTA's flag is at the call's mark (odd) from when its part of an item that goes on
+// is there until the item's joiner has seen it. A captured call keeps its mark in every replay, so
+// no flag may stay at it when the kernel ends, whatever ended it: a joiner whose wait gave
+// up leaves the mark's complement, and the later of the two takes the flag back.
+// F: swap(v) exchanges the flag for v (acquire and release), set(v) stores it.
+template <class F>
+QM_BOTH void take_back(F f, unsigned long long before, unsigned long long mark) {  // by the part's CTA: `before` the mark
+    if (before == ~mark) f.set(0);
+}
+template <class F>
+QM_BOTH bool give_up(F f, unsigned long long mark) {  // by the joiner; true: the part came after all
+    if (f.swap(~mark) != mark) return false;
+    f.set(0);
+    return true;
+}
+
 }  // namespace attend
 }  // namespace qm

@@ -13,7 +13,18 @@ CSRC = os.path.join(ROOT, "packed_qmatmul_gb300", "csrc")
 
 SOURCE = r"""
 #include "qm_attend_parts.h"
-extern "C" int last_part(const int* desc, int c, int runs) { return qm::attend::last_part(desc, c, runs); }
+typedef unsigned long long u64;
+struct Word {
+    u64* p;
+    u64 swap(u64 v) const { u64 old = *p; *p = v; return old; }
+    void set(u64 v) const { *p = v; }
+};
+extern "C" {
+int last_part(const int* desc, int c, int runs) { return qm::attend::last_part(desc, c, runs); }
+u64 swap(u64* flag, u64 v) { return Word{flag}.swap(v); }
+void take_back(u64* flag, u64 before, u64 mark) { qm::attend::take_back(Word{flag}, before, mark); }
+int give_up(u64* flag, u64 mark) { return qm::attend::give_up(Word{flag}, mark); }
+}
 """
 
 
@@ -25,7 +36,12 @@ def parts(tmp_path_factory):
     (d / "parts.cpp").write_text(SOURCE)
     lib = str(d / "parts.so")
     subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-I", CSRC, "-o", lib, str(d / "parts.cpp")], check=True)
-    return ctypes.CDLL(lib)
+    lib = ctypes.CDLL(lib)
+    word, flag = ctypes.c_uint64, ctypes.POINTER(ctypes.c_uint64)
+    lib.swap.argtypes, lib.swap.restype = [flag, word], word
+    lib.take_back.argtypes, lib.take_back.restype = [flag, word, word], None
+    lib.give_up.argtypes, lib.give_up.restype = [flag, word], ctypes.c_int
+    return lib
 
 
 def last_part(parts, desc, c):
@@ -66,3 +82,56 @@ def test_no_descriptor_past_the_last_run_is_looked_at(parts):
     d[3:6, 0] = 1
     assert parts.last_part(d.ctypes.data_as(ctypes.c_void_p), 2, 6) == -1
     assert parts.last_part(d.ctypes.data_as(ctypes.c_void_p), 5, 6) == -1
+
+
+# ---------------------------------------------------------------- the flags of attend_rows_kernel
+MARK = 0x9E3779B97F4A7C15
+
+
+class Replay:
+    """One run of a captured call: a part's CTA and the item's joiner over one flag, each step an exchange or a store."""
+
+    def __init__(self, parts, flag):
+        self.parts, self.flag = parts, flag
+
+    def part_is_there(self):
+        before = self.parts.swap(ctypes.byref(self.flag), MARK)
+        self.parts.take_back(ctypes.byref(self.flag), before, MARK)
+
+    def seen(self):
+        return self.flag.value == MARK
+
+    def joined(self):
+        self.flag.value = 0
+
+    def gives_up(self):
+        return bool(self.parts.give_up(ctypes.byref(self.flag), MARK))
+
+
+@pytest.mark.parametrize("held", [0, 1, 12345, MARK ^ 2])  # what the workspace held
+def test_no_flag_stays_at_its_mark_whatever_ends_a_call(parts, held):
+    def replay():
+        r = Replay(parts, flag)
+        assert not r.seen()  # nothing of an earlier replay is taken for this one's
+        return r
+
+    def plain():
+        r = replay()
+        r.part_is_there()
+        assert r.seen()
+        r.joined()
+
+    flag = ctypes.c_uint64(held)
+    plain()
+    for late in (False, True):
+        r = replay()
+        if late:  # the joiner's wait gave up, then the part came
+            assert not r.gives_up()
+            assert not r.seen()
+            r.part_is_there()
+        else:  # it came between the joiner's last look and its giving up
+            r.part_is_there()
+            assert r.gives_up()
+        assert flag.value == 0
+        plain()
+        plain()

@@ -685,3 +685,17 @@ def test_strides_of_axes_of_one_do_not_count():
     (a,) = qm.head_norm_rope([odd], weights=[torch.ones(64, dtype=BF, device="cuda")])
     (b,) = qm.head_norm_rope([q.cuda()], weights=[torch.ones(64, dtype=BF, device="cuda")])
     assert torch.equal(a, b)
+
+
+def test_no_part_flag_stays_set():
+    """Items split between CTAs leave the workspace's flags (its first eight bytes a CTA) as a replay has to find them."""
+    g = gen(51)
+    P = Paged(g, [(1, 5000), (1, 700), (1, 3000)], 2, 128, 16, BF)
+    q = randn(g, 3, 4, 128, dtype=BF)
+    cache, batch = P.cache(), P.batch()
+    ws = torch.zeros(qm.qm_cache_attend_workspace(cache, batch, 4), dtype=torch.uint8, device="cuda")
+    flags = ws[: 8 * torch.cuda.get_device_properties(0).multi_processor_count]
+    for _ in range(3):
+        out = qm.cache_attend(cache, batch, q.cuda(), scale=0.1, workspace=ws)
+        assert not flags.any() and ws.any()
+        check_attend(P, q, out.cpu(), None, 0.1)
