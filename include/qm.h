@@ -358,7 +358,8 @@ size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, i
  * a token does not see never reach its results, whatever they hold. q's dtype is
  * the cache's, or either 16-bit type over QM_I8; out's is q's. Weights are rounded
  * to the cache's type before they meet values (over codes: with the value's scale, to
- * float16); in float16 one below 2^-22 of its row's largest loses bits, below 2^-33 all. Rows of no
+ * float16, or not at all beside a scale past 2^+-80); in float16 one below 2^-22 of its row's largest loses bits,
+ * below 2^-33 all. Scales may be of any size and sign. Rows of no
  * sequence are not written. out shares no element with q or the cache. The
  * results are the same bits in every run of the same arguments. */
 qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm_heads* q, const qm_heads* out,

@@ -32,9 +32,10 @@
 // are float16 whatever q's type: a code takes fewer instructions to become one than to become
 // bfloat16, bfloat16 queries fit after an exact power of two for each row, and scaled weights
 // have three bits more (the running maximum includes the values' scales, which
-// keeps them within [0, 2^8]). Instructions, not bytes, are what bounds it: 4 sequences
-// of 65 to 131 thousand tokens (32 / 8 heads) 179 us, 4.6 TB/s (205 in steps of 16 keys, 238 with keys also turned into
-// bfloat16); 16 x 2 tokens of 8 query heads to a key head over 8192 74 us (84, 93).
+// keeps them within 2^+-8; beside a scale past 2^+-80 the values' products are formed one by one in
+// float32). Instructions, not bytes, are what bounds it: 4 sequences
+// of 65 to 131 thousand tokens (32 / 8 heads) 174 us, 4.7 TB/s (205 in steps of 16 keys, 238 with keys also turned into
+// bfloat16); 16 x 2 tokens of 8 query heads to a key head over 8192 73 us (84, 93).
 //
 // Float16 weights, here and over a float16 cache: lifted by 2^8, a weight (times its value's scale)
 // keeps all its bits down to 2^-22 of the row's largest, fewer below, and none past 2^-33.
@@ -404,7 +405,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         }
             }
             float vs[NT][2], lv[NT][2];  // value scales of keys 8n + 2t + e, and their logarithms
+            bool far = false;            // a value scale is out of float16's reach
             if constexpr (I8) {
+                far = __any_sync(0xffffffffu, far_scale(__uint_as_float(lds_u32(kb + 2 * L::kPart + 4 * KEYS + 4 * lane))));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint2 sc = lds_v2(kb + 2 * L::kPart + 4 * KEYS + 4 * (8 * n + 2 * t));
@@ -519,6 +522,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                                         acc[mt][j][2 * x + 1] = fmaf(pk[mt][x], v1, acc[mt][j][2 * x + 1]);
                                     }
                         }
+                    }
+                }
+            } else if (far) {
+#pragma unroll 1
+                for (int k = 0; k < KEYS; ++k) {
+                    const int src = 4 * g + ((k & 7) >> 1);  // (as above for 16-bit values)
+                    float pk[MT][2];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t mine = 0;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mine |= __float_as_uint((k & 1) ? p[mt][n][2 * x + 1] : p[mt][n][2 * x]) & (k >> 3 == n ? ~0u : 0u);
+                            pk[mt][x] = __uint_as_float(__shfl_sync(0xffffffffu, mine, src));
+                        }
+#pragma unroll
+                    for (int jb = 0; jb < DP / 32; ++jb) {  // elements 32 jb + 8 t + 4 z + i
+                        const uint2 w = lds_v2(vb + L::v_at(k, 2 * jb + (t >> 1)) + 8 * (t & 1));
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float v = static_cast<float>(static_cast<int8_t>((z ? w.y : w.x) >> (8 * i)));
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) acc[mt][4 * jb + i][2 * x + z] = fmaf(pk[mt][x], v, acc[mt][4 * jb + i][2 * x + z]);
+                            }
                     }
                 }
             } else {

@@ -463,11 +463,21 @@ QM_DEV uint32_t to_f16x2(uint32_t pair, float by) {
     return pack_f16x2(__uint_as_float(pair << 16) * by, __uint_as_float(pair & 0xFFFF0000u) * by);
 }
 
-// log2 of a value scale, held within 2^+-30 (zero and NaN: the low end).
+// Value scales. A weight is 2^(s - m) times its value's scale, rounded to float16, and m the running maximum
+// of s + log2 |scale|: within [0, 2^12] with the kernels' lift and slack, and whole down to 2^-22 of the row's largest. The
+// logarithm is held within 2^+-80 (zero and NaN: the low end), so that the totals, sums of
+// 2^(s - m), stay in float32: at most 2^92 for a key, at least 2^-72 for the largest. A finite scale
+// beyond that is a far one: its products are formed one by one in float32, as a user will
+// hardly ever have them (2^80 is 10^24), and their range is float32's.
+constexpr int kFarLog2 = 80;
 QM_DEV float scale_log2(float s) {
     float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(s));
-    return fminf(fmaxf(y, -30.f), 30.f);
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(fabsf(s)));
+    return fminf(fmaxf(y, static_cast<float>(-kFarLog2)), static_cast<float>(kFarLog2));
+}
+QM_DEV bool far_scale(float s) {  // finite, not zero, and past 2^+-80
+    const uint32_t u = __float_as_uint(s) & 0x7FFFFFFFu, e = u >> 23;
+    return u != 0u && e != 255u && (e < 127u - kFarLog2 || e >= 127u + kFarLog2);
 }
 
 // Whether an infinity or NaN is among pairs of 16-bit values: the largest exponents

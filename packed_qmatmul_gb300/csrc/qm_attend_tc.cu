@@ -32,7 +32,7 @@
 // products' rate; of 4096 over 16384 365 us in pages of 64, 376 in pages of 16 or 20. A unit takes
 // 3300 clocks, 2048 of them products: a tile's scores wait 1700 for their weights, then
 // those 1500 for the products and the next scores, and the tiles' turns hide most but not all of it.
-// Over 8-bit codes 1146 us (4096 over 16384): the scales, broadcast from shared memory to every row,
+// Over 8-bit codes 1168 us (4096 over 16384): the scales, broadcast from shared memory to every row,
 // and the products share its bandwidth.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -60,7 +60,8 @@ struct Lay {
     static constexpr int kQ = 2 * kTile;
     static constexpr int kSlots = I8 ? 4 : DP == 128 ? 5 : 8;
     static constexpr int kScale = kQ + kSlots * kTile;  // [2][3][128] floats: key scales, value scales, their logarithms
-    static constexpr int kBars = kScale + (I8 ? 2 * 3 * 512 : 0);
+    static constexpr int kFar = kScale + 2 * 3 * 512;   // [2] ints: a value scale is out of float16's reach
+    static constexpr int kBars = kScale + (I8 ? 2 * 3 * 512 + 16 : 0);
     static constexpr int kCursors = kBars + 256;       // of the warps that form weights: they are out of registers
     static constexpr int kSmem = kCursors + 8 * 96;
 };
@@ -160,9 +161,9 @@ QM_DEV void quad_transpose(uint32_t (&w)[4][8]) {
 
 // O[row] += P[row] V over the unit's keys that the row sees, product by product:
 // for a unit in which rows see different keys and a value is infinite or NaN (0
-// times it would be NaN in rows that do not see it). p: the row's weights in tensor
-// memory (16-bit pairs), o: its sums, zeros instead if `fresh`; keys [a, b] are seen.
-template <int DP, bool BF16>
+// times it would be NaN in rows that do not see it). p: the row's weights in tensor memory
+// (16-bit pairs; WIDE: float32), o: its sums, zeros instead if `fresh`; keys [a, b] are seen.
+template <int DP, bool BF16, bool WIDE>
 __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, uint32_t v, int a, int b) {
 #pragma unroll 1
     for (int c = 0; c < DP / 32; ++c) {
@@ -174,14 +175,20 @@ __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, ui
         for (int i = 0; i < 32; ++i) acc[i] = fresh ? 0.f : __uint_as_float(r[i]);
 #pragma unroll 1
         for (int kb = 0; kb < 8; ++kb) {
-            uint32_t w[8];
-            tmem_ld8(p + 8 * kb, w);
+            uint32_t w[WIDE ? 16 : 8];
+            if constexpr (WIDE) tmem_ld16(p + 16 * kb, w);
+            else tmem_ld8(p + 8 * kb, w);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int key = 16 * kb + k;
-                const uint32_t h = (k & 1) ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
-                const float pk = BF16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+                float pk;
+                if constexpr (WIDE) {
+                    pk = __uint_as_float(w[k]);
+                } else {
+                    const uint32_t h = (k & 1) ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu;
+                    pk = BF16 ? __uint_as_float(h << 16) : f16_bits_to_f32(h);
+                }
                 const bool see = key >= a && key <= b;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -209,6 +216,53 @@ __device__ __noinline__ void exact_values(uint32_t p, uint32_t o, bool fresh, ui
         tmem_st16(o + 32 * c + 16, hi);
         tmem_wait_st();
     }
+}
+
+// A unit of codes with a far value scale: the row's scores in tensor memory become its weights in float32,
+// which meet the values the same way. sc: the unit's key scales, value scales and their logarithms; keys [a, b]
+// are seen. From and to the row's reference and total.
+template <int DP>
+__device__ __noinline__ float2 far_unit(uint32_t p, uint32_t o, bool fresh, uint32_t v, const float* sc, int a, int b, float ref, float total) {
+    const auto score = [&](int key, uint32_t raw) { return key >= a && key <= b ? __uint_as_float(raw) * sc[key] : -INFINITY; };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int kb = 0; kb < 8; ++kb) {
+        uint32_t w[16];
+        tmem_ld16(p + 16 * kb, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) top = fmaxf(top, score(16 * kb + k, w[k]) + sc[256 + 16 * kb + k]);
+    }
+    const float old = ref;
+    ref = fmaxf(ref, top - 8.f);  // the lift of float16 weights
+    const float base = ref == -INFINITY ? 0.f : ref, f = ex2(old - base);
+    total *= f;
+#pragma unroll 1
+    for (int c = 0; c < DP / 16 && !fresh; ++c) {
+        uint32_t r[16];
+        tmem_ld16(o + 16 * c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+        tmem_st16(o + 16 * c, r);
+    }
+#pragma unroll 1
+    for (int kb = 0; kb < 8; ++kb) {
+        uint32_t w[16];
+        tmem_ld16(p + 16 * kb, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int key = 16 * kb + k;
+            const float x = ex2(score(key, w[k]) - base);
+            total += x;
+            w[k] = key >= a && key <= b ? __float_as_uint(x * sc[128 + key]) : 0u;
+        }
+        tmem_st16(p + 16 * kb, w);
+    }
+    tmem_wait_st();
+    exact_values<DP, false, true>(p, o, fresh, v, a, b);
+    return make_float2(ref, total);
 }
 
 struct TileArgs {
@@ -345,134 +399,153 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                 // keys that every row of the item sees lie within [all_lo, all_hi]
                 const int all_hi = min(now->span.p0, a.cap - 1), all_lo = first_seen(a, now->span.p1);
                 const bool differ = now->span.p0 != now->span.p1;
-                for (int j = 0; j < n; ++j, ++nth) {
-                    const int key0 = (now->u + j) * kUnit;
-                    const bool cut = key0 + kUnit - 1 > all_hi || key0 < all_lo;
-                    const int sa = max(kmin - key0, 0), sb = min(kmax - key0, kUnit - 1);  // the unit's keys that the row sees
-                    const uint32_t vi = 2 * (index + j) + 1;  // the values' slot
-                    const int slot = vi % NS;
-                    const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
-                    // (only then is the unit's slot in turn: a tile that sat out an item runs ahead of the copies)
-                    if (!wait(s_full(t), nth & 1)) { ok = false; break; }
-                    bool odd = false;
-                    if constexpr (!I8) {
-                        // 0 times an infinity or NaN is NaN: where rows see different keys, a look at the
-                        // unit's values (each thread at one key's) tells whether the tensor cores may add them
-                        if (cut && differ) {
-                            if (!wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
-                            const uint32_t v = ring + slot * L::kTile;
-                            uint32_t high = 0;
+                int j = 0;
+                while (true) {
+                    for (; j < n; ++j, ++nth) {
+                        const int key0 = (now->u + j) * kUnit;
+                        const bool cut = key0 + kUnit - 1 > all_hi || key0 < all_lo;
+                        const int sa = max(kmin - key0, 0), sb = min(kmax - key0, kUnit - 1);  // the unit's keys that the row sees
+                        const uint32_t vi = 2 * (index + j) + 1;  // the values' slot
+                        const int slot = vi % NS;
+                        const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (I8 ? ((index + j) & 1) * 384 : 0);
+                        // (only then is the unit's slot in turn: a tile that sat out an item runs ahead of the copies)
+                        if (!wait(s_full(t), nth & 1)) { ok = false; break; }
+                        bool odd = false;
+                        if constexpr (!I8) {
+                            // 0 times an infinity or NaN is NaN: where rows see different keys, a look at the
+                            // unit's values (each thread at one key's) tells whether the tensor cores may add them
+                            if (cut && differ) {
+                                if (!wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                                const uint32_t v = ring + slot * L::kTile;
+                                uint32_t high = 0;
 #pragma unroll
-                            for (int c = 0; c < DP / 8; ++c)
-                                if (c < 2 * ksteps) high = top_exponents<BF16>(high, lds_v4(v + at16<DP>(row, c)));
-                            uint32_t* word = odd_word + 2 * (checks % 3) + t;
-                            // the next check's word, which every warp read two checks ago
-                            if (row == 0) odd_word[2 * ((checks + 1) % 3) + t] = 0;
-                            if (nonfinite<BF16>(high)) atomicOr(word, 1u);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(agreed(t));
-                            if (!wait(agreed(t), checks & 1)) { ok = false; break; }
-                            odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
-                            ++checks;
-                        }
-                    }
-                    if (I8 && !wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    uint32_t raw[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, raw[c]);
-                    tmem_wait_ld();
-                    float s[128];
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(raw[i / 32][i % 32]);
-                    if constexpr (I8) {
-#pragma unroll
-                        for (int i = 0; i < 128; i += 4) {
-                            const float4 k = *reinterpret_cast<const float4*>(sc + i);
-                            s[i] *= k.x; s[i + 1] *= k.y; s[i + 2] *= k.z; s[i + 3] *= k.w;
-                        }
-                    }
-                    if (cut) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {  // where the warp's rows all see 32 keys, nothing is compared
-                            if (__any_sync(0xffffffffu, sb < 32 * c + 31)) {
-#pragma unroll
-                                for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i <= sb ? s[i] : -INFINITY;
-                            }
-                            if (__any_sync(0xffffffffu, sa > 32 * c)) {
-#pragma unroll
-                                for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i >= sa ? s[i] : -INFINITY;
+                                for (int c = 0; c < DP / 8; ++c)
+                                    if (c < 2 * ksteps) high = top_exponents<BF16>(high, lds_v4(v + at16<DP>(row, c)));
+                                uint32_t* word = odd_word + 2 * (checks % 3) + t;
+                                // the next check's word, which every warp read two checks ago
+                                if (row == 0) odd_word[2 * ((checks + 1) % 3) + t] = 0;
+                                if (nonfinite<BF16>(high)) atomicOr(word, 1u);
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(agreed(t));
+                                if (!wait(agreed(t), checks & 1)) { ok = false; break; }
+                                odd = *reinterpret_cast<volatile uint32_t*>(word) != 0;
+                                ++checks;
                             }
                         }
-                    }
-                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if constexpr (I8) {
+                        if (I8 && !wait(kv_full(slot), (vi / NS) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        if (I8 && *reinterpret_cast<const volatile int*>(smem + L::kFar + 4 * ((index + j) & 1))) break;  // see below
+                        uint32_t raw[4][32];
 #pragma unroll
-                        for (int i = 0; i < 128; i += 4) {
-                            const float4 lv = *reinterpret_cast<const float4*>(sc + 256 + i);
-                            m[0] = fmaxf(m[0], s[i] + lv.x);
-                            m[1] = fmaxf(m[1], s[i + 1] + lv.y);
-                            m[2] = fmaxf(m[2], s[i + 2] + lv.z);
-                            m[3] = fmaxf(m[3], s[i + 3] + lv.w);
-                        }
-                    } else {
+                        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, raw[c]);
+                        tmem_wait_ld();
+                        float s[128];
 #pragma unroll
-                        for (int i = 0; i < 128; i += 8) {
+                        for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(raw[i / 32][i % 32]);
+                        if constexpr (I8) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + 4 + e]);
-                        }
-                    }
-                    // scores of 8-bit codes are in powers of two already (their key scales hold the factor)
-                    const float top = max3(max3(m[0], m[1], m[2]), m[3], m[3]) * (I8 ? 1.f : a.scale2) - kLift;
-                    if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-                        const float old = ref;
-                        ref = fmaxf(ref, top);
-                        const float f = ex2(old - (ref == -INFINITY ? 0.f : ref));
-                        total *= f;
-                        if (j > 0) {
-#pragma unroll 1
-                            for (int c = 0; c < DP / 16; ++c) {
-                                uint32_t r[16];
-                                tmem_ld16(to + 16 * c, r);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                                tmem_st16(to + 16 * c, r);
+                            for (int i = 0; i < 128; i += 4) {
+                                const float4 k = *reinterpret_cast<const float4*>(sc + i);
+                                s[i] *= k.x; s[i + 1] *= k.y; s[i + 2] *= k.z; s[i + 3] *= k.w;
                             }
                         }
-                    }
-                    const float base = ref == -INFINITY ? 0.f : ref;
-                    const float2 sc2 = I8 ? make_float2(1.f, 1.f) : make_float2(a.scale2, a.scale2), nb = make_float2(-base, -base);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        if (cut) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t w[16];
+                            for (int c = 0; c < 4; ++c) {  // where the warp's rows all see 32 keys, nothing is compared
+                                if (__any_sync(0xffffffffu, sb < 32 * c + 31)) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int k = 32 * c + 2 * i;
-                            const float2 x = fma2(make_float2(s[k], s[k + 1]), sc2, nb);
-                            float2 p = make_float2(ex2(x.x), ex2(x.y));
-                            sum[i & 1] = add2(sum[i & 1], p);
-                            if constexpr (I8) {
-                                p = mul2(p, *reinterpret_cast<const float2*>(sc + 128 + k));
-                                if (cut) {  // a scale that the row does not see may be infinite or NaN
-                                    if (k < sa || k > sb) p.x = 0.f;
-                                    if (k + 1 < sa || k + 1 > sb) p.y = 0.f;
+                                    for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i <= sb ? s[i] : -INFINITY;
+                                }
+                                if (__any_sync(0xffffffffu, sa > 32 * c)) {
+#pragma unroll
+                                    for (int i = 32 * c; i < 32 * c + 32; ++i) s[i] = i >= sa ? s[i] : -INFINITY;
                                 }
                             }
-                            w[i] = pack16<PBF>(p.x, p.y);
                         }
-                        tmem_st16(ts + 16 * c, w);
-                    }
-                    total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_wait_st();
-                    if constexpr (!I8) {
-                        if (odd) exact_values<DP, BF16>(ts, to, j == 0, ring + slot * L::kTile, sa, sb);
+                        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        if constexpr (I8) {
+#pragma unroll
+                            for (int i = 0; i < 128; i += 4) {
+                                const float4 lv = *reinterpret_cast<const float4*>(sc + 256 + i);
+                                m[0] = fmaxf(m[0], s[i] + lv.x);
+                                m[1] = fmaxf(m[1], s[i + 1] + lv.y);
+                                m[2] = fmaxf(m[2], s[i + 2] + lv.z);
+                                m[3] = fmaxf(m[3], s[i + 3] + lv.w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + 4 + e]);
+                            }
+                        }
+                        // scores of 8-bit codes are in powers of two already (their key scales hold the factor)
+                        const float top = max3(max3(m[0], m[1], m[2]), m[3], m[3]) * (I8 ? 1.f : a.scale2) - kLift;
+                        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+                            const float old = ref;
+                            ref = fmaxf(ref, top);
+                            const float f = ex2(old - (ref == -INFINITY ? 0.f : ref));
+                            total *= f;
+                            if (j > 0) {
+#pragma unroll 1
+                                for (int c = 0; c < DP / 16; ++c) {
+                                    uint32_t r[16];
+                                    tmem_ld16(to + 16 * c, r);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                                    tmem_st16(to + 16 * c, r);
+                                }
+                            }
+                        }
+                        const float base = ref == -INFINITY ? 0.f : ref;
+                        const float2 sc2 = I8 ? make_float2(1.f, 1.f) : make_float2(a.scale2, a.scale2), nb = make_float2(-base, -base);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = 32 * c + 2 * i;
+                                const float2 x = fma2(make_float2(s[k], s[k + 1]), sc2, nb);
+                                float2 p = make_float2(ex2(x.x), ex2(x.y));
+                                sum[i & 1] = add2(sum[i & 1], p);
+                                if constexpr (I8) {
+                                    p = mul2(p, *reinterpret_cast<const float2*>(sc + 128 + k));
+                                    if (cut) {  // a scale that the row does not see may be infinite or NaN
+                                        if (k < sa || k > sb) p.x = 0.f;
+                                        if (k + 1 < sa || k + 1 > sb) p.y = 0.f;
+                                    }
+                                }
+                                w[i] = pack16<PBF>(p.x, p.y);
+                            }
+                            tmem_st16(ts + 16 * c, w);
+                        }
+                        total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        tmem_wait_st();
+                        if constexpr (!I8) {
+                            if (odd) exact_values<DP, BF16, false>(ts, to, j == 0, ring + slot * L::kTile, sa, sb);
+                        }
                         if (row == 0) skip[t] = odd ? 1u : 0u;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full(t));
                     }
+                    if (!I8 || !ok || j == n) break;
+                    // a unit with a far value scale, out of the loop's way (within it, 1146 us of a chunk of 4096 over 16384
+                    // became 1220; so 1168)
+                    const int key0 = (now->u + j) * kUnit;
+                    const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + ((index + j) & 1) * 384;
+                    const float2 at = far_unit<DP>(ts, to, j == 0, ring + (2 * (index + j) + 1) % NS * L::kTile, sc, max(kmin - key0, 0),
+                                                   min(kmax - key0, kUnit - 1), ref, total);
+                    ref = at.x;
+                    total = at.y;
+                    if (row == 0) skip[t] = 1u;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(p_full(t));
+                    ++j;
+                    ++nth;
                 }
                 // ---- the part's end
                 const bool starts = now->first(), done_here = starts && now->u + n == now->u1;
@@ -835,15 +908,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                                     *reinterpret_cast<uint4*>(dst + (dst16[y] ^ 16u) + 32 * 128 * x) = make_uint4(o[4], o[5], o[6], o[7]);
                                 }
                             }
-                        if (v == 1 && lw == 0) {
+                        if (v == 1 && lw < 2) {  // a warp for the key scales, one for the values'
                             // the values two units back have been used, so their scales have been read
                             float* sc = reinterpret_cast<float*>(smem + L::kScale) + ((i >> 1) & 1) * 384;
+                            const float* from = lw ? a.vs : a.ks;
+                            float got[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const float ks = place[x] != kNoRow ? __ldg(a.ks + splace[x]) : 0.f, vs = place[x] != kNoRow ? __ldg(a.vs + splace[x]) : 0.f;
-                                sc[32 * x + lane] = ks * a.scale2;
-                                sc[128 + 32 * x + lane] = vs;
-                                sc[256 + 32 * x + lane] = scale_log2(vs);
+                            for (int x = 0; x < 4; ++x) got[x] = place[x] != kNoRow ? __ldg(from + splace[x]) : 0.f;
+                            if (lw == 0) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) sc[32 * x + lane] = got[x] * a.scale2;
+                            } else {
+                                bool far = false;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    sc[128 + 32 * x + lane] = got[x];
+                                    sc[256 + 32 * x + lane] = scale_log2(got[x]);
+                                    far |= far_scale(got[x]);
+                                }
+                                far = __any_sync(0xffffffffu, far);
+                                if (lane == 0) reinterpret_cast<int*>(smem + L::kFar)[(i >> 1) & 1] = far;
                             }
                         }
                         mbar_arrive(kv_full(slot));

@@ -699,3 +699,50 @@ def test_no_part_flag_stays_set():
         out = qm.cache_attend(cache, batch, q.cuda(), scale=0.1, workspace=ws)
         assert not flags.any() and ws.any()
         check_attend(P, q, out.cpu(), None, 0.1)
+
+
+def far_codes(g, seqs, kv, dim, page, kind):
+    """A cache of codes, none of them 0, with value scales of either sign and of any size."""
+    P = Paged(g, seqs, kv, dim, page, BF, codes=True)
+    for i, (_, n) in enumerate(seqs):
+        j = torch.arange(n)
+        p, r = P.table[i].long()[j // page], j % page
+        v = torch.randint(1, 128, (n, kv, dim), generator=g) * (torch.randint(0, 2, (n, kv, dim), generator=g) * 2 - 1)
+        vs = (torch.rand(n, kv, generator=g) * 0.03 + 0.003) * (torch.randint(0, 2, (n, kv), generator=g) * 2 - 1)
+        if kind == "any":
+            vs = vs.double() * 2.0 ** torch.randint(-110, 111, (n, kv), generator=g).double()
+        else:
+            vs = vs.double() * 2.0 ** kind
+        vs[torch.rand(n, kv, generator=g) < 0.05] = 0.0
+        P.v[p, :, r], P.vs[p, :, r] = v.to(torch.int8), vs.float()
+        P.vals[i] = v.double() * vs.float().double()[..., None]
+    return P
+
+
+@pytest.mark.parametrize("kind", [0, -115, -85, -78, -40, 40, 78, 85, 110, "any"])
+@pytest.mark.parametrize("new,length,heads,dim", [(1, 700, 4, 128), (5, 300, 8, 64), (5, 300, 6, 96), (70, 400, 4, 128), (200, 300, 2, 80), (1, 9000, 3, 128)])
+def test_value_scales_of_any_size_and_sign(new, length, heads, dim, kind):
+    """A code's scale is any finite float32: nothing overflows or vanishes on its way to a bfloat16 result."""
+    g = gen(41)
+    P = far_codes(g, [(new, length), (1, 40)], 1, dim, 16, kind)
+    q = randn(g, new + 1, heads, dim, dtype=BF)
+    out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=dim ** -0.5, lse=True)
+    qm.qm_device_status()
+    check_attend(P, q, out.cpu(), None, dim ** -0.5)
+    # the total is held against a maximum that counts the scales: the logarithm is a difference of two numbers of up to
+    # 80 more each in powers of two, rounded in float32
+    at = 0
+    for i, (n, length_) in enumerate(P.seqs):
+        _, wl, _, size = attend_def(q[at: at + n], P.keys[i], P.vals[i], n, length_, heads, dim ** -0.5, 0, P.width * P.page)
+        ds = size * (dim + 4) * 2.0 ** -23
+        assert ((lse[at: at + n].cpu() - wl).abs() <= ds + 2.0 ** -20 * (1 + wl.abs() + 80)).all()
+        at += n
+
+
+@pytest.mark.parametrize("new", [1, 5, 70])
+def test_negative_value_scales_in_float16(new):
+    g = gen(43)
+    P = far_codes(g, [(new, 300)], 2, 64, 32, 0)
+    q = randn(g, new, 4, 64, dtype=HF)
+    out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=0.125, lse=True)
+    check_attend(P, q, out.cpu(), lse.cpu(), 0.125)
