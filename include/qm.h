@@ -354,7 +354,7 @@ size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, i
  * on) below its sequence's length: out = sum_j w_j v_j, w = softmax over those j
  * of scale * (q . k_j) (scale > 0). lse (NULL or float32 [tokens, q->heads])
  * receives the natural logarithm of the sum of exp(scale * (q . k_j)). A token
- * that sees nothing gets zeros and -infinity; values and scores at positions that
+ * that sees nothing gets zeros and -infinity; one with a score of +infinity NaN and +infinity; values and scores at positions that
  * a token does not see never reach its results, whatever they hold. q's dtype is
  * the cache's, or either 16-bit type over QM_I8; out's is q's. Weights are rounded
  * to the cache's type before they meet values (over codes: with the value's scale, to

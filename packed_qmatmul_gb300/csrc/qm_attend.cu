@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     float f[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        f[x] = ex2(from[x] - (top[mt][x] == kNegInf ? 0.f : top[mt][x]));
+                        f[x] = ex2(from[x] - reference(top[mt][x]));
                         sum[mt][x] *= f[x];
                     }
 #pragma unroll
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                         acc[mt][j][2] *= f[1]; acc[mt][j][3] *= f[1];
                     }
                 }
-                const float ref[2] = {top[mt][0] == kNegInf ? 0.f : top[mt][0] - kLift, top[mt][1] == kNegInf ? 0.f : top[mt][1] - kLift};
+                const float ref[2] = {reference(top[mt][0]) - kLift, reference(top[mt][1]) - kLift};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                 float m = kNegInf;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kRows + g + 8 * x].x);
-                const float f = ex2(top[mt][y] - (m == kNegInf ? 0.f : m));
+                const float f = ex2(top[mt][y] - reference(m));
                 float* mine = red + (warp * 8 + g) * DP;
                 if constexpr (!I8) {
 #pragma unroll
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_rows_kernel(const __gri
                     float mm = kNegInf;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + row].x);
-                    const float mr = mm == kNegInf ? 0.f : mm;
+                    const float mr = reference(mm);
                     float total = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

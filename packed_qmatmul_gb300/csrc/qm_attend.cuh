@@ -22,6 +22,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <climits>
 
 #include "qm_attend_parts.h"
@@ -395,6 +396,10 @@ QM_DEV float ex2(float x) {
     return y;
 }
 
+// What exponents are taken against, given a running maximum: 0 where there is none yet, and for +infinity
+// the largest float32, so that the total becomes infinity, as its definition has it, and not infinity less infinity.
+QM_DEV float reference(float top) { return top == -INFINITY ? 0.f : fminf(top, FLT_MAX); }
+
 template <bool BF16>
 QM_DEV uint32_t pack16(float lo, float hi) {
     if constexpr (BF16) {
@@ -521,7 +526,7 @@ struct Sum4 {
     float m, total;
     float4 o;
     QM_DEV void add(float em, float et, const float4& v) {
-        const float mn = fmaxf(m, em), ref = mn == -INFINITY ? 0.f : mn;
+        const float mn = fmaxf(m, em), ref = reference(mn);
         const float f = ex2(m - ref), fe = ex2(em - ref);
         total = total * f + et * fe;
         o.x = o.x * f + v.x * fe; o.y = o.y * f + v.y * fe;

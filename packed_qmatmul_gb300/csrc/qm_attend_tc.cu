@@ -234,8 +234,8 @@ __device__ __noinline__ float2 far_unit(uint32_t p, uint32_t o, bool fresh, uint
         for (int k = 0; k < 16; ++k) top = fmaxf(top, score(16 * kb + k, w[k]) + sc[256 + 16 * kb + k]);
     }
     const float old = ref;
-    ref = fmaxf(ref, top - 8.f);  // the lift of float16 weights
-    const float base = ref == -INFINITY ? 0.f : ref, f = ex2(old - base);
+    ref = fminf(fmaxf(ref, top - 8.f), FLT_MAX);  // the lift of float16 weights
+    const float base = reference(ref), f = ex2(old - base);
     total *= f;
 #pragma unroll 1
     for (int c = 0; c < DP / 16 && !fresh; ++c) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
                         const float top = max3(max3(m[0], m[1], m[2]), m[3], m[3]) * (I8 ? 1.f : a.scale2) - kLift;
                         if (__any_sync(0xffffffffu, top > ref + kSlack)) {
                             const float old = ref;
-                            ref = fmaxf(ref, top);
+                            ref = fminf(fmaxf(ref, top), FLT_MAX);
                             const float f = ex2(old - (ref == -INFINITY ? 0.f : ref));
                             total *= f;
                             if (j > 0) {

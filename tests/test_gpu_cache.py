@@ -746,3 +746,38 @@ def test_negative_value_scales_in_float16(new):
     q = randn(g, new, 4, 64, dtype=HF)
     out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=0.125, lse=True)
     check_attend(P, q, out.cpu(), lse.cpu(), 0.125)
+
+
+@pytest.mark.parametrize("new,length", [(1, 200), (1, 9000), (5, 300), (60, 400), (300, 3000)])
+@pytest.mark.parametrize("dtype,codes", [(BF, False), (HF, False), (BF, True), (HF, True)])
+def test_a_score_of_infinity(new, length, dtype, codes):
+    """The log-sum-exp of a row with a score of +infinity is +infinity, of one with a NaN among its scores NaN; the weights are
+    the definition's infinity less infinity either way."""
+    g = gen(47)
+    P = Paged(g, [(new, length), (2, 50)], 1, 64, 16, dtype, codes)
+
+    def put(pos, what):  # the key at a position of sequence 0 (codes: its scale), and the definition's
+        p, r = int(P.table[0, pos // 16]), pos % 16
+        if codes:
+            P.k[p, 0, r] = P.k[p, 0, r].abs().clamp(min=1)
+            P.ks[p, 0, r] = what
+            P.keys[0][pos, 0] = P.k[p, 0, r].double() * what
+        else:
+            P.k[p, 0, r, 7] = what
+            P.keys[0][pos, 0, 7] = what
+
+    put(length // 3, math.inf)
+    put(length // 3 + 5, -math.inf)
+    if new > 4:
+        put(length - 2, math.nan)  # the last two tokens see this one too
+    q = randn(g, new + 2, 3, 64, dtype=dtype).abs()  # so that an infinity's sign is its score's
+    q[:, 2] = -q[:, 2]
+    out, lse = qm.cache_attend(P.cache(), P.batch(), q.cuda(), scale=0.125, lse=True)
+    qm.qm_device_status()
+    out, lse = out.cpu(), lse.cpu()
+    seen = new - 2 if new > 4 else new  # rows that see no NaN
+    if new <= length - length // 3 - 6:  # every row sees both infinities
+        assert torch.isposinf(lse[:seen]).all()
+        assert torch.isnan(out[:new]).all() and torch.isnan(lse[seen:new]).all()
+    assert torch.isfinite(lse[new:]).all()
+    check_attend(P, q, out, None, 0.125)
