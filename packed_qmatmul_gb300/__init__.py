@@ -288,6 +288,20 @@ def _heads_and_like(x: torch.Tensor, tokens: int, dim: int, name: str):
     return _HEADS(x.data_ptr(), ts, hs, heads, code), y, _HEADS(y.data_ptr(), row, dim, heads, code)
 
 
+def _one_gpu(gpus: Sequence[Optional[int]], names: Sequence[str]):
+    """Refuses a call whose tensors are not on one GPU, where a kernel would read a host tensor's address as its
+    own. gpus: each part's get_device(), None for a part that the call goes without."""
+    gpu = gpus[0]
+    if gpu < 0 or gpus.count(gpu) + gpus.count(None) != len(gpus):
+        for g, name in zip(gpus, names):
+            if g is not None and (g < 0 or g != gpu):
+                _refuse(f"{name}: {'not on a GPU' if g < 0 else 'on another GPU than ' + names[0]}")
+
+
+def _gpu(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.get_device()
+
+
 def _i32(t: torch.Tensor, name: str) -> int:
     if t.dtype != torch.int32:
         _refuse(f"{name}: must be int32")
@@ -306,6 +320,7 @@ class Rope:
             _refuse('rope: style must be "half" or "pairs"')
         self.table, self.style = table, style
         self.dim = table.shape[1]
+        self.gpu = table.get_device()
         self._c = _ROPE(_ptr(table), table.shape[0], self.dim, QM_ROPE_HALF if style == "half" else QM_ROPE_PAIRS)
 
 
@@ -332,6 +347,9 @@ class Cache:
             if any(s.dtype != torch.float32 or s.shape != k.shape[:3] for s in scales) or k_scales.stride() != v_scales.stride():
                 _refuse("k_scales: scales must be float32 [pages, heads, page_size] of the same strides")
             sst = k_scales.stride()
+        self.gpu = k.get_device()
+        if any(s is not None and s.get_device() != self.gpu for s in (v, *scales)):
+            _refuse("cache: its tensors must be on one device")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.pages, self.heads, self.page_size, self.dim = k.shape
         self._need = {}
@@ -355,6 +373,9 @@ class Batch:
             _refuse("q_offsets: must be [seqs + 1]")
         if page_table.dtype != torch.int32 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
             _refuse("page_table: must be int32 with contiguous rows")
+        self.gpu = lens.get_device()
+        if page_table.get_device() != self.gpu or (q_offsets is not None and q_offsets.get_device() != self.gpu):
+            _refuse("batch: its tensors must be on one device")
         self.lens, self.page_table, self.q_offsets = lens, page_table, q_offsets
         self.seqs, self.tokens, self.max_new = seqs, seqs if tokens is None else int(tokens), int(max_new)
         self._c = _BATCH(_i32(lens, "lens"), page_table.data_ptr(), 0 if q_offsets is None else _i32(q_offsets, "q_offsets"),
@@ -499,6 +520,17 @@ def _norm_rope(xs, outs, positions, rope, weights, eps, stream) -> list:
         if ptype is None or positions.shape != (T,):
             _refuse("positions: must be int32 or int64 [tokens]")
         pos = _ptr(positions)
+    gpus = [x.get_device() for x in xs]
+    if outs is not None:
+        gpus += [y.get_device() for y in outs]
+    if weights is not None:
+        gpus += [None if w is None else w.get_device() for w in weights]
+    if positions is not None:
+        gpus.append(positions.get_device())
+    if rope is not None:
+        gpus.append(rope.gpu)
+    if gpus[0] < 0 or gpus.count(gpus[0]) != len(gpus):
+        _one_gpu(gpus, ["x"] * n + ["out"] * (n if outs else 0) + ["weights"] * (n if weights else 0) + ["positions"] * (positions is not None) + ["rope"])
     _check(load_library().qm_head_norm_rope(b"".join(xd), b"".join(od), warr, n, T, D, eps, None if rope is None else rope._c,
                                             pos, ptype, _stream(stream)))
     return made
@@ -515,10 +547,10 @@ def qm_cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor
                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
     if k_weight is not None and (k_weight.shape != (cache.dim,) or k_weight.dtype != k.dtype):
         _refuse("k_weight: must be [dim] of k's dtype")
-    _check(load_library().qm_cache_append(
-        cache._c, batch._c, _heads(k, batch.tokens, cache.heads, cache.dim, "k"),
-        _heads(v, batch.tokens, cache.heads, cache.dim, "v"), _ptr(k_weight), eps, None if rope is None else rope._c,
-        _stream(stream)))
+    kd, vd = _heads(k, batch.tokens, cache.heads, cache.dim, "k"), _heads(v, batch.tokens, cache.heads, cache.dim, "v")
+    _one_gpu((cache.gpu, batch.gpu, k.get_device(), v.get_device(), _gpu(k_weight), None if rope is None else rope.gpu),
+             ("cache", "batch", "k", "v", "k_weight", "rope"))
+    _check(load_library().qm_cache_append(cache._c, batch._c, kd, vd, _ptr(k_weight), eps, None if rope is None else rope._c, _stream(stream)))
 
 
 def qm_cache_attend_workspace(cache: Cache, batch: Batch, heads: int) -> int:
@@ -539,9 +571,11 @@ def qm_cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, out: torch.Tens
     T, H = batch.tokens, q.shape[1]
     if lse is not None and (lse.shape != (T, H) or lse.dtype != torch.float32):
         _refuse("lse: must be float32 [tokens, heads]")
+    qd, od = _heads(q, T, H, cache.dim, "q"), _heads(out, T, H, cache.dim, "out")
+    _one_gpu((cache.gpu, batch.gpu, q.get_device(), out.get_device(), _gpu(lse), _gpu(workspace)),
+             ("cache", "batch", "q", "out", "lse", "workspace"))
     _check(load_library().qm_cache_attend(
-        cache._c, batch._c, _heads(q, T, H, cache.dim, "q"), _heads(out, T, H, cache.dim, "out"), _ptr(lse), scale, window,
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+        cache._c, batch._c, qd, od, _ptr(lse), scale, window, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def qm_check_wait_timeout(limit_ns: int, stream=None) -> None:
@@ -638,6 +672,7 @@ def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[fl
     the scores' log-sum-exp [tokens, heads])."""
     with _on(stream):
         qd, out, od = _heads_and_like(q, batch.tokens, cache.dim, "q")
+        _one_gpu((cache.gpu, batch.gpu, q.get_device(), _gpu(workspace)), ("cache", "batch", "q", "workspace"))
         heads = q.shape[1]
         total = torch.empty((batch.tokens, heads), dtype=torch.float32, device=q.device) if lse else None
         if workspace is None:

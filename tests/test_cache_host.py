@@ -141,3 +141,62 @@ def test_binding_refusals():
         with pytest.raises(qm.QMError) as e:
             f()
         assert e.value.status == qm.QM_EINVAL
+
+
+class Elsewhere:
+    """A tensor that says it is on another device."""
+
+    def __init__(self, t, gpu):
+        self.t, self.gpu = t, gpu
+
+    def get_device(self):
+        return self.gpu
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("gpu,why", [(-1, "not on a GPU"), (1, "on another GPU than")])
+def test_every_tensor_of_a_call_is_on_one_gpu(gpu, why):
+    """A tensor of the host, or of another GPU, is refused by name before the library is called."""
+    def on(t, here=0):
+        return Elsewhere(t, here)
+
+    bf = torch.bfloat16
+    x, w = torch.zeros(2, 2, 64, dtype=bf), torch.zeros(64, dtype=bf)
+    k, lens, table = torch.zeros(3, 2, 16, 64, dtype=bf), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
+    ws, lse, pos, turns = torch.zeros(8, dtype=torch.uint8), torch.zeros(2, 2), torch.zeros(2, dtype=torch.int32), torch.zeros(4, 64)
+
+    def cache(at=0):
+        return qm.Cache(on(k, at), on(k, at))
+
+    def batch(at=0):
+        return qm.Batch(on(lens, at), on(table, at))
+
+    def rope(at=0):
+        return qm.Rope(on(turns, at))
+
+    calls = [
+        ("x", lambda: qm.qm_head_norm_rope([on(x), on(x, gpu)], [on(x), on(x)])), ("out", lambda: qm.qm_head_norm_rope([on(x)], [on(x, gpu)])),
+        ("weights", lambda: qm.qm_head_norm_rope([on(x), on(x)], [on(x), on(x)], weights=[None, on(w, gpu)])),
+        ("positions", lambda: qm.qm_head_norm_rope([on(x)], [on(x)], on(pos, gpu), rope())),
+        ("rope", lambda: qm.qm_head_norm_rope([on(x)], [on(x)], on(pos), rope(gpu))),
+        ("batch", lambda: qm.cache_append(cache(), batch(gpu), on(x), on(x))), ("k", lambda: qm.cache_append(cache(), batch(), on(x, gpu), on(x))),
+        ("v", lambda: qm.cache_append(cache(), batch(), on(x), on(x, gpu))), ("rope", lambda: qm.cache_append(cache(), batch(), on(x), on(x), rope(gpu))),
+        ("k_weight", lambda: qm.cache_append(cache(), batch(), on(x), on(x), rope(), on(w, gpu))),
+        ("batch", lambda: qm.qm_cache_attend(cache(), batch(gpu), on(x), on(x), 1.0, on(ws))),
+        ("q", lambda: qm.qm_cache_attend(cache(), batch(), on(x, gpu), on(x), 1.0, on(ws))),
+        ("out", lambda: qm.qm_cache_attend(cache(), batch(), on(x), on(x, gpu), 1.0, on(ws))),
+        ("lse", lambda: qm.qm_cache_attend(cache(), batch(), on(x), on(x), 1.0, on(ws), lse=on(lse, gpu))),
+        ("workspace", lambda: qm.qm_cache_attend(cache(), batch(), on(x), on(x), 1.0, on(ws, gpu))),
+    ]
+    if gpu < 0:  # and where everything is on the host
+        calls += [("cache", lambda: qm.cache_append(qm.Cache(k, k), qm.Batch(lens, table), x, x)), ("x", lambda: qm.head_norm_rope([x])),
+                  ("cache", lambda: qm.cache_attend(qm.Cache(k, k), qm.Batch(lens, table), x))]
+    for part, call in calls:
+        with pytest.raises(qm.QMError, match=f"QM_EINVAL: {part}: {why}"):
+            call()
+    for make in (lambda: qm.Cache(on(k), on(k, gpu)), lambda: qm.Batch(on(lens), on(table, gpu)), lambda: qm.Batch(on(lens, gpu), on(table)),
+                 lambda: qm.Batch(on(lens), on(table), on(torch.zeros(3, dtype=torch.int32), gpu))):
+        with pytest.raises(qm.QMError, match="must be on one device"):
+            make()
