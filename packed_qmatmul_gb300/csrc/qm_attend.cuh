@@ -201,12 +201,6 @@ struct Cursor {
     }
 };
 
-// total * c / runs, in 32 bits where they hold it.
-QM_DEV int64_t share(int64_t total, int c, int runs) {
-    if (total < (1 << 22) && c < 1024) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(runs);
-    return total * c / runs;
-}
-
 // The calling warp's cursor at unit g (every lane returns the same; left is not
 // set). seq and units: the lane's sequence and its units of one key head, of
 // sequences 0..31. each: g counts items, and units their row tiles.
@@ -311,12 +305,6 @@ QM_DEV Load measure(const Args& a, int runs) {
 struct Split {
     int inside, beyond;
 };
-
-// Whether every item has a CTA to itself: there are enough of them, and no item is so long that splitting it
-// would be quicker (cost: what a split costs, in units).
-QM_DEV bool item_each(const Load& w, int runs, int cost) {
-    return w.items <= runs && w.most <= share(w.total, 1, w.runs) + cost;
-}
 
 // Where run `c` begins: unit `at`, and the cursor there (the calling warp's; every
 // lane returns the same, left is not set); the last one's end for c = runs. Moved to an

@@ -1,6 +1,9 @@
-// qm_attend_parts.h -- how the CTAs that share an item of cache_attend tell of its
-// parts. Plain C++, so that a test on the host compiles it as it stands.
+// qm_attend_parts.h -- of cache_attend's cut into runs what needs no warp: shares of the
+// units, and how the CTAs that share an item tell of its parts. Plain C++, so that a test
+// on the host compiles it as it stands.
 #pragma once
+
+#include <stdint.h>
 
 #ifdef __CUDACC__
 #define QM_BOTH __host__ __device__ __forceinline__
@@ -10,6 +13,19 @@
 
 namespace qm {
 namespace attend {
+
+// total * c / runs, in 32 bits where they hold it.
+QM_BOTH int64_t share(int64_t total, int c, int runs) {
+    if (total < (1 << 22) && c < 1024) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(runs);
+    return total * c / runs;
+}
+
+// Whether every item has a CTA to itself: there are enough of them, and no item is so long that splitting it
+// would be quicker (cost: what a split costs, in units). items: how many, the longest of `most` units; `total`
+// units on `used` of `runs` CTAs (none where no sequence has rows).
+QM_BOTH bool item_each(int items, int most, int64_t total, int used, int runs, int cost) {
+    return used > 0 && items <= runs && most <= share(total, 1, used) + cost;
+}
 
 // attend_tiles_kernel, for attend_join_kernel: eight ints of each CTA. [0] its first part; [1] 1 if
 // its last part begins an item that it does not finish, whose [2] first token, [3] key

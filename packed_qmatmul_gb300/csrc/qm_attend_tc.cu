@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const __grid_
         // 144 items of 9 to 11 units 60 -> 34.
         const Load work = measure<kRows>(a, gridDim.x);
         int64_t at;
-        const bool each = item_each(work, gridDim.x, 8);
+        const bool each = item_each(work.items, work.most, work.total, work.runs, gridDim.x, 8);
         const Cursor<kRows> k = run_start<kRows>(a, work, blockIdx.x + (each ? 0 : warp), each, Split{9, 9}, Split{14, 14}, at);
         if (each) at = warp == 0 ? 0 : k.u1 - k.u;
         if (lane == 0) {

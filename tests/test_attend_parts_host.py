@@ -23,6 +23,7 @@ extern "C" {
 int last_part(const int* desc, int c, int runs) { return qm::attend::last_part(desc, c, runs); }
 u64 swap(u64* flag, u64 v) { return Word{flag}.swap(v); }
 void take_back(u64* flag, u64 before, u64 mark) { qm::attend::take_back(Word{flag}, before, mark); }
+int item_each(int items, int most, int64_t total, int used, int runs, int cost) { return qm::attend::item_each(items, most, total, used, runs, cost); }
 int give_up(u64* flag, u64 mark) { return qm::attend::give_up(Word{flag}, mark); }
 }
 """
@@ -42,6 +43,15 @@ def parts(tmp_path_factory):
     lib.take_back.argtypes, lib.take_back.restype = [flag, word, word], None
     lib.give_up.argtypes, lib.give_up.restype = [flag, word], ctypes.c_int
     return lib
+
+
+def test_an_item_to_each_cta(parts):
+    def each(items, most, total, runs=152):
+        return bool(parts.item_each(items, most, ctypes.c_int64(total), min(runs, total), runs, 8))
+
+    assert each(152, 9, 152) and not each(153, 9, 153)
+    assert each(10, 18, 1520) and not each(10, 19, 1520)
+    assert not each(0, 0, 0)  # no sequence has rows: no run to take a share of
 
 
 def last_part(parts, desc, c):
