@@ -781,3 +781,54 @@ def test_a_score_of_infinity(new, length, dtype, codes):
         assert torch.isnan(out[:new]).all() and torch.isnan(lse[seen:new]).all()
     assert torch.isfinite(lse[new:]).all()
     check_attend(P, q, out, None, 0.125)
+
+
+@pytest.mark.parametrize("news", [
+    # new tokens of each sequence by replay; the rows of a call stay as many
+    [(1, 1, 1, 1)] * 6,                                                             # few rows to a key head
+    [(40, 300, 0, 100), (440, 0, 0, 0), (110, 110, 110, 110), (0, 0, 439, 1), (40, 300, 0, 100), (1, 1, 437, 1)],  # chunks, joined after
+    [(3, 5, 0, 4), (5, 5, 2, 0), (0, 0, 12, 0), (3, 5, 0, 4), (1, 1, 1, 9), (12, 0, 0, 0)],
+])
+@pytest.mark.parametrize("codes", [False, True])
+def test_a_captured_call_replayed_over_other_lengths(news, codes):
+    """Lengths, rows and page table change in place between replays: items are split, whole and gone again, and
+    each replay gives the bits of a plain call."""
+    g = gen(53)
+    T, kv, heads, dim, page = sum(news[0]), 2, 4, 128, 16
+    P = Paged(g, [(0, 4000)] * 4, kv, dim, page, BF, codes)
+    lengths = [(4000, 10, 3, 700), (0, 4000, 4000, 0), (900, 901, 902, 903), (64, 0, 3999, 5), (4000, 10, 3, 700), (1, 1, 2500, 1)]
+    q = randn(g, T, heads, dim, dtype=BF).cuda()
+    cache, i32 = P.cache(), dict(dtype=torch.int32, device="cuda")
+    lens, table, offsets = torch.zeros(4, **i32), P.table.cuda(), torch.zeros(5, **i32)
+    batch = qm.Batch(lens, table, offsets, tokens=T, max_new=max(max(n) for n in news))
+    ws = torch.empty(qm.qm_cache_attend_workspace(cache, batch, heads), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(T, heads, dim, dtype=BF, device="cuda"), torch.empty(T, heads, device="cuda")
+
+    def put(i):
+        lens.copy_(torch.tensor([max(n, m) for n, m in zip(lengths[i], news[i])], **i32))
+        offsets.copy_(torch.tensor([0] + list(np.cumsum(news[i])), **i32))
+        table.copy_(P.table.roll(i, 0))
+
+    def call(to, total):
+        qm.qm_cache_attend(cache, batch, q, to, 0.1, ws, lse=total)
+
+    put(0)
+    call(out, lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, lse)
+    for i in list(range(len(news))) * 2:
+        put(i)
+        for _ in range(3):
+            out.zero_()
+            lse.zero_()
+            graph.replay()
+        want, total = torch.zeros_like(out), torch.zeros_like(lse)
+        call(want, total)
+        qm.qm_device_status()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse.view(torch.int32), total.view(torch.int32)), i
+    put(2)  # and the definition's values
+    graph.replay()
+    P.seqs = list(zip(news[2], lens.tolist()))
+    P.keys, P.vals = (x[-2:] + x[:-2] for x in (P.keys, P.vals))
+    check_attend(P, q.cpu(), out.cpu(), lse.cpu(), 0.1)
