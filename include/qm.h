@@ -251,7 +251,8 @@ qm_status qm_experts_route(const void* ids, int32_t id_type, int64_t P, int64_t 
  * Between the packed products: head norms and rotation, a paged key/value
  * cache and the attention that reads it. The pages have no counterpart; these
  * are the operators a decode step needs between its q/k/v and o products.
- * All arithmetic is float32, each result rounded once to its type. */
+ * Sums, softmax statistics and norms are float32, and each result is rounded once to its
+ * type; the products of cache_attend take 16-bit operands, as said there. */
 
 /* Rows of heads: element i of head h of token t at
  * data[t*token_stride + h*head_stride + i] (strides in elements, multiples of 8
@@ -357,10 +358,11 @@ size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, i
  * that sees nothing gets zeros and -infinity; one with a score of +infinity NaN and +infinity; values and scores at positions that
  * a token does not see never reach its results, whatever they hold. q's dtype is
  * the cache's, or either 16-bit type over QM_I8; out's is q's. Weights are rounded
- * to the cache's type before they meet values (over codes: with the value's scale, to
- * float16, or not at all beside a scale past 2^+-80); in float16 one below 2^-22 of its row's largest loses bits,
- * below 2^-33 all. Scales may be of any size and sign. Rows of no
- * sequence are not written. out shares no element with q or the cache. The
+ * to the cache's type before they meet values, after they are summed (over codes: with the
+ * value's scale, to float16, or not at all beside a scale past 2^+-80); in float16 one below
+ * 2^-22 of its row's largest loses bits, below 2^-33 all. Over codes a bfloat16 query may become
+ * float16 after an exact power of two for its row: elements below 2^-31 of the row's largest lose
+ * bits. Scales may be of any size and sign. Rows of no sequence are not written. out shares no element with q or the cache. The
  * results are the same bits in every run of the same arguments. */
 qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm_heads* q, const qm_heads* out,
                           float* lse, float scale, int64_t window, void* workspace, size_t workspace_bytes,

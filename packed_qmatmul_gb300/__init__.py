@@ -655,7 +655,7 @@ def route(ids: torch.Tensor, E: int, stream=None):
 def head_norm_rope(xs: Sequence[torch.Tensor], positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
                    weights: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6, stream=None) -> list:
     """Every head of xs[i] [tokens, heads_i, dim] (queries, keys: any strided rows) normed by weights[i] [dim] and
-    rotated by its token's position."""
+    rotated by its token's position. qm_head_norm_rope takes outs and allocates nothing."""
     with _on(stream):
         return _norm_rope(xs, None, positions, rope, weights, eps, stream)
 
@@ -669,7 +669,8 @@ def cache_append(cache: Cache, batch: Batch, k: torch.Tensor, v: torch.Tensor, r
 def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
                  lse: bool = False, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of the new tokens' queries [tokens, heads, dim] over their sequences in the cache; with lse, (out,
-    the scores' log-sum-exp [tokens, heads])."""
+    the scores' log-sum-exp [tokens, heads]). Rows of no sequence are not written: what is returned there is
+    uninitialised. qm_cache_attend takes out, lse and workspace and allocates nothing."""
     with _on(stream):
         qd, out, od = _heads_and_like(q, batch.tokens, cache.dim, "q")
         _one_gpu((cache.gpu, batch.gpu, q.get_device(), _gpu(workspace)), ("cache", "batch", "q", "workspace"))

@@ -6,8 +6,8 @@
 // in one pass over the keys: with m the running maximum of the scores (in powers
 // of two: t = scale log2(e) (q . k)), l = sum 2^(t_j - m) and o = sum 2^(t_j - m) v_j are
 // rescaled by 2^(m - m') when m grows to m'. Scores, weights' sums and o are float32;
-// a weight is rounded to the values' 16-bit type to enter its product (a relative
-// 2^-9 or 2^-12 that does not add up over keys, as the output's own rounding).
+// a weight is rounded to the values' 16-bit type to enter its product (a relative 2^-8 or
+// 2^-11 at most that does not add up over keys, as the output's own rounding).
 //
 // Every key and value is read once for up to 16 rows, 2 flops a byte and row: what
 // bounds it is HBM. One CTA per SM, eight warps; a warp takes an eighth of a unit's keys and
@@ -21,11 +21,11 @@
 // end of an item the warps' sums are added through shared memory in warp order while
 // the next item's copies are already under way. Up to 32 rows (48 of heads of 64
 // elements: the sums fit in registers) take two or three such tiles of rows at once, their queries
-// in shared memory; against attend_tiles_kernel 112 to 121 us for 32 x 8 tokens of 4 query
-// heads to a key head over 4096, and 121 to 361 over 8-bit codes.
+// in shared memory; against attend_tiles_kernel 113 to 117 us for 32 x 8 tokens of 4 query
+// heads to a key head over 4096, 124 to 339 over 8-bit codes, and 28 to 36 for 32 x 5 drafted tokens (7 heads of 64).
 // Measured: one token of 64 ragged sequences of up to 8192 (16 / 8 heads of 128,
-// 1.08 GB) 175 to 180 us, 6.0 to 6.2 TB/s, 0.9 of the copy rate; of one sequence of 1500 8.4 us, of one of
-// 32768 30 us (4.4 TB/s).
+// 1.08 GB) 176 to 179 us, 6.0 to 6.1 TB/s, 0.9 of the copy rate (184 with 64 / 8 heads); of one sequence of 1500
+// 8.5 us, of one of 32768 30 us (4.4 TB/s).
 //
 // 8-bit codes are exact in both 16-bit types, so they enter the products as they
 // are: a key's scale multiplies its score, a value's scale its weight. All operands
@@ -805,7 +805,10 @@ void set_quotient(int d, uint32_t* mul, int* shift) {
 
 // Rows of an item: by the rows that share a key head (the most of any sequence, if
 // the caller said; else the average). Up to 16, and up to 32 of heads over 64
-// elements or 48 of others, go to attend_rows_kernel, more to attend_tiles_kernel.
+// elements or 48 of others, go to attend_rows_kernel, more to attend_tiles_kernel. So one chunk takes the
+// sequences that decode beside it to items of 256 rows: against a call for each kind, 60 decoding sequences and a
+// chunk of 64 or 512, all of 1024 to 8192 tokens, take 0.61 to 0.77 of the time (14 / 2 heads of 64; 0.9 to 1.03 of 8192)
+// and 0.77 to 1.09 (16 / 8 and 32 / 8 of 128: ahead at 1024, up to 9 % behind at 8192).
 int item_rows(const qm_batch& b, int group, int dp) {
     const int64_t most = b.max_new > 0 ? std::min<int64_t>(b.max_new, b.tokens) : (b.tokens + b.seqs - 1) / b.seqs;
     const int64_t rows = most * group;

@@ -28,8 +28,9 @@
 //    loaders' registers on the way and enter the products exactly.
 // Every wait is bounded; a wait that gives up raises the device flag and the CTA
 // winds down with its copies and products drained.
-// Measured (16 / 8 heads of 128): chunk of 4096 over 32768 706 us, 1460 TFLOP/s, 0.75 of the
-// products' rate; of 4096 over 16384 365 us in pages of 64, 376 in pages of 16 or 20. A unit takes
+// Measured (16 / 8 heads of 128): chunk of 4096 over 32768 706 us, 1460 TFLOP/s, 0.77 of the
+// products' rate in a burst (757 to 767 us after a second of nothing else, when power holds the clock at
+// some 1700 MHz: 0.79 of the sustained rate); of 4096 over 16384 364 us in pages of 64, 373 in pages of 16 or 20. A unit takes
 // 3300 clocks, 2048 of them products: a tile's scores wait 1700 for their weights, then
 // those 1500 for the products and the next scores, and the tiles' turns hide most but not all of it.
 // Over 8-bit codes 1168 us (4096 over 16384): the scales, broadcast from shared memory to every row,
@@ -964,10 +965,10 @@ cudaError_t run_tiles(const TileArgs& a, int runs, cudaStream_t st) {
 }
 
 // Tensor maps of the queries where a tile of 128 rows is whole tokens, and
-// of a 16-bit cache whose pages are multiples of 32 tokens (boxes of 16
-// rows, 2 KB, come slower than the loaders' own copies: 495 against 419 us for
-// a chunk of 4096 over 16384; boxes of 32 and more take 394) and whose heads
-// have at least a box's 64 elements.
+// of a 16-bit cache whose pages are multiples of 32 tokens and whose heads have at least a
+// box's 64 elements. Against the loaders' own copies, chunk of 4096 over 16384 (16 / 8 heads of 128):
+// boxes of 16 rows, 2 KB, 475 us to 372; of 32 rows 379 to 371, but 125 to 147 for 2048 over 8192 with heads of 96,
+// 48 to 51 for 16 x 512 and 287 to 292 for 8192 over itself; of 64 rows 362 to 372.
 void make_maps(TileArgs& t, const qm_cache& c) {
     const Args& a = t.a;
     // the stride of an axis of one never counts, but has to be one that a map can have
