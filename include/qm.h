@@ -57,7 +57,8 @@
  * Errors: QM_EINVAL for a bad argument, with qm_last_error() (thread-local,
  * valid until the next call on the thread) naming the part: "w", "codes",
  * "scales", "biases", "x", "y", "out", "ids", "axis", "workspace" (and for the
- * cache operators "cache", "batch", "k", "v", "q", "rope" and so on). QM_ECUDA if
+ * cache operators "cache", "batch", "k", "v", "q", "rope" and so on, for an
+ * epilogue "bias", "residual", "epilogue", for a router "router", "logits"). QM_ECUDA if
  * a launch fails. A device-side wait that runs past its limit (two seconds of
  * the GPU's global timer) abandons its work and raises a device flag;
  * qm_device_status() reads it. No entry point synchronizes the stream.
@@ -367,6 +368,99 @@ size_t qm_cache_attend_workspace(const qm_cache* cache, const qm_batch* batch, i
 qm_status qm_cache_attend(const qm_cache* cache, const qm_batch* batch, const qm_heads* q, const qm_heads* out,
                           float* lse, float scale, int64_t window, void* workspace, size_t workspace_bytes,
                           qm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the products of a layer: a bias, an activation or gate and a residual
+ * in a product's epilogue, and, for layers of experts, the choice of each token's
+ * experts before the products and their weighted sum after them. The pages have
+ * no counterpart. Everything between the products' sums and the one rounding of a
+ * result is float32. */
+
+typedef enum qm_act {
+    QM_ACT_NONE = 0,
+    QM_ACT_RELU = 1,     /* max(v, 0) */
+    QM_ACT_SILU = 2,     /* v / (1 + exp(-alpha v)) */
+    QM_ACT_GELU = 3,     /* v (1 + erf(v / sqrt 2)) / 2 */
+    QM_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+} qm_act;
+
+/* What becomes of a product's sums v [rows, n] before they are rounded. With the
+ * bias added: act(v) (gated 0), n to a row; or (gated 1, n even) the rows of w are
+ * pairs, 2i a gate g and 2i + 1 beside it u, and n/2 results to a row are
+ * act(min(g, limit)) * (min(max(u, -limit), limit) + up_offset). Then the residual is
+ * added. What the sums hold of infinities and NaN meets these formulas as IEEE
+ * arithmetic says (silu and gelu of -infinity are NaN). A weight whose gates and ups lie in
+ * halves is laid out in pairs once by qm_take along its axis of rows. */
+typedef struct qm_epilogue {
+    const void* bias;        /* NULL, or [n] of bias_dtype (experts: [E, n]), 16-byte aligned */
+    const void* residual;    /* NULL, or [M, n or n/2] of y's dtype (not with experts): row m at
+                                residual + m*residual_stride elements. May be y itself (the same
+                                address and rows); shares no element with it otherwise */
+    int64_t residual_stride; /* not negative; 0: one row for all */
+    int32_t bias_dtype;      /* QM_F32, QM_BF16 or QM_F16 */
+    int32_t act;             /* qm_act */
+    int32_t gated;           /* 0 or 1 */
+    float alpha;             /* QM_ACT_SILU: finite; 0 stands for 1. Otherwise ignored */
+    float limit;             /* gated: above 0, or 0 for none. Must be 0 where not gated */
+    float up_offset;         /* gated: finite. Must be 0 where not gated */
+} qm_epilogue;
+
+/* apply_fused: y [M, n] (gated: [M, n/2]) = ep of x times W^T, the product and its conditions
+ * those of qm_apply; ep must not be NULL. One launch. bias shares no element with y. */
+qm_status qm_apply_fused(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype, const qm_epilogue* ep,
+                         void* y, qm_stream_t stream);
+
+/* apply_experts_fused: qm_apply_experts with ep at each position, the bias its expert's
+ * row of ep->bias [E, n]; y [T, topk, n] (gated: n/2). A position whose id is outside
+ * [0, E) gets zeros, whatever the bias. The workspace is qm_apply_experts_workspace(w, T, topk) bytes. */
+qm_status qm_apply_experts_fused(const qm_weight* w, const void* ids, int32_t id_type, int64_t T, int64_t topk,
+                                 const void* x, int64_t x_rows, int32_t x_dtype, const qm_epilogue* ep, void* y,
+                                 void* workspace, size_t workspace_bytes, qm_stream_t stream);
+
+typedef enum qm_score { QM_SCORE_SOFTMAX = 0, QM_SCORE_SIGMOID = 1 } qm_score;
+typedef enum qm_group_score { QM_GROUP_MAX = 0, QM_GROUP_TOP2 = 1 } qm_group_score;
+
+/* Most experts a token goes to, most experts to choose from, most groups of them. */
+#define QM_MAX_TOPK 31
+#define QM_MAX_EXPERTS 1024
+#define QM_MAX_GROUPS 32
+
+/* How a token's experts are chosen from its logits l [experts]: scores s = softmax(l)
+ * or 1 / (1 + exp(-l)), keys s + bias (bias NULL: s). Experts whose logit or bias is
+ * -infinity, or whose key is NaN, are never chosen. groups > 1: experts lie in `groups`
+ * runs of equal length; a group's score is its largest key, or the sum of its two
+ * largest (-infinity where it has not that many), and only the topk_groups groups
+ * of the largest scores are chosen from. The topk largest keys, largest first, are the
+ * choice. Equal keys and equal groups go to the lower index; keys and groups are ordered as
+ * real numbers would be, up to float64's precision. Where fewer are left than topk,
+ * the last ids are -1 and their weights 0 (apply_experts gives zeros there). weights: the chosen
+ * experts' s, divided by their sum where renormalize is 1, times scale. A token with
+ * a NaN logit, or one of +infinity, has no softmax: its ids are -1, its weights NaN. */
+typedef struct qm_router {
+    const float* bias;    /* NULL or [experts] */
+    int32_t experts;      /* 1 .. QM_MAX_EXPERTS */
+    int32_t topk;         /* 1 .. QM_MAX_TOPK, at most experts */
+    int32_t score;        /* qm_score */
+    int32_t groups;       /* 1 .. QM_MAX_GROUPS, dividing experts; QM_ENOTSUP where 32 / groups lanes (groups
+                             rounded up to a power of two) at 32 experts each cannot hold a group */
+    int32_t topk_groups;  /* 1 .. groups */
+    int32_t group_score;  /* qm_group_score; QM_GROUP_TOP2 needs two experts to a group */
+    int32_t renormalize;  /* 0 or 1 */
+    float scale;          /* finite */
+} qm_router;
+
+/* experts_select: for logits [T, experts] of logits_dtype (QM_F32, QM_BF16 or QM_F16; row t at
+ * logits + t*logits_stride elements), ids int32 [T, topk] and weights float32 [T, topk].
+ * T = 0 launches nothing. */
+qm_status qm_experts_select(const qm_router* router, const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                            int64_t T, int32_t* ids, float* weights, qm_stream_t stream);
+
+/* experts_combine: out [T, n] = the sum over j of weights[t, j] * y[t, j] (y [T, topk, n], weights
+ * float32 [T, topk]), added from j = 0 on, plus residual (NULL, or row t at residual +
+ * t*residual_stride elements, as in qm_epilogue; it may be out itself). y, residual and out
+ * are of dtype (QM_BF16). out shares no element with y. topk = 0 is an empty sum. */
+qm_status qm_experts_combine(const void* y, const float* weights, int64_t T, int64_t topk, int64_t n, int32_t dtype,
+                             const void* residual, int64_t residual_stride, void* out, qm_stream_t stream);
 
 /* Exercises the failure path of the bounded device waits without a fault:
  * enqueues one warp that waits on a barrier nothing will complete, with the

@@ -24,13 +24,15 @@ import torch
 __all__ = [
     "QM_AFFINE", "QM_Q8_0", "QM_MXFP4", "QM_MXFP4_BLOCKS", "QM_Q4_K", "QM_Q6_K", "QM_WEIGHT_STATIC", "QM_F32", "QM_BF16", "QM_F16", "QM_I8", "QM_I32", "QM_I64",
     "QM_ROPE_HALF", "QM_ROPE_PAIRS",
-    "QMError", "QWeight", "Rope", "Cache", "Batch", "library_path", "load_library",
+    "QMError", "QWeight", "Rope", "Cache", "Batch", "Epilogue", "Router", "library_path", "load_library",
     "qm_dequant", "qm_quantize_q8_0", "qm_apply", "qm_apply_many", "qm_take", "qm_apply_experts", "qm_apply_experts_workspace",
     "qm_experts_route_workspace",
     "qm_experts_route", "qm_apply_experts_static", "qm_check_wait_timeout", "qm_device_status", "qm_last_error",
     "qm_version", "qm_head_norm_rope", "qm_cache_append", "qm_cache_attend", "qm_cache_attend_workspace",
     "dequant", "quantize_q8_0", "apply", "apply_many", "take", "apply_experts", "route",
     "head_norm_rope", "cache_append", "cache_attend",
+    "qm_apply_fused", "qm_apply_experts_fused", "qm_experts_select", "qm_experts_combine",
+    "apply_fused", "apply_experts_fused", "experts_select", "experts_combine",
 ]
 
 QM_OK, QM_EINVAL, QM_ECUDA, QM_ETIMEOUT, QM_ENOTSUP = 0, 1, 2, 3, 4
@@ -42,6 +44,7 @@ QM_WEIGHT_STATIC = 1
 QM_MAX_NDIM = 4
 QM_MAX_MANY = 8
 QM_MAX_HEAD_SETS = 4
+QM_MAX_TOPK, QM_MAX_EXPERTS, QM_MAX_GROUPS = 31, 1024, 32
 
 _STATUS = {QM_EINVAL: "QM_EINVAL", QM_ECUDA: "QM_ECUDA", QM_ETIMEOUT: "QM_ETIMEOUT",
            QM_ENOTSUP: "QM_ENOTSUP"}
@@ -49,6 +52,9 @@ _FORMATS = {"affine": QM_AFFINE, "q8_0": QM_Q8_0, "mxfp4": QM_MXFP4, "mxfp4_bloc
             "q4_k": QM_Q4_K, "q6_k": QM_Q6_K}
 _DTYPES = {torch.float32: QM_F32, torch.bfloat16: QM_BF16, torch.float16: QM_F16}
 _ITYPES = {torch.int32: QM_I32, torch.int64: QM_I64}
+_ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
 _CACHE_DTYPES = {torch.bfloat16: QM_BF16, torch.float16: QM_F16, torch.int8: QM_I8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -108,6 +114,10 @@ def load_library():
             "qm_cache_append": ([vp, vp, vp, vp, vp, ctypes.c_float, vp, vp], i32),
             "qm_cache_attend_workspace": ([vp, vp, i32], sz),
             "qm_cache_attend": ([vp, vp, vp, vp, vp, ctypes.c_float, i64, vp, sz, vp], i32),
+            "qm_apply_fused": ([wp, vp, i64, i32, vp, vp, vp], i32),
+            "qm_apply_experts_fused": ([wp, vp, i32, i64, i64, vp, i64, i32, vp, vp, vp, sz, vp], i32),
+            "qm_experts_select": ([vp, vp, i32, i64, i64, vp, vp, vp], i32),
+            "qm_experts_combine": ([vp, vp, i64, i64, i64, i32, vp, i64, vp, vp], i32),
             "qm_device_status": ([vp], i32),
             "qm_last_error": ([], ctypes.c_char_p),
             "qm_version": ([], i32),
@@ -382,6 +392,68 @@ class Batch:
                          self.tokens, page_table.shape[1], page_table.stride(0), seqs, self.max_new)
 
 
+# ---------------------------------------------------------------- around a layer's products
+_EPILOGUE = struct.Struct("2Pq3i3f").pack
+_ROUTER = struct.Struct("P7if").pack
+
+
+class Epilogue:
+    """What becomes of a product's sums before they are rounded (qm_epilogue): `bias` [n] (experts: [E, n])
+    float32, bfloat16 or float16; act None, "relu", "silu" (v / (1 + exp(-alpha v))), "gelu" or "gelu_tanh";
+    gated: the weight's rows are pairs, 2i a gate g and 2i + 1 beside it u, and n / 2 results to a row are
+    act(min(g, limit)) * (min(max(u, -limit), limit) + up_offset), limit 0 standing for none. A weight whose gates
+    and ups lie in halves is laid out in pairs once by take along its rows. The descriptor is built here, from
+    the bias's address at that time."""
+
+    def __init__(self, bias: Optional[torch.Tensor] = None, act: Optional[str] = None, gated: bool = False, alpha: float = 1.0,
+                 limit: float = 0.0, up_offset: float = 0.0):
+        if act not in _ACTS:
+            _refuse('epilogue: act must be None, "relu", "silu", "gelu" or "gelu_tanh"')
+        if bias is not None and bias.dtype not in _DTYPES:
+            _refuse("bias: must be float32, bfloat16 or float16")
+        if alpha == 0.0:
+            _refuse("epilogue: alpha must not be 0")
+        self.bias, self.act, self.gated = bias, act, bool(gated)
+        self.gpu = _gpu(bias)
+        self._shape = None if bias is None else tuple(bias.shape)
+        self._tail = (0 if bias is None else _DTYPES[bias.dtype], _ACTS[act], int(self.gated), alpha, limit, up_offset)
+        self._bias = _ptr(bias) or 0
+        self._c = _EPILOGUE(self._bias, 0, 0, *self._tail)
+
+    def _with(self, residual: torch.Tensor) -> bytes:
+        """The descriptor with a residual [M, n or n/2] whose rows are contiguous."""
+        return _EPILOGUE(self._bias, residual.data_ptr(), residual.stride(0), *self._tail)
+
+
+class Router:
+    """How a token's experts are chosen from its logits (qm_router): scores by "softmax" or "sigmoid", a float32
+    bias [experts] added where experts are chosen (not to their weights), groups of which topk_groups stay (None: all)
+    by their largest key ("max") or the sum of their two largest ("top2"), topk experts, their weights divided by their sum
+    (renormalize) and times scale. The bias may be updated in place between calls."""
+
+    def __init__(self, topk: int, score: str = "softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
+                 topk_groups: Optional[int] = None, group_score: str = "max", renormalize: bool = True, scale: float = 1.0):
+        if score not in _SCORES:
+            _refuse('router: score must be "softmax" or "sigmoid"')
+        if group_score not in _GROUP_SCORES:
+            _refuse('router: group_score must be "max" or "top2"')
+        if bias is not None and (bias.dtype != torch.float32 or bias.dim() != 1):
+            _refuse("bias: must be float32 [experts]")
+        self.topk, self.bias, self.gpu = int(topk), bias, _gpu(bias)
+        self._args = (self.topk, _SCORES[score], groups, groups if topk_groups is None else topk_groups, _GROUP_SCORES[group_score],
+                      int(bool(renormalize)), scale)
+        self._bias = _ptr(bias) or 0
+        self._made = {}
+
+    def _c(self, experts: int) -> bytes:
+        got = self._made.get(experts)
+        if got is None:
+            if self.bias is not None and self.bias.shape[0] != experts:
+                _refuse(f"bias: shape {tuple(self.bias.shape)}, expected {(experts,)}")
+            got = self._made[experts] = _ROUTER(self._bias, experts, *self._args)
+        return got
+
+
 # ---------------------------------------------------------------- C entry points
 def qm_version() -> int:
     return load_library().qm_version()
@@ -578,6 +650,140 @@ def qm_cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, out: torch.Tens
         cache._c, batch._c, qd, od, _ptr(lse), scale, window, _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+def _bf16(t: torch.Tensor, name: str) -> int:
+    """The address of a contiguous bfloat16 tensor."""
+    if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        _refuse(f"{name}: must be contiguous bfloat16")
+    return t.data_ptr()
+
+
+def _residual(residual: torch.Tensor, rows: int, n: int) -> None:
+    if residual.shape != (rows, n) or residual.dtype != torch.bfloat16:
+        _refuse(f"residual: must be bfloat16 {(rows, n)}")
+    if residual.stride(1) != 1 and n > 1:
+        _refuse("residual: rows must be contiguous")
+
+
+def _fused_columns(w: QWeight, ep: Epilogue, ndim: int) -> int:
+    """y's columns; refuses a bias that is not the weight's."""
+    shape = w.shape
+    if len(shape) != ndim:
+        _refuse(f"w: must have {ndim} axes")
+    if ep._shape is not None and ep._shape != shape[:-1]:
+        _refuse(f"bias: shape {ep._shape}, expected {shape[:-1]}")
+    return shape[-2] // 2 if ep.gated else shape[-2]
+
+
+def _fused(w: QWeight, x: torch.Tensor, ep: Epilogue, residual, y, stream) -> torch.Tensor:
+    n = _fused_columns(w, ep, 2)
+    if x.dim() != 2 or x.shape[1] != w.shape[1]:
+        _refuse(f"x: shape {tuple(x.shape)}, expected {('M', w.shape[1])}")
+    M, gpu = x.shape[0], x.get_device()
+    xp = _bf16(x, "x")
+    if y is None:
+        y = torch.empty((M, n), dtype=torch.bfloat16, device=x.device)
+    elif y.shape != (M, n):
+        _refuse(f"y: shape {tuple(y.shape)}, expected {(M, n)}")
+    c = ep._c
+    if residual is not None:
+        _residual(residual, M, n)
+        c = ep._with(residual)
+    _one_gpu((gpu, y.get_device(), w.codes.get_device(), ep.gpu, _gpu(residual)), ("x", "y", "w", "bias", "residual"))
+    _check(load_library().qm_apply_fused(w._ref(), xp, M, QM_BF16, c, _bf16(y, "y"), _stream(stream)))
+    return y
+
+
+def qm_apply_fused(w: QWeight, x: torch.Tensor, ep: Epilogue, y: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = ep of x [M, k] times w^T, plus residual (any strided rows; y itself to add in place)."""
+    _fused(w, x, ep, residual, y, stream)
+
+
+def _experts_fused(w: QWeight, ids: torch.Tensor, x: torch.Tensor, ep: Epilogue, y, workspace, stream) -> torch.Tensor:
+    n = _fused_columns(w, ep, 3)
+    if ids.dim() != 2:
+        _refuse("ids: must be [T, topk]")
+    T, topk = ids.shape
+    itype = _ITYPES.get(ids.dtype)
+    if itype is None or not ids.is_contiguous():
+        _refuse("ids: must be contiguous int32 or int64")
+    if x.dim() != 2 or x.shape[1] != w.shape[2] or x.shape[0] not in (T, T * topk):
+        _refuse(f"x: shape {tuple(x.shape)}, expected {('T or T*topk', w.shape[2])}")
+    if y is None:
+        y = torch.empty((T, topk, n), dtype=torch.bfloat16, device=x.device)
+    elif y.shape != (T, topk, n):
+        _refuse(f"y: shape {tuple(y.shape)}, expected {(T, topk, n)}")
+    if workspace is None:
+        need = qm_apply_experts_workspace(w, T, topk)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _one_gpu((x.get_device(), ids.get_device(), y.get_device(), w.codes.get_device(), ep.gpu, _gpu(workspace)),
+             ("x", "ids", "y", "w", "bias", "workspace"))
+    _check(load_library().qm_apply_experts_fused(
+        w._ref(), ids.data_ptr(), itype, T, topk, _bf16(x, "x"), x.shape[0], QM_BF16, ep._c, _bf16(y, "y"), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+    return y
+
+
+def qm_apply_experts_fused(w: QWeight, ids: torch.Tensor, x: torch.Tensor, ep: Epilogue, y: torch.Tensor, workspace: torch.Tensor,
+                           stream=None) -> None:
+    """y [T, topk, columns] = ep of each position's expert's product; the workspace as for qm_apply_experts."""
+    _experts_fused(w, ids, x, ep, y, workspace, stream)
+
+
+def _select(logits: torch.Tensor, router: Router, ids, weights, stream):
+    if logits.dim() != 2:
+        _refuse("logits: must be [T, experts]")
+    T, E = logits.shape
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
+        _refuse("logits: must be float32, bfloat16 or float16")
+    stride, es = logits.stride()
+    if es != 1 and E > 1:
+        _refuse("logits: rows must be contiguous")
+    c, shape = router._c(E), (T, router.topk)
+    if ids is None:
+        device = logits.device
+        ids, weights = torch.empty(shape, dtype=torch.int32, device=device), torch.empty(shape, dtype=torch.float32, device=device)
+    else:
+        if ids.shape != shape or ids.dtype != torch.int32 or not ids.is_contiguous():
+            _refuse(f"ids: must be contiguous int32 {shape}")
+        if weights.shape != shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+            _refuse(f"weights: must be contiguous float32 {shape}")
+    _one_gpu((logits.get_device(), ids.get_device(), weights.get_device(), router.gpu), ("logits", "ids", "weights", "bias"))
+    _check(load_library().qm_experts_select(c, logits.data_ptr(), dtype, stride, T, ids.data_ptr(), weights.data_ptr(),
+                                            _stream(stream)))
+    return ids, weights
+
+
+def qm_experts_select(logits: torch.Tensor, router: Router, ids: torch.Tensor, weights: torch.Tensor, stream=None) -> None:
+    """ids int32 and weights float32 [T, topk] of the experts that `router` chooses for logits [T, experts]."""
+    _select(logits, router, ids, weights, stream)
+
+
+def _combine(y: torch.Tensor, weights: torch.Tensor, residual, out, stream) -> torch.Tensor:
+    if y.dim() != 3:
+        _refuse("y: must be [T, topk, n]")
+    T, topk, n = y.shape
+    if weights.shape != (T, topk) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        _refuse(f"weights: must be contiguous float32 {(T, topk)}")
+    if out is None:
+        out = torch.empty((T, n), dtype=torch.bfloat16, device=y.device)
+    elif out.shape != (T, n):
+        _refuse(f"out: shape {tuple(out.shape)}, expected {(T, n)}")
+    rp, stride = None, 0
+    if residual is not None:
+        _residual(residual, T, n)
+        rp, stride = residual.data_ptr(), residual.stride(0)
+    _one_gpu((y.get_device(), weights.get_device(), out.get_device(), _gpu(residual)), ("y", "weights", "out", "residual"))
+    _check(load_library().qm_experts_combine(_bf16(y, "y"), weights.data_ptr(), T, topk, n, QM_BF16, rp, stride, _bf16(out, "out"),
+                                             _stream(stream)))
+    return out
+
+
+def qm_experts_combine(y: torch.Tensor, weights: torch.Tensor, out: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out [T, n] = the sum over j of weights[t, j] * y[t, j], plus residual (any strided rows; out itself to add in place)."""
+    _combine(y, weights, residual, out, stream)
+
+
 def qm_check_wait_timeout(limit_ns: int, stream=None) -> None:
     _check(load_library().qm_check_wait_timeout(limit_ns, _stream(stream)))
 
@@ -683,3 +889,29 @@ def cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, scale: Optional[fl
             cache._c, batch._c, qd, od, _ptr(total), cache.dim ** -0.5 if scale is None else scale, window, _ptr(workspace),
             0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
         return (out, total) if lse else out
+
+
+def apply_fused(w: QWeight, x: torch.Tensor, epilogue: Epilogue, residual: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """epilogue of x [M, k] times w^T, plus residual [M, columns], rounded once."""
+    with _on(stream):
+        return _fused(w, x, epilogue, residual, None, stream)
+
+
+def apply_experts_fused(w: QWeight, ids: torch.Tensor, x: torch.Tensor, epilogue: Epilogue, workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """apply_experts with an epilogue at each position (its bias that of the position's expert) -> [T, topk, columns]."""
+    with _on(stream):
+        return _experts_fused(w, ids, x, epilogue, None, workspace, stream)
+
+
+def experts_select(logits: torch.Tensor, router: Router, stream=None):
+    """(ids int32, weights float32) [T, topk] of the experts that `router` chooses for logits [T, experts] (any strided
+    rows). qm_experts_select takes both and allocates nothing."""
+    with _on(stream):
+        return _select(logits, router, None, None, stream)
+
+
+def experts_combine(y: torch.Tensor, weights: torch.Tensor, residual: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """[T, n]: the sum over j of weights[t, j] * y[t, j], plus residual [T, n]."""
+    with _on(stream):
+        return _combine(y, weights, residual, None, stream)

@@ -307,31 +307,42 @@ static bool few_token_register_path(const WDesc& d, int64_t M) {
 }
 
 // The launches of a validated product (M >= 1, n >= 1, k >= 1).
-static qm_status apply_launch(const WDesc& d, const void* x, int64_t M, void* y, cudaStream_t st) {
-    if (M == 1 && one_token_register_path(d)) return check_launch(launch_gemv1(d, x, y, st), "gemv launch");
+static qm_status apply_launch(const WDesc& d, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st) {
+    if (M == 1 && one_token_register_path(d)) return check_launch(launch_gemv1(d, ep, x, y, st), "gemv launch");
     if (few_token_register_path(d, M)) {
         void* ys[1] = {y};
-        return check_launch(launch_gemvr_many(&d, 1, x, M, ys, st), "gemv launch");
+        return check_launch(launch_gemvr_many(&d, 1, x, M, ys, st, &ep), "gemv launch");
     }
-    if (M <= 16 && gemv_supported(d, M)) return launch_gemv(d, x, M, y, st);
-    if (gemm_supported(d, M)) return launch_gemm(d, x, M, y, st);
-    return check_launch(launch_apply_simple(d, x, M, y, st), "apply launch");
+    if (M <= 16 && gemv_supported(d, M)) return launch_gemv(d, ep, x, M, y, st);
+    if (gemm_supported(d, M)) return launch_gemm(d, ep, x, M, y, st);
+    return check_launch(launch_apply_simple(d, ep, x, M, y, st), "apply launch");
 }
 
-qm_status qm_apply(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype, void* y,
-                   qm_stream_t stream) {
-    set_error("");
+// A product without an epilogue.
+static Epi plain(const WDesc& d) {
+    Epi e;
+    e.yn = d.n;
+    return e;
+}
+
+// qm_apply, and with an epilogue qm_apply_fused.
+static qm_status apply_checked(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype, const qm_epilogue* ep, void* y,
+                               qm_stream_t stream) {
     WDesc d;
     qm_status s = validate_weight(w, &d);
     if (s != QM_OK) return s;
     if (d.ndim != 2) return fail(QM_ENOTSUP, "w: apply takes a 2-d weight [n, k]");
     if (M < 0) return fail(QM_EINVAL, "x: negative row count M");
     if (x_dtype != QM_BF16) return fail(QM_ENOTSUP, "x: apply takes bfloat16 activations");
+    Epi e = plain(d);
+    if (ep && (s = validate_epilogue(ep, d, M, &e)) != QM_OK) return s;
     if (M == 0 || d.n == 0) return QM_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!y) return fail(QM_EINVAL, "y: NULL");
     if (!aligned16(y)) return fail(QM_EINVAL, "y: base address must be 16-byte aligned");
+    if (ep && (s = check_epilogue_overlap(e, d, M, y)) != QM_OK) return s;
     if (d.k == 0) {  // an empty sum
+        if (e.on) return check_launch(launch_apply_simple(d, e, x, M, y, st), "apply launch");
         return check_launch(cudaMemsetAsync(y, 0, static_cast<size_t>(M * d.n * 2), st),
                             "apply memset");
     }
@@ -339,8 +350,21 @@ qm_status qm_apply(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype
     if (!aligned16(x)) return fail(QM_EINVAL, "x: base address must be 16-byte aligned");
     const char* xb = static_cast<const char*>(x);
     const char* yb = static_cast<const char*>(y);
-    if (xb < yb + M * d.n * 2 && yb < xb + M * d.k * 2) return fail(QM_EINVAL, "y: overlaps x");
-    return apply_launch(d, x, M, y, st);
+    if (xb < yb + M * e.yn * 2 && yb < xb + M * d.k * 2) return fail(QM_EINVAL, "y: overlaps x");
+    return apply_launch(d, e, x, M, y, st);
+}
+
+qm_status qm_apply(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype, void* y,
+                   qm_stream_t stream) {
+    set_error("");
+    return apply_checked(w, x, M, x_dtype, nullptr, y, stream);
+}
+
+qm_status qm_apply_fused(const qm_weight* w, const void* x, int64_t M, int32_t x_dtype, const qm_epilogue* ep,
+                         void* y, qm_stream_t stream) {
+    set_error("");
+    if (!ep) return fail(QM_EINVAL, "epilogue: NULL");
+    return apply_checked(w, x, M, x_dtype, ep, y, stream);
 }
 
 qm_status qm_apply_many(const qm_weight* const* ws, int32_t count, const void* x, int64_t M, int32_t x_dtype,
@@ -405,7 +429,7 @@ qm_status qm_apply_many(const qm_weight* const* ws, int32_t count, const void* x
         if (k == 0)
             s = check_launch(cudaMemsetAsync(live_y[i], 0, static_cast<size_t>(M * live[i].n * 2), st), "apply memset");
         else
-            s = apply_launch(live[i], x, M, live_y[i], st);
+            s = apply_launch(live[i], plain(live[i]), x, M, live_y[i], st);
         if (s != QM_OK) return s;
     }
     return QM_OK;
@@ -494,12 +518,21 @@ qm_status qm_apply_experts(const qm_weight* w, const void* ids, int32_t id_type,
                                  workspace_bytes, stream, true);
 }
 
+qm_status qm_apply_experts_fused(const qm_weight* w, const void* ids, int32_t id_type, int64_t T, int64_t topk,
+                                 const void* x, int64_t x_rows, int32_t x_dtype, const qm_epilogue* ep, void* y,
+                                 void* workspace, size_t workspace_bytes, qm_stream_t stream) {
+    set_error("");
+    if (!ep) return fail(QM_EINVAL, "epilogue: NULL");
+    return apply_experts_checked(w, ids, id_type, T, topk, x, x_rows, x_dtype, y, workspace,
+                                 workspace_bytes, stream, true, ep);
+}
+
 }  // extern "C"
 
 qm_status qm::apply_experts_checked(const qm_weight* w, const void* ids, int32_t id_type, int64_t T,
                                     int64_t topk, const void* x, int64_t x_rows, int32_t x_dtype, void* y,
                                     void* workspace, size_t workspace_bytes, qm_stream_t stream,
-                                    bool allow_tensor) {
+                                    bool allow_tensor, const qm_epilogue* ep) {
     set_error("");
     WDesc d;
     qm_status s = validate_weight(w, &d);
@@ -513,22 +546,25 @@ qm_status qm::apply_experts_checked(const qm_weight* w, const void* ids, int32_t
     if (x_rows != T && x_rows != T * topk)
         return fail(QM_EINVAL, "x: rows must be T (broadcast over topk) or T*topk");
     const int64_t P = T * topk;
+    Epi e = plain(d);
+    if (ep && (s = validate_epilogue(ep, d, P, &e)) != QM_OK) return s;
     if (P == 0 || d.n == 0) return QM_OK;
     if (!y) return fail(QM_EINVAL, "y: NULL");
     if (!aligned16(y)) return fail(QM_EINVAL, "y: base address must be 16-byte aligned");
     if (!ids) return fail(QM_EINVAL, "ids: NULL");
     if ((reinterpret_cast<uintptr_t>(ids) & (id_type == QM_I64 ? 7u : 3u)) != 0)
         return fail(QM_EINVAL, "ids: misaligned");
+    if (ep && (s = check_epilogue_overlap(e, d, P, y)) != QM_OK) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (d.k == 0)
+    if (d.k == 0 && !e.on)
         return check_launch(cudaMemsetAsync(y, 0, static_cast<size_t>(P * d.n * 2), st), "experts memset");
-    if (!x) return fail(QM_EINVAL, "x: NULL");
+    if (!x && d.k > 0) return fail(QM_EINVAL, "x: NULL");
     if (!aligned16(x)) return fail(QM_EINVAL, "x: base address must be 16-byte aligned");
     const size_t need = experts_workspace_bytes(d, P, allow_tensor);
     if (!workspace || workspace_bytes < need)
         return fail(QM_EINVAL, "workspace: needs " + std::to_string(need) + " bytes");
     if (!aligned16(workspace)) return fail(QM_EINVAL, "workspace: must be 16-byte aligned");
-    return launch_experts(d, ids, id_type == QM_I64, T, topk, x, x_rows, y, workspace,
+    return launch_experts(d, e, ids, id_type == QM_I64, T, topk, x, x_rows, y, workspace,
                           workspace_bytes, st, allow_tensor);
 }
 

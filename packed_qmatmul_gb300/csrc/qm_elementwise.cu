@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -526,53 +527,63 @@ cudaError_t launch_take_packed(const TakeParts& tp, int64_t outer, int64_t len, 
 // sums lanes in a fixed butterfly order. Used where the fast paths decline.
 namespace {
 template <int FMT, int BITS>
-__global__ void __launch_bounds__(256) apply_simple_kernel(DecodeArgs a, int64_t n, const uint16_t* x,
+__global__ void __launch_bounds__(256) apply_simple_kernel(DecodeArgs a, const Epi ep, const uint16_t* x,
                                                            int64_t M, uint16_t* y) {
     const int lane = threadIdx.x & 31;
     const int64_t warp = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
     const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t mblocks = (M + 7) / 8;
     const int64_t upr = a.k / 32;
-    for (int64_t job = warp; job < n * mblocks; job += nwarps) {
+    // a job: column j of y (one row of w, or where gated the pair 2j, 2j + 1) for eight tokens
+    for (int64_t job = warp; job < ep.yn * mblocks; job += nwarps) {
         const int64_t j = job / mblocks, m0 = (job % mblocks) * 8;
-        float acc[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-        for (int64_t u = lane; u < upr; u += 32) {
-            float v[32];
-            decode_unit<FMT, BITS>(a, j, u, v);
+        const int64_t row = ep.gated ? 2 * j : j;
+        float acc[8] = {}, gate[8];
+        #pragma unroll 1
+        for (int h = 0; h <= ep.gated; ++h) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (m0 + i < M) {
-                    const uint16_t* xr = x + (m0 + i) * a.k + 32 * u;
-                    float s = 0.0f;
+                gate[i] = acc[i];  // the gate's sums once the second row begins
+                acc[i] = 0.0f;
+            }
+            for (int64_t u = lane; u < upr; u += 32) {
+                float v[32];
+                decode_unit<FMT, BITS>(a, row + h, u, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s = fmaf(bf16_bits_to_f32(xr[e]), v[e], s);
-                    acc[i] += s;
+                for (int i = 0; i < 8; ++i) {
+                    if (m0 + i < M) {
+                        const uint16_t* xr = x + (m0 + i) * a.k + 32 * u;
+                        float s = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s = fmaf(bf16_bits_to_f32(xr[e]), v[e], s);
+                        acc[i] += s;
+                    }
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
             }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float s = acc[i];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            if (lane == 0 && m0 + i < M) {
-                __nv_bfloat16 b = __float2bfloat16_rn(s);
-                y[(m0 + i) * n + j] = *reinterpret_cast<uint16_t*>(&b);
-            }
+            if (lane == 0 && m0 + i < M)
+                y[(m0 + i) * ep.yn + j] = !ep.on     ? bf16_bits(acc[i])
+                                          : ep.gated ? epi_finish(ep, gate[i], acc[i], row, m0 + i, j)
+                                                     : epi_finish(ep, acc[i], 0.0f, row, m0 + i, j);
         }
     }
 }
 }  // namespace
 
-cudaError_t launch_apply_simple(const WDesc& w, const void* x, int64_t M, void* y, cudaStream_t st) {
+cudaError_t launch_apply_simple(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st) {
     DecodeArgs a{w.codes, w.scales, w.biases, w.k, w.code_row_bytes, w.scale_row_bytes, w.gs, w.sdt};
-    const int64_t jobs = w.n * ((M + 7) / 8);
+    const int64_t jobs = ep.yn * ((M + 7) / 8);
     const int64_t blocks = std::min<int64_t>((jobs * 32 + 255) / 256, int64_t(num_sms()) * 8);
     const uint16_t* xb = static_cast<const uint16_t*>(x);
     uint16_t* yb = static_cast<uint16_t*>(y);
-#define QM_SIMPLE(B) apply_simple_kernel<QM_AFFINE, B><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb)
+#define QM_SIMPLE(B) apply_simple_kernel<QM_AFFINE, B><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb)
     if (w.fmt == QM_AFFINE && w.bits == 2) QM_SIMPLE(2);
     else if (w.fmt == QM_AFFINE && w.bits == 3) QM_SIMPLE(3);
     else if (w.fmt == QM_AFFINE && w.bits == 4) QM_SIMPLE(4);
@@ -581,15 +592,15 @@ cudaError_t launch_apply_simple(const WDesc& w, const void* x, int64_t M, void* 
     else if (w.fmt == QM_AFFINE) QM_SIMPLE(8);
 #undef QM_SIMPLE
     else if (w.fmt == QM_Q8_0)
-        apply_simple_kernel<QM_Q8_0, 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb);
+        apply_simple_kernel<QM_Q8_0, 8><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb);
     else if (w.fmt == QM_MXFP4_BLOCKS)
-        apply_simple_kernel<QM_MXFP4_BLOCKS, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb);
+        apply_simple_kernel<QM_MXFP4_BLOCKS, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb);
     else if (w.fmt == QM_Q4_K)
-        apply_simple_kernel<QM_Q4_K, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb);
+        apply_simple_kernel<QM_Q4_K, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb);
     else if (w.fmt == QM_Q6_K)
-        apply_simple_kernel<QM_Q6_K, 6><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb);
+        apply_simple_kernel<QM_Q6_K, 6><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb);
     else
-        apply_simple_kernel<QM_MXFP4, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, w.n, xb, M, yb);
+        apply_simple_kernel<QM_MXFP4, 4><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, xb, M, yb);
     return cudaGetLastError();
 }
 

@@ -14,6 +14,7 @@
 #include <string>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -62,6 +63,7 @@ enum class Path { kSimple, kDecode, kTensor };
 
 Path experts_path(const WDesc& w, int64_t P, bool allow_tensor) {
     const int64_t E = w.shape[0];
+    if (w.k == 0) return Path::kSimple;  // empty sums, through an epilogue
     const bool decode = gemv_grouped_supported(w, P);
     if (decode && P <= 32 * E) return Path::kDecode;   // few positions per expert: HBM-bound
     if (allow_tensor && gemm_grouped_supported(w, P)) return Path::kTensor;
@@ -260,9 +262,10 @@ QM_DEV float value_at(const ExpArgs& a, int64_t r, int64_t i) {
     }
 }
 
-// Plain segmented product: one warp per (routed position, output row).
+// Plain segmented product: one warp per (routed position, output column: one
+// row of the expert's matrix, or where gated the pair 2j, 2j + 1).
 template <int FMT, int BITS>
-__global__ void __launch_bounds__(256) experts_simple_kernel(ExpArgs a, const void* ids, int id64,
+__global__ void __launch_bounds__(256) experts_simple_kernel(ExpArgs a, const Epi ep, const void* ids, int id64,
                                                              int64_t P, int64_t topk, int64_t T,
                                                              const uint16_t* x, int64_t x_rows,
                                                              const int32_t* perm,
@@ -271,23 +274,31 @@ __global__ void __launch_bounds__(256) experts_simple_kernel(ExpArgs a, const vo
     const int64_t warp = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
     const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
     const int64_t n_in = offsets[a.E];
-    for (int64_t job = warp; job < P * a.n; job += nwarps) {
-        const int64_t q = job / a.n, j = job % a.n;
+    for (int64_t job = warp; job < P * ep.yn; job += nwarps) {
+        const int64_t q = job / ep.yn, j = job % ep.yn;
         const int64_t p = perm[q];
-        float s = 0.0f;
+        float s = 0.0f, gate = 0.0f;
+        int64_t row = 0;
         if (q < n_in) {
             const int64_t e = load_id(ids, id64, p);
             const int64_t xr = (x_rows == T) ? p / topk : p;
             const uint16_t* xp = x + xr * a.k;
-            for (int64_t i = lane; i < a.k; i += 32)
-                s = fmaf(bf16_bits_to_f32(xp[i]), value_at<FMT, BITS>(a, e * a.n + j, i), s);
+            row = e * a.n + (ep.gated ? 2 * j : j);
+            #pragma unroll 1
+            for (int h = 0; h <= ep.gated; ++h) {
+                gate = s;  // the gate's sum once the second row begins
+                s = 0.0f;
+                for (int64_t i = lane; i < a.k; i += 32)
+                    s = fmaf(bf16_bits_to_f32(xp[i]), value_at<FMT, BITS>(a, row + h, i), s);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            }
         }
-        if (lane == 0) {
-            __nv_bfloat16 b = __float2bfloat16_rn(s);
-            y[p * a.n + j] = (q < n_in) ? *reinterpret_cast<uint16_t*>(&b) : uint16_t(0);
-        }
+        if (lane == 0)
+            y[p * ep.yn + j] = q >= n_in  ? uint16_t(0)
+                               : !ep.on   ? bf16_bits(s)
+                               : ep.gated ? epi_finish(ep, gate, s, row, p, j)
+                                          : epi_finish(ep, s, 0.0f, row, p, j);
     }
 }
 
@@ -329,7 +340,7 @@ cudaError_t launch_route(const void* ids, int id64, int64_t P, int64_t E, int32_
                       static_cast<const int32_t*>(chunk_counts), counts, offsets, perm, zy, zn);
 }
 
-qm_status launch_experts(const WDesc& w, const void* ids, int id64, int64_t T, int64_t topk,
+qm_status launch_experts(const WDesc& w, const Epi& ep, const void* ids, int id64, int64_t T, int64_t topk,
                          const void* x, int64_t x_rows, void* y, void* ws, size_t ws_bytes,
                          cudaStream_t st, bool allow_tensor) {
     (void)ws_bytes;
@@ -342,10 +353,10 @@ qm_status launch_experts(const WDesc& w, const void* ids, int id64, int64_t T, i
     int32_t* perm = reinterpret_cast<int32_t*>(wb + l.perm);
     const int xdiv = x_rows == T ? static_cast<int>(topk) : 1;
     cudaError_t e = launch_route(ids, id64, P, E, counts, offsets, perm, ws, st,
-                                 path != Path::kSimple ? static_cast<uint16_t*>(y) : nullptr, w.n);
+                                 path != Path::kSimple ? static_cast<uint16_t*>(y) : nullptr, ep.yn);
     if (e != cudaSuccess) return cuda_fail(e, "route launch");
     if (path == Path::kDecode)  // experts averaging few positions: chunks through the decode product
-        return launch_gemv_grouped(w, offsets, perm, P, xdiv, x, y, st);
+        return launch_gemv_grouped(w, ep, offsets, perm, P, xdiv, x, y, st);
     if (path == Path::kTensor) {  // routed rows gathered expert by expert, then the tensor-core product
         uint4* xs = reinterpret_cast<uint4*>(wb + l.xs);
         const int64_t blocks = std::min<int64_t>((P + 7) / 8, int64_t(num_sms()) * 8);
@@ -353,15 +364,15 @@ qm_status launch_experts(const WDesc& w, const void* ids, int id64, int64_t T, i
                        static_cast<const int32_t*>(offsets + E), static_cast<const int32_t*>(perm), xdiv,
                        static_cast<const uint4*>(x), static_cast<int64_t>(w.k * 2 / 16), xs);
         if (e != cudaSuccess) return cuda_fail(e, "gather launch");
-        return launch_gemm_grouped(w, offsets, perm, P, xs, y, st);
+        return launch_gemm_grouped(w, ep, offsets, perm, P, xs, y, st);
     }
     ExpArgs a{w.codes, w.scales, w.biases, E, w.n, w.k, w.code_row_bytes, w.scale_row_bytes, w.gs, w.sdt};
-    const int64_t jobs = P * w.n;
+    const int64_t jobs = P * ep.yn;
     const int64_t blocks = std::min<int64_t>((jobs * 32 + 255) / 256, int64_t(num_sms()) * 8);
     const uint16_t* xb = static_cast<const uint16_t*>(x);
     uint16_t* yb = static_cast<uint16_t*>(y);
 #define QM_EXP_CASE(F, B)                                                                         \
-    experts_simple_kernel<F, B><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ids, id64, P, topk, T, \
+    experts_simple_kernel<F, B><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a, ep, ids, id64, P, topk, T, \
                                                                                xb, x_rows, perm, \
                                                                                offsets, yb)
     if (w.fmt == QM_AFFINE && w.bits == 2) QM_EXP_CASE(QM_AFFINE, 2);

@@ -43,12 +43,13 @@ bool gemm_supported(const WDesc& w, int64_t M) {
     return true;
 }
 
-qm_status launch_gemm(const WDesc& w, const void* x, int64_t M, void* y, cudaStream_t st) {
+qm_status launch_gemm(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st) {
     using namespace gemm;
     Params p{};
     p.scales = w.scales;
     p.biases = w.biases;
     p.y = static_cast<uint16_t*>(y);
+    p.ep = ep;
     p.M = M;
     p.n = w.n;
     p.k = w.k;
@@ -57,7 +58,7 @@ qm_status launch_gemm(const WDesc& w, const void* x, int64_t M, void* y, cudaStr
     p.ksteps = static_cast<int>((w.k + BK - 1) / BK);
     cudaError_t e = dispatch(p, w, x, st);
     if (e == cudaErrorNotSupported) {  // no TMA descriptor for these operands: the plain kernel
-        e = launch_apply_simple(w, x, M, y, st);
+        e = launch_apply_simple(w, ep, x, M, y, st);
         return e == cudaSuccess ? QM_OK : cuda_fail(e, "apply launch");
     }
     if (e != cudaSuccess) return cuda_fail(e, "gemm launch");
@@ -71,7 +72,7 @@ bool gemm_grouped_supported(const WDesc& w, int64_t P) {
     return true;
 }
 
-qm_status launch_gemm_grouped(const WDesc& w, const int32_t* offsets, const int32_t* perm, int64_t P,
+qm_status launch_gemm_grouped(const WDesc& w, const Epi& ep, const int32_t* offsets, const int32_t* perm, int64_t P,
                               const void* xs, void* y, cudaStream_t st) {
     using namespace gemm;
     if (!gemm_grouped_supported(w, P)) return fail(QM_ENOTSUP, "w: no grouped tensor-core plan for this shape");
@@ -79,6 +80,7 @@ qm_status launch_gemm_grouped(const WDesc& w, const int32_t* offsets, const int3
     p.scales = w.scales;
     p.biases = w.biases;
     p.y = static_cast<uint16_t*>(y);
+    p.ep = ep;
     p.M = P;
     p.n = w.n;
     p.k = w.k;

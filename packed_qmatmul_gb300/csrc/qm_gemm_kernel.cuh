@@ -44,6 +44,7 @@
 #include <algorithm>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -102,6 +103,7 @@ struct Params {
     const uint8_t* scales;
     const uint8_t* biases;
     uint16_t* y;
+    Epi ep;              // what becomes of the sums before they are rounded
     int64_t M, n, k;
     int64_t scale_row_bytes;
     int sdt;
@@ -402,6 +404,85 @@ static __device__ __noinline__ void tile_lookup(const Params& p, int mt, int bm,
         before += __shfl_sync(0xffffffffu, inc, 31);
     }
     if (lane == 0) { s_grp[0] = found; s_grp[1] = ge; s_grp[2] = gm0; s_grp[3] = gend; }
+}
+
+// The sums of a warp's 32 rows (this lane's row: row0 + lane) for `cols` tokens from
+// token m0 on (r[c]: token m0 + c), through the epilogue to y. The bias is added
+// while a lane holds one row; act runs there too, or, gated, once lane pairs have
+// swapped values so that each thread holds two adjacent rows (a gate and what is
+// beside it) of one token. Residuals are 4-byte (gated: 2-byte) loads of a row's
+// 64 (32) bytes, issued ahead of all of it. brow0: row0's element of the bias.
+QM_DEV void store_fused(const Params& p, uint32_t (&r)[32], uint8_t* stage, int lane, int64_t row0, int64_t brow0, int64_t m0,
+                        int64_t mend, int cols) {
+    const Epi& e = p.ep;
+    const int odd = lane & 1, two = lane & ~1;
+    const bool gated = e.gated != 0;
+    const int64_t col0 = gated ? row0 >> 1 : row0;               // y's column of the warp's first row
+    const int64_t col = gated ? (row0 + two) >> 1 : row0 + two;  // this thread's, once it holds pairs
+    uint32_t res[16];
+    if (e.residual) {
+        const bool second = !gated && col + 1 < e.yn;
+        // both of a thread's rows in one word where every such word is aligned
+        const bool word = second && !(e.residual_stride & 1) && !(reinterpret_cast<uintptr_t>(e.residual) & 3);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const int64_t m = m0 + c + odd;
+            uint32_t v = 0u;
+            if (c + odd < cols && m < mend && col < e.yn) {
+                const uint16_t* a = e.residual + m * e.residual_stride + col;
+                if (word) v = __ldca(reinterpret_cast<const uint32_t*>(a));
+                else v = static_cast<uint32_t>(__ldca(a)) | (second ? static_cast<uint32_t>(__ldca(a + 1)) << 16 : 0u);
+            }
+            res[c / 2] = v;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) res[c] = 0u;
+    }
+    float v[32];
+    const float b = row0 + lane < p.n ? epi_bias(e, brow0 + lane) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]) + b;
+    if (!gated) act_all<1>(e, v);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {  // rows two, two + 1 of token c + odd
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
+        const float own = odd ? v[c + 1] : v[c];
+        v[c] = odd ? got : own;
+        v[c + 1] = odd ? own : got;
+    }
+    // y's columns of one token lie pitch bytes apart in the stage: 64 + 16, or gated 32 + 16
+    const int pitch = gated ? 48 : 80;
+    if (gated) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) v[c] = clamp_gate(e, v[c]);
+        act_all<2>(e, v);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+            *reinterpret_cast<uint16_t*>(stage + (c + odd) * pitch + lane / 2 * 2) =
+                bf16_bits(fmaf(v[c], clamp_up(e, v[c + 1]), bf16_bits_to_f32(res[c / 2])));
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+            *reinterpret_cast<uint32_t*>(stage + (c + odd) * pitch + lane / 2 * 4) =
+                bf2(v[c] + __uint_as_float(res[c / 2] << 16), v[c + 1] + __uint_as_float(res[c / 2] & 0xFFFF0000u));
+    }
+    __syncwarp();
+    const int64_t m = m0 + lane;
+    const int wide = gated ? 16 : 32;
+    if (lane < cols && m < mend) {
+        const int64_t ym = p.g_off ? static_cast<int64_t>(__ldg(p.g_perm + m)) : m;
+        uint16_t* yr = p.y + ym * e.yn + col0;
+        const uint8_t* src = stage + lane * pitch;
+        if ((e.yn & 7) == 0 && col0 + wide <= e.yn) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (8 * q < wide) reinterpret_cast<uint4*>(yr)[q] = *reinterpret_cast<const uint4*>(src + 16 * q);
+        } else {
+            for (int i = 0; i < wide && col0 + i < e.yn; ++i) yr[i] = reinterpret_cast<const uint16_t*>(src)[i];
+        }
+    }
+    __syncwarp();
 }
 
 template <int FMT, int BITS, int GS, int NTOK, bool DUAL>
@@ -709,7 +790,8 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 uint32_t r[32];
                 load_acc(col, r);
                 if (!ok || s_abort) continue;
-                store32(r, col);
+                if (p.ep.on) store_fused(p, r, stage, lane, row0, wrow0 + row0, m0 + col, mend, 32);
+                else store32(r, col);
             }
         } else {
             // Split k. The tokens are cut into S slices of NTOK / S; CTA q adds
@@ -760,7 +842,9 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 }
                 r[c] = __float_as_uint(v);
             }
-            if (live) {
+            if (live && p.ep.on) {
+                store_fused(p, r, stage, lane, row0, row0, m0 + static_cast<int64_t>(rank) * slice + c0, mend, cols);
+            } else if (live) {
                 // the store's tokens past `cols` belong to the next warp's part: keep them out
                 const int64_t keep_end = mend;
                 const int64_t first = m0 + static_cast<int64_t>(rank) * slice + c0;

@@ -55,6 +55,7 @@
 #include <unordered_map>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -90,6 +91,7 @@ struct Params {
     int M;
     int sdt;
     int64_t code_row_bytes, scale_row_bytes;
+    Epi ep;                  // what becomes of the sums before they are rounded
     // decomposition
     int S;                   // CTAs per cluster, splitting k
     int64_t krange;          // k values per CTA
@@ -429,6 +431,12 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
     };
     int M = p.M;
     int64_t wrow0 = 0;  // first row of this CTA's matrix in the codes and scales
+    // the result of row `row`'s sum v for token m (gated: of an even row's sum and the next row's, u)
+    auto put = [&](int64_t row, int m, float v, float u) {
+        const int64_t yr = p.g_off ? s_pos[m] : m;
+        const int64_t col = p.ep.gated ? row >> 1 : row;
+        p.y[yr * p.ep.yn + col] = p.ep.on ? epi_finish(p.ep, v, u, wrow0 + row, yr, col) : bf16_bits(v);
+    };
     if (p.g_off) {
         // which chunk of which expert: the routing tables come from the previous kernel
         if (warp == 0) {
@@ -959,15 +967,12 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
             // ---- the team's sum in warp order, spread over the team's warps;
             //      then undo the token scale and store
             const int64_t row0 = (stage0 + j) * kRows;
-            auto store = [&](int tt, int nt, int ln, int i, float v) {
+            const bool pairs = p.ep.gated && S == 1;  // a split's pairs meet after the ranks' sums
+            auto store = [&](int tt, int nt, int ln, int i, float v, float u) {
                 const int m = nt * 8 + 2 * (ln & 3) + (i & 1);
                 const int r = 16 * tt + (ln >> 2) + ((i & 2) ? 8 : 0);
                 if (S == 1) {
-                    if (m < M && row0 + r < p.n) {
-                        __nv_bfloat16 bv = __float2bfloat16_rn(v);
-                        const int64_t yr = p.g_off ? s_pos[m] : m;
-                        p.y[yr * p.n + row0 + r] = *reinterpret_cast<uint16_t*>(&bv);
-                    }
+                    if (m < M && row0 + r < p.n) put(row0 + r, m, v, u);
                 } else {
                     partial[(j * kRows + r) * 16 + m] = v;
                 }
@@ -987,19 +992,18 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                 named_bar_sync(2 + team, T * 32);
                 if (live && !s_abort) {
                     const int e = wi * (32 / T) + lane;  // warp wi adds rows [wi*32/T, (wi+1)*32/T)
-                    if (lane < 32 / T) {
-                        float sum = 0.0f;
+                    if (lane < 32 / T && !(pairs && (e & 1))) {  // an even row's lane forms a pair
+                        float sum = 0.0f, beside = 0.0f;
 #pragma unroll 1
                         for (int q = 0; q < T; ++q) sum += base[q * 32 + e];
-                        const float v = sum;
+                        if (pairs) {
+#pragma unroll 1
+                            for (int q = 0; q < T; ++q) beside += base[q * 32 + e + 1];
+                        }
                         if (S == 1) {
-                            if (row0 + e < p.n) {
-                                __nv_bfloat16 bv = __float2bfloat16_rn(v);
-                                const int64_t yr = p.g_off ? s_pos[0] : 0;
-                                p.y[yr * p.n + row0 + e] = *reinterpret_cast<uint16_t*>(&bv);
-                            }
+                            if (row0 + e < p.n) put(row0 + e, 0, sum, beside);
                         } else {
-                            partial[(j * kRows + e) * 16] = v;
+                            partial[(j * kRows + e) * 16] = sum;
                         }
                     }
                 }
@@ -1021,11 +1025,17 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                     // warp wi adds entries [wi*E/T, (wi+1)*E/T) over the team's warps in order
                     #pragma unroll 1
                     for (int e = wi * (E / T) + lane; e < (wi + 1) * (E / T); e += 32) {
-                        float sum = 0.0f;
+                        const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
+                        // rows 2i and 2i + 1 lie four lanes apart, sixteen entries: the even one's thread forms the pair
+                        if (pairs && (ln & 4)) continue;
+                        float sum = 0.0f, beside = 0.0f;
                         #pragma unroll 1
                         for (int q = 0; q < T; ++q) sum += base[q * E + e];
-                        const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
-                        store(tn / NT, tn % NT, ln, i, sum);
+                        if (pairs) {
+                            #pragma unroll 1
+                            for (int q = 0; q < T; ++q) beside += base[q * E + e + 16];
+                        }
+                        store(tn / NT, tn % NT, ln, i, sum, beside);
                     }
                 }
                 buf ^= 1;
@@ -1060,14 +1070,17 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
             for (int e = threadIdx.x; ok && e < ent; e += blockDim.x) {
                 const int rr = e / M, m = e % M;
                 const int64_t row = stage0 * kRows + rr;
-                if (row >= p.n) continue;
-                float sum = 0.0f;
+                if (row >= p.n || (p.ep.gated && (rr & 1))) continue;
+                float sum = 0.0f, beside = 0.0f;
                 sum += own[rr * 16 + m];
                 #pragma unroll 1
                 for (int q = 1; q < S; ++q) sum += recv[(q - 1) * ent + e];
-                __nv_bfloat16 b = __float2bfloat16_rn(sum);
-                const int64_t yr = p.g_off ? s_pos[m] : m;
-                p.y[yr * p.n + row] = *reinterpret_cast<uint16_t*>(&b);
+                if (p.ep.gated) {  // the next row's entry of this token is M entries on
+                    beside += own[(rr + 1) * 16 + m];
+                    #pragma unroll 1
+                    for (int q = 1; q < S; ++q) beside += recv[(q - 1) * ent + e + M];
+                }
+                put(row, m, sum, beside);
             }
         }
     }
@@ -1397,20 +1410,21 @@ bool gemv_supported(const WDesc& w, int64_t M) {
     return pr && pr->pl.ok;
 }
 
-qm_status launch_gemv(const WDesc& w, const void* x, int64_t M, void* y, cudaStream_t st) {
+qm_status launch_gemv(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st) {
     using namespace gemv;
     cudaError_t err = cudaSuccess;
     const Prepared* pr = prepared(w, M, &err);
     if (!pr) return cuda_fail(err, "cudaGetDevice");
     if (!pr->pl.ok) return fail(QM_ENOTSUP, "w: no decode plan for this shape");
     if (!pr->maps) {  // the driver refused a descriptor for this shape: the plain kernel
-        cudaError_t e = launch_apply_simple(w, x, M, y, st);
+        cudaError_t e = launch_apply_simple(w, ep, x, M, y, st);
         return e == cudaSuccess ? QM_OK : cuda_fail(e, "apply launch");
     }
     Plan pl = pr->pl;
     Params& p = pl.p;
     p.x = static_cast<const uint16_t*>(x);
     p.y = static_cast<uint16_t*>(y);
+    p.ep = ep;
     const int ntk = M > 8 ? 2 : (M > 1 ? 1 : 0);
     cudaError_t e = cudaErrorInvalidValue;
 #define QM_GEMV_CASE(F, B, G)                                                                  \
@@ -1463,7 +1477,7 @@ bool gemv_grouped_supported(const WDesc& w, int64_t P) {
     return gemv::grouped_plan(w, P, &pl, &slots);
 }
 
-qm_status launch_gemv_grouped(const WDesc& w, const int32_t* offsets, const int32_t* perm, int64_t P,
+qm_status launch_gemv_grouped(const WDesc& w, const Epi& ep, const int32_t* offsets, const int32_t* perm, int64_t P,
                               int xdiv, const void* x, void* y, cudaStream_t st) {
     using namespace gemv;
     Plan pl;
@@ -1477,6 +1491,7 @@ qm_status launch_gemv_grouped(const WDesc& w, const int32_t* offsets, const int3
     p.biases = w.biases;
     p.x = static_cast<const uint16_t*>(x);
     p.y = static_cast<uint16_t*>(y);
+    p.ep = ep;
     p.n = w.n;
     p.k = w.k;
     p.M = Q;

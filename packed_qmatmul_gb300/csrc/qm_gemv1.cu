@@ -43,6 +43,7 @@
 #include <algorithm>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -76,6 +77,7 @@ struct Args {
     int sdt;             // affine scale dtype
     int nchunk;          // chunks of 1024 inputs: ceil(k / 1024)
     int static_w;        // the weights may be read before the previous kernel ends
+    Epi ep;              // EPI kernels (one weight): what becomes of the sums
     int ks;              // warps splitting one block's chunks (1: a warp takes all of k)
 };
 
@@ -486,7 +488,8 @@ static __device__ __noinline__ float lane_exact(const Args& a, const Part& P, in
     return acc;
 }
 
-template <int FMT, int BITS>
+// EPI: the sums pass through an epilogue, a kernel of its own so that plain products keep theirs.
+template <int FMT, int BITS, bool EPI>
 __global__ void __launch_bounds__(kWarps * 32) gemv1_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31;
     // 32-bit block indices (a block is R rows; fewer than 2^31 blocks) and steps
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kWarps * 32) gemv1_kernel(const __grid_constan
     // and the warps' sums meet in shared memory (added in warp order), so a
     // long row costs one warp's share of k, not all of it, after the wait.
     const int ks = a.ks, kp = static_cast<int>(threadIdx.x >> 5);
-    const bool split = ks > 1;
+    const bool split = ks > 1, kp_stores = kp == 0 || !split;
     const int warp0 = split ? static_cast<int>(blockIdx.x)
                             : static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
     const int nwarp = split ? static_cast<int>(gridDim.x) : static_cast<int>((gridDim.x * blockDim.x) >> 5);
@@ -571,6 +574,15 @@ __global__ void __launch_bounds__(kWarps * 32) gemv1_kernel(const __grid_constan
             have_x = true;
         }
         const Part& P = a.part[cg];
+        // the block's last chunk: bias and residual are on their way while the chunk is summed
+        float bias = 0.0f, residual = 0.0f;
+        if constexpr (EPI) {
+            const int64_t row = static_cast<int64_t>(clb) * R + lane;
+            if (c == c_hi - 1 && kp_stores && lane < R && row < P.n) {
+                bias = epi_bias(a.ep, row);
+                if (!a.ep.gated || lane == 0) residual = epi_residual(a.ep, 0, a.ep.gated ? row >> 1 : row);
+            }
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             bool exact;
@@ -599,8 +611,16 @@ __global__ void __launch_bounds__(kWarps * 32) gemv1_kernel(const __grid_constan
                 }
                 __syncthreads();  // s_red is written again for the next block
             }
-            if (kp == 0 || !split) {
-                if (lane < R && row < P.n) {
+            if (kp_stores) {
+                if constexpr (EPI) {
+                    v += bias;
+                    if (a.ep.gated) {  // lane 0 the gate, lane 1 beside it (n is even: both are rows)
+                        const float u = __shfl_xor_sync(0xffffffffu, v, 1);
+                        if (lane == 0 && row < P.n) P.y[row >> 1] = bf16_bits(epi_gate(a.ep, v, u) + residual);
+                    } else if (lane < R && row < P.n) {
+                        P.y[row] = bf16_bits(epi_act(a.ep, v) + residual);
+                    }
+                } else if (lane < R && row < P.n) {
                     __nv_bfloat16 bv = __float2bfloat16_rn(v);
                     P.y[row] = *reinterpret_cast<uint16_t*>(&bv);
                 }
@@ -624,16 +644,21 @@ __global__ void __launch_bounds__(kWarps * 32) gemv1_kernel(const __grid_constan
     }
 }
 
-template <int FMT, int BITS>
-cudaError_t launch_t(const Args& a, cudaStream_t st) {
+template <int FMT, int BITS, bool EPI>
+cudaError_t launch_e(const Args& a, cudaStream_t st) {
     // all warps resident at once where the rows allow: 16 warps per SM
     const int64_t nb = a.bstart[a.nparts], cap = int64_t(num_sms()) * 16;
     if (a.ks > 1)  // a CTA of ks warps per block
-        return launch_pdl(gemv1_kernel<FMT, BITS>, static_cast<unsigned>(std::min<int64_t>(nb, cap / a.ks)),
+        return launch_pdl(gemv1_kernel<FMT, BITS, EPI>, static_cast<unsigned>(std::min<int64_t>(nb, cap / a.ks)),
                           a.ks * 32, 0, st, a);
     const int64_t warps = std::min<int64_t>(nb, cap);
     const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
-    return launch_pdl(gemv1_kernel<FMT, BITS>, grid, kWarps * 32, 0, st, a);
+    return launch_pdl(gemv1_kernel<FMT, BITS, EPI>, grid, kWarps * 32, 0, st, a);
+}
+
+template <int FMT, int BITS>
+cudaError_t launch_t(const Args& a, cudaStream_t st) {
+    return a.ep.on ? launch_e<FMT, BITS, true>(a, st) : launch_e<FMT, BITS, false>(a, st);
 }
 
 }  // namespace g1
@@ -662,11 +687,13 @@ bool gemv1_many_supported(const WDesc* ws, int count) {
     return blocks < (int64_t(1) << 31);
 }
 
-cudaError_t launch_gemv1_many(const WDesc* ws, int count, const void* x, void* const* ys, cudaStream_t st) {
+cudaError_t launch_gemv1_many(const WDesc* ws, int count, const void* x, void* const* ys, cudaStream_t st,
+                              const Epi* ep) {
     using namespace g1;
     const WDesc& w = ws[0];
     Args a{};
     a.nparts = count;
+    if (ep) a.ep = *ep;
     a.bstart[0] = 0;
     bool all_static = true;
     for (int i = 0; i < count; ++i) {
@@ -712,9 +739,9 @@ cudaError_t launch_gemv1_many(const WDesc* ws, int count, const void* x, void* c
     return launch_t<QM_MXFP4_BLOCKS, 4>(a, st);
 }
 
-cudaError_t launch_gemv1(const WDesc& w, const void* x, void* y, cudaStream_t st) {
+cudaError_t launch_gemv1(const WDesc& w, const Epi& ep, const void* x, void* y, cudaStream_t st) {
     void* ys[1] = {y};
-    return launch_gemv1_many(&w, 1, x, ys, st);
+    return launch_gemv1_many(&w, 1, x, ys, st, &ep);
 }
 
 }  // namespace qm

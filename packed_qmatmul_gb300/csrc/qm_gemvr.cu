@@ -40,6 +40,7 @@
 #include <algorithm>
 
 #include "qm_device.cuh"
+#include "qm_epilogue.cuh"
 #include "qm_internal.h"
 
 namespace qm {
@@ -74,6 +75,7 @@ struct Args {
     int tpc;                    // tiles per CTA (4 / ks where ks <= 2, else 1)
     int nsteps;                 // steps of kStep inputs in one warp's k range
     int static_w;
+    Epi ep;                     // EPI kernels (one weight): what becomes of the sums
 };
 
 QM_DEV void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -221,7 +223,8 @@ static __device__ __noinline__ float exact_sum(const Args& a, const Part& P, int
     return acc;
 }
 
-template <int GS>
+// EPI: the sums pass through an epilogue, a kernel of its own so that plain products keep theirs.
+template <int GS, bool EPI>
 __global__ void __launch_bounds__(kMaxWarps * 32) gemvr_kernel(const __grid_constant__ Args a) {
     using St = Step<GS>;
     constexpr int G = St::G, V = St::V;
@@ -330,12 +333,33 @@ __global__ void __launch_bounds__(kMaxWarps * 32) gemvr_kernel(const __grid_cons
                     y[i] = exact_sum(a, P, row, tok, kbase, kbase + krange, GSHIFT);
             }
         }
-        auto store = [&](const float (&v)[4]) {
+        auto store = [&](const float (&s)[4]) {  // by whole warps
+            float v[4] = {s[0], s[1], s[2], s[3]};
+            if constexpr (EPI) {
+                const float b0 = cr0 + g < P.n ? epi_bias(a.ep, cr0 + g) : 0.0f;
+                const float b8 = cr0 + g + 8 < P.n ? epi_bias(a.ep, cr0 + g + 8) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += (i & 2) ? b8 : b0;
+                if (a.ep.gated) {  // row 2i's lane holds the gate, row 2i + 1's (four lanes on) what is beside it
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = __shfl_xor_sync(0xffffffffu, v[i], 4);
+                        const int64_t row = cr0 + g + ((i & 2) ? 8 : 0);
+                        const int tok = 2 * t + (i & 1);
+                        if (!(g & 1) && row < P.n && tok < a.M)
+                            P.y[tok * a.ep.yn + (row >> 1)] =
+                                bf16_bits(epi_gate(a.ep, v[i], u) + epi_residual(a.ep, tok, row >> 1));
+                    }
+                    return;
+                }
+                act_all<1>(a.ep, v);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t row = cr0 + g + ((i & 2) ? 8 : 0);
                 const int tok = 2 * t + (i & 1);
                 if (row < P.n && tok < a.M) {
+                    if constexpr (EPI) v[i] += epi_residual(a.ep, tok, row);
                     __nv_bfloat16 bv = __float2bfloat16_rn(v[i]);
                     P.y[static_cast<int64_t>(tok) * P.n + row] = *reinterpret_cast<uint16_t*>(&bv);
                 }
@@ -366,13 +390,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32) gemvr_kernel(const __grid_cons
     }
 }
 
-template <int GS>
-static cudaError_t launch_t(const Args& a, cudaStream_t st) {
+template <int GS, bool EPI>
+static cudaError_t launch_e(const Args& a, cudaStream_t st) {
     const int wpc = a.ks * a.tpc;  // warps per CTA
     const int64_t ntiles = a.tstart[a.nparts];
     // all warps resident at once where the tiles allow: 16 warps per SM
     const int64_t ctas = std::min<int64_t>((ntiles + a.tpc - 1) / a.tpc, int64_t(num_sms()) * 16 / wpc);
-    return launch_pdl(gemvr_kernel<GS>, static_cast<unsigned>(std::max<int64_t>(1, ctas)), wpc * 32, 0, st, a);
+    return launch_pdl(gemvr_kernel<GS, EPI>, static_cast<unsigned>(std::max<int64_t>(1, ctas)), wpc * 32, 0, st, a);
+}
+
+template <int GS>
+static cudaError_t launch_t(const Args& a, cudaStream_t st) {
+    return a.ep.on ? launch_e<GS, true>(a, st) : launch_e<GS, false>(a, st);
 }
 
 }  // namespace gr
@@ -396,11 +425,12 @@ bool gemvr_many_supported(const WDesc* ws, int count, int64_t M) {
 }
 
 cudaError_t launch_gemvr_many(const WDesc* ws, int count, const void* x, int64_t M, void* const* ys,
-                              cudaStream_t st) {
+                              cudaStream_t st, const Epi* ep) {
     using namespace gr;
     const WDesc& w = ws[0];
     Args a{};
     a.nparts = count;
+    if (ep) a.ep = *ep;
     a.tstart[0] = 0;
     bool all_static = true;
     for (int i = 0; i < count; ++i) {

@@ -29,6 +29,20 @@ struct WDesc {
     bool is_static = false;       // QM_WEIGHT_STATIC: may be read before the previous kernel ends
 };
 
+// What a product kernel does with its sums before they are rounded (qm_epilogue,
+// validated), and y's shape. Without an epilogue only yn is set.
+struct Epi {
+    const void* bias = nullptr;
+    const uint16_t* residual = nullptr;
+    int64_t residual_stride = 0;
+    int64_t yn = 0;     // elements of a row of y: n, or n/2 where gated
+    int bias_dtype = QM_BF16;
+    int act = QM_ACT_NONE;
+    int gated = 0;
+    int on = 0;         // any of it
+    float alpha = 1.0f, limit = 0.0f, up_offset = 0.0f;  // limit: infinity for none
+};
+
 // Thread-local error message of the calling thread (qm_last_error()).
 void set_error(const std::string& msg);
 qm_status fail(qm_status st, const std::string& msg);
@@ -104,37 +118,38 @@ cudaError_t launch_take_dense(const WDesc& w, int axis, const void* ids, int id6
 // up to 8 weights that read the same x (same format, widths and k) as one
 // grid, y_i for weight i.
 bool gemv1_supported(const WDesc& w);
-cudaError_t launch_gemv1(const WDesc& w, const void* x, void* y, cudaStream_t st);
+cudaError_t launch_gemv1(const WDesc& w, const Epi& ep, const void* x, void* y, cudaStream_t st);
 bool gemv1_many_supported(const WDesc* ws, int count);
-cudaError_t launch_gemv1_many(const WDesc* ws, int count, const void* x, void* const* ys, cudaStream_t st);
+cudaError_t launch_gemv1_many(const WDesc* ws, int count, const void* x, void* const* ys, cudaStream_t st,
+                              const Epi* ep = nullptr);  // ep: with one weight only
 // y_i [M, n_i] = x [M, k] * W_i^T for up to 8 MLX affine 4-bit weights that
 // read the same x, 1 <= M <= 8, k a multiple of 256: weight tiles in registers,
 // products on mma.sync (qm_gemvr.cu).
 bool gemvr_supported(const WDesc& w, int64_t M);
 bool gemvr_many_supported(const WDesc* ws, int count, int64_t M);
 cudaError_t launch_gemvr_many(const WDesc* ws, int count, const void* x, int64_t M, void* const* ys,
-                              cudaStream_t st);
+                              cudaStream_t st, const Epi* ep = nullptr);  // ep: with one weight only
 // y [M, n] = x [M, k] * W^T for a 2-d weight, M <= 16, x and y bf16.
-qm_status launch_gemv(const WDesc& w, const void* x, int64_t M, void* y, cudaStream_t st);
+qm_status launch_gemv(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st);
 bool gemv_supported(const WDesc& w, int64_t M);
 // Grouped decode product over a weight [E, n, k]: chunks of routed positions
 // (offsets [E+1] and perm from the routing step, on the device), activation
 // row of position q is q / xdiv; y [P, n] by position.
-qm_status launch_gemv_grouped(const WDesc& w, const int32_t* offsets, const int32_t* perm, int64_t P,
+qm_status launch_gemv_grouped(const WDesc& w, const Epi& ep, const int32_t* offsets, const int32_t* perm, int64_t P,
                               int xdiv, const void* x, void* y, cudaStream_t st);
 bool gemv_grouped_supported(const WDesc& w, int64_t P);
 // Tensor-core product for larger M (tcgen05); returns QM_ENOTSUP if the
 // shape is outside what the kernel handles.
-qm_status launch_gemm(const WDesc& w, const void* x, int64_t M, void* y, cudaStream_t st);
+qm_status launch_gemm(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y, cudaStream_t st);
 bool gemm_supported(const WDesc& w, int64_t M);
 // Grouped tensor-core product over a weight [E, n, k]: xs holds the routed
 // activation rows expert by expert (offsets [E+1]); row i of the result goes
 // to row perm[i] of y [P, n].
-qm_status launch_gemm_grouped(const WDesc& w, const int32_t* offsets, const int32_t* perm, int64_t P,
+qm_status launch_gemm_grouped(const WDesc& w, const Epi& ep, const int32_t* offsets, const int32_t* perm, int64_t P,
                               const void* xs, void* y, cudaStream_t st);
 bool gemm_grouped_supported(const WDesc& w, int64_t P);
 // Plain reference-order kernel for shapes the fast paths refuse.
-cudaError_t launch_apply_simple(const WDesc& w, const void* x, int64_t M, void* y,
+cudaError_t launch_apply_simple(const WDesc& w, const Epi& ep, const void* x, int64_t M, void* y,
                                 cudaStream_t st);
 
 // Experts.
@@ -145,14 +160,29 @@ size_t experts_workspace_bytes(const WDesc& w, int64_t P, bool allow_tensor);
 cudaError_t launch_route(const void* ids, int id64, int64_t P, int64_t E, int32_t* counts,
                          int32_t* offsets, int32_t* perm, void* ws, cudaStream_t st,
                          uint16_t* zero_y = nullptr, int64_t zero_n = 0);
-qm_status launch_experts(const WDesc& w, const void* ids, int id64, int64_t T, int64_t topk,
+qm_status launch_experts(const WDesc& w, const Epi& ep, const void* ids, int id64, int64_t T, int64_t topk,
                          const void* x, int64_t x_rows, void* y, void* ws, size_t ws_bytes,
                          cudaStream_t st, bool allow_tensor);
 // qm_apply_experts's checks, then launch_experts.
 qm_status apply_experts_checked(const qm_weight* w, const void* ids, int32_t id_type, int64_t T,
                                 int64_t topk, const void* x, int64_t x_rows, int32_t x_dtype, void* y,
                                 void* workspace, size_t workspace_bytes, qm_stream_t stream,
-                                bool allow_tensor);
+                                bool allow_tensor, const qm_epilogue* ep = nullptr);
+
+// The choice of experts and the sum over a token's experts (qm_router.cu); the arguments
+// are validated (qm_layers.cu).
+cudaError_t launch_experts_select(const qm_router& r, const void* logits, int dtype, int64_t stride, int64_t T, int32_t* ids,
+                                  float* weights, cudaStream_t st);
+cudaError_t launch_experts_combine(const void* y, const float* weights, int64_t T, int64_t topk, int64_t n, const void* residual,
+                                   int64_t residual_stride, void* out, cudaStream_t st);
+// The logits a warp's lane holds where 32 / groups lanes (groups rounded up to a power of two)
+// share a group's experts, or 0 where they would be too many.
+int select_width(int experts, int groups, int* lanes_log2);
+
+// Validates ep for a product of M rows and fills e (y's own checks are the product's).
+qm_status validate_epilogue(const qm_epilogue* ep, const WDesc& w, int64_t M, Epi* e);
+// Refuses a bias or residual that y would overwrite while they are read.
+qm_status check_epilogue_overlap(const Epi& e, const WDesc& w, int64_t M, const void* y);
 
 // Head norms, rotation and the paged cache (qm_heads.cu, qm_attend.cu, qm_attend_tc.cu); the
 // arguments are validated (qm_cache.cu).
