@@ -441,8 +441,7 @@ typedef struct qm_router {
     int32_t experts;      /* 1 .. QM_MAX_EXPERTS */
     int32_t topk;         /* 1 .. QM_MAX_TOPK, at most experts */
     int32_t score;        /* qm_score */
-    int32_t groups;       /* 1 .. QM_MAX_GROUPS, dividing experts; QM_ENOTSUP where 32 / groups lanes (groups
-                             rounded up to a power of two) at 32 experts each cannot hold a group */
+    int32_t groups;       /* 1 .. QM_MAX_GROUPS, dividing experts */
     int32_t topk_groups;  /* 1 .. groups */
     int32_t group_score;  /* qm_group_score; QM_GROUP_TOP2 needs two experts to a group */
     int32_t renormalize;  /* 0 or 1 */

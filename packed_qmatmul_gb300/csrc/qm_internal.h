@@ -175,9 +175,6 @@ cudaError_t launch_experts_select(const qm_router& r, const void* logits, int dt
                                   float* weights, cudaStream_t st);
 cudaError_t launch_experts_combine(const void* y, const float* weights, int64_t T, int64_t topk, int64_t n, const void* residual,
                                    int64_t residual_stride, void* out, cudaStream_t st);
-// The logits a warp's lane holds where 32 / groups lanes (groups rounded up to a power of two)
-// share a group's experts, or 0 where they would be too many.
-int select_width(int experts, int groups, int* lanes_log2);
 
 // Validates ep for a product of M rows and fills e (y's own checks are the product's).
 qm_status validate_epilogue(const qm_epilogue* ep, const WDesc& w, int64_t M, Epi* e);

@@ -102,9 +102,6 @@ qm_status qm_experts_select(const qm_router* r, const void* logits, int32_t logi
         return fail(QM_EINVAL, "router: group_score must be QM_GROUP_MAX or QM_GROUP_TOP2");
     if (r->groups > 1 && r->group_score == QM_GROUP_TOP2 && r->experts / r->groups < 2)
         return fail(QM_EINVAL, "router: QM_GROUP_TOP2 needs two experts to a group");
-    int lanes = 0;
-    if (r->topk_groups < r->groups && select_width(r->experts, r->groups, &lanes) == 0)
-        return fail(QM_ENOTSUP, "router: too many experts to a group");
     if (r->renormalize != 0 && r->renormalize != 1) return fail(QM_EINVAL, "router: renormalize must be 0 or 1");
     if (!std::isfinite(r->scale)) return fail(QM_EINVAL, "router: scale must be finite");
     if (reinterpret_cast<uintptr_t>(r->bias) & 3u) return fail(QM_EINVAL, "bias: misaligned");

@@ -145,7 +145,7 @@ static __device__ __noinline__ int select_exact(const Select& a, int64_t t, int 
     }
     // without a bias the logits order the experts, as in the float32 path
     int got = -1;
-    uint32_t taken = 0u;  // of this lane's experts
+    uint64_t taken = 0u;  // of this lane's experts
     for (int r = 0; r < a.topk; ++r) {
         double best = -INFINITY;
         int idx = 0x7FFFFFFF, slot = 0;
@@ -171,7 +171,7 @@ static __device__ __noinline__ int select_exact(const Select& a, int64_t t, int 
             }
         }
         if (idx == 0x7FFFFFFF) break;  // none left, for every lane
-        if (idx == own) taken |= 1u << slot;
+        if (idx == own) taken |= uint64_t(1) << slot;
         if (lane == r) got = idx;
     }
     return got;
@@ -362,19 +362,11 @@ cudaError_t by_width(const Select& a, int width, cudaStream_t st) {
     if (width <= 4) return launch_select<4, GROUPS>(a, st);
     if (width <= 8) return launch_select<8, GROUPS>(a, st);
     if (width <= 16) return launch_select<16, GROUPS>(a, st);
-    return launch_select<32, GROUPS>(a, st);
+    if (width <= 32) return launch_select<32, GROUPS>(a, st);
+    return launch_select<64, GROUPS>(a, st);  // 1024 experts in 2^i + 1 .. groups: fewer than twice 32 to a lane
 }
 
 }  // namespace
-
-int select_width(int experts, int groups, int* lanes_log2) {
-    int g2 = 0;
-    while ((1 << g2) < groups) ++g2;
-    *lanes_log2 = 5 - g2;
-    const int lanes = 1 << *lanes_log2, gsize = experts / groups;
-    const int width = (gsize + lanes - 1) / lanes;
-    return width <= 32 ? width : 0;
-}
 
 cudaError_t launch_experts_select(const qm_router& r, const void* logits, int dtype, int64_t stride, int64_t T, int32_t* ids,
                                   float* weights, cudaStream_t st) {
@@ -395,7 +387,10 @@ cudaError_t launch_experts_select(const qm_router& r, const void* logits, int dt
     a.sigmoid = r.score == QM_SCORE_SIGMOID;
     a.renormalize = r.renormalize;
     a.scale = r.scale;
-    const int width = select_width(r.experts, a.groups, &a.lanes_log2);
+    int g2 = 0;
+    while ((1 << g2) < a.groups) ++g2;
+    a.lanes_log2 = 5 - g2;
+    const int width = ((a.gsize - 1) >> a.lanes_log2) + 1;  // logits that a lane holds
     return a.groups > 1 ? by_width<true>(a, width, st) : by_width<false>(a, width, st);
 }
 

@@ -336,7 +336,8 @@ def select64(logits, topk, score="softmax", bias=None, groups=1, topk_groups=Non
             if renormalize:
                 if score == "sigmoid":  # in the logarithm, where scores are too small to add
                     ls = -np.logaddexp(0, -row[order])
-                    got = np.exp(ls - np.logaddexp.reduce(ls))
+                    got = np.exp(ls - ls.max())
+                    got = got / got.sum()
                 else:
                     got = np.exp(row[order] - row[order].max())
                     got = got / got.sum()
@@ -366,7 +367,7 @@ SELECTS = [
     dict(E=160, topk=6, groups=8, topk_groups=3, renormalize=False, scale=16.0), dict(E=72, topk=5, groups=3, topk_groups=2, group_score="top2"),
     dict(E=100, topk=30, groups=5, topk_groups=1), dict(E=96, topk=4, groups=32, topk_groups=7, score="sigmoid", group_score="top2"),
     dict(E=64, topk=3, groups=4, topk_groups=4, group_score="top2", bias=True), dict(E=960, topk=9, groups=6, topk_groups=2, bias=True, score="sigmoid"),
-    dict(E=12, topk=3, groups=12, topk_groups=2), dict(E=544, topk=5, groups=17, topk_groups=3, bias=True, group_score="top2"),
+    dict(E=1020, topk=8, groups=17, topk_groups=4, score="sigmoid", group_score="top2"), dict(E=12, topk=3, groups=12, topk_groups=2), dict(E=544, topk=5, groups=17, topk_groups=3, bias=True, group_score="top2"),
 ]
 
 
