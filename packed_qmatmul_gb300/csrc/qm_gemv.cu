@@ -944,6 +944,25 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                 do_group(gi, acc0);
                 epilogue(gi, acc0, raw0);
             }
+            // Rows past n (of a ragged last stage) hold whatever their slot held before: a lane
+            // that such a row sent to the element-by-element sums looks again without it, so
+            // that the rows beside it are summed the same way in every run.
+            const int nrow = static_cast<int>(std::min<int64_t>(kRows, p.n - (stage0 + j) * kRows));
+            if (nrow < kRows && big != 0 && !xbad) {
+                big = 0;
+                #pragma unroll 1
+                for (int q = gb; q < gend; ++q) {
+                    uint32_t raw[2][4];
+                    ep_load(q, raw);
+#pragma unroll
+                    for (int tt = 0; tt < 2; ++tt) {
+                        if (16 * tt + g >= nrow) raw[tt][0] = raw[tt][2] = 0u;
+                        if (16 * tt + g + 8 >= nrow) raw[tt][1] = raw[tt][3] = 0u;
+                        float s0, s8, b0, b8;
+                        if (scales_of(raw[tt], s0, s8, b0, b8)) big |= 1u << tt;
+                    }
+                }
+            }
             // the stage's sums at their true size: one power-of-two product per
             // output (exact), or the element-by-element sums of a big tile; both
             // before the stage's slot is released

@@ -174,6 +174,26 @@ def test_residual_strides_and_in_place(M):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M", [1, 5, 12])
+def test_rows_past_the_last_do_not_decide(M):
+    """A ragged last stage's missing rows hold what an earlier launch left in shared memory: whatever that is, the
+    rows beside them are summed the same way. k = 1600 keeps whole rows of scales in a stage; the launches between
+    leave scales of every size there."""
+    n, k = 33002 if M == 1 else 1002, 1600  # one token: a weight past 24 MB, for the tensor-map pipeline
+    w = qm.QWeight.from_arrays(synth.affine_weight(synth.rng(5), n, k, bits=4, group_size=32))
+    x = torch.randn(M, k, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    want = None
+    for scale in (0.0, 1.0, 2.0 ** 100, float("inf"), float("nan"), 2.0 ** -100):
+        fill = synth.affine_weight(synth.rng(7), (n + 31) // 32 * 32, k, bits=4, group_size=32)
+        f = qm.QWeight.from_arrays(fill)
+        f.scales.view(torch.bfloat16).fill_(scale)
+        f.biases.view(torch.bfloat16).fill_(scale)
+        qm.apply(f, x)
+        y = qm.apply(w, x)
+        want = y if want is None else want
+        assert torch.equal(y, want), scale
+
+
 def test_exact_sums_round_once():
     """Zero products: bias, activation and residual alone, rounded once."""
     n, k = 256, 256
