@@ -55,18 +55,21 @@ QM_DEV float load_logit(const Select& a, int64_t t, int e) {
     return a.dtype == QM_F16 ? f16_bits_to_f32(h) : bf16_bits_to_f32(h);
 }
 
-// Float order as unsigned order; 0 is below every number. Zeros of both signs meet.
+// Float order as unsigned order, zeros of both signs as one, shifted so that -infinity is 0:
+// what stands for an expert that cannot be chosen. +infinity is kTop, a NaN of either sign above it.
+constexpr uint32_t kNone = 0u, kLow = 0x007FFFFFu, kTop = 0xFF800000u - kLow;
 QM_DEV uint32_t ordered(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u)) - kLow;
 }
-QM_DEV float unordered(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+QM_DEV float unordered(uint32_t k) {
+    k += kLow;
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
 
-constexpr uint32_t kNone = 0u;
-
-// 1 / (1 + exp(-x)): expf is within 2 units and the sum and quotient within half a
-// unit each, so it is off by at most 2^-22 of itself.
-QM_DEV float sigmoid_key(float x) {
+// 1 / (1 + exp(-x)) for a weight: expf is within 2 units and the sum and quotient
+// within half a unit each, so it is off by at most 2^-22 of itself.
+QM_DEV float sigmoid_weight(float x) {
     const float t = expf(-fabsf(x));
     return __fdiv_rn(x < 0.0f ? t : 1.0f, 1.0f + t);
 }
@@ -177,193 +180,440 @@ static __device__ __noinline__ int select_exact(const Select& a, int64_t t, int 
     return got;
 }
 
-template <int V, bool GROUPS>
-__global__ void __launch_bounds__(kSelectWarps * 32) select_kernel(const __grid_constant__ Select a) {
+// Scores for the order alone. exp2 of the scaled argument is off by 2^-22 and 2^-23 for each
+// unit of the argument (softmax: and 2^-24, the difference's rounding), the reciprocal and the
+// sum below it by 2^-22.4. z exp(-z) stays below 0.37, so of a score, at most 1, the error is
+// below 2^-20; softmax adds up to 37 roundings of its sum, below 2^-18 in all. Results below 2^-126 are 0.
+QM_DEV float exp_fast(float v) {
+    float t;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(v * 1.44269504f));
+    return t;
+}
+QM_DEV float sigmoid_score(float l) {
+    const float t = exp_fast(-fabsf(l));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + t));
+    return l < 0.0f ? t * r : r;
+}
+QM_DEV float score_of(const Select& a, float l, float top, float inv_sum) {
+    return a.sigmoid ? sigmoid_score(l) : exp_fast(l - top) * inv_sum;
+}
+QM_DEV float most_error(const Select& a) { return a.sigmoid ? 0x1p-20f : 0x1p-17f; }
+
+// The key of expert e with logit l, as an ordered integer.
+QM_DEV uint32_t key_of(const Select& a, float l, int e, float top, float inv_sum) {
+    float k = l;
+    if (a.bias) k = l > -INFINITY ? score_of(a, l, top, inv_sum) + __ldg(a.bias + e) : -INFINITY;
+    const uint32_t key = ordered(k);
+    return key <= kTop ? key : kNone;  // NaN
+}
+
+// Keys nearer than this may change places: both errors, the sums' roundings, and as much again.
+QM_DEV float key_margin(const Select& a, float k) { return 4.0f * most_error(a) + 0x1p-21f * fabsf(k); }
+
+// The choice among many equal or nearly equal keys, one after another (`stays`: this lane's group
+// does): lane r receives the r-th chosen expert (-1: none). Sets *near where float32 cannot tell the order.
+template <int V>
+static __device__ __noinline__ int select_ties(const Select& a, int64_t t, int lane, bool stays, float top, float inv_sum, bool* near) {
+    const Place at(a, lane);
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = at.base + (i << a.lanes_log2);
+        key[i] = stays && i < at.count ? key_of(a, load_logit(a, t, e), e, top, inv_sum) : kNone;
+    }
+    int idx = -1;
+    uint32_t picked = kNone;
+    const int picks = a.topk + (a.bias ? 1 : 0);
+    for (int r = 0; r < picks; ++r) {
+        uint32_t mk = kNone;
+        int mi = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > mk) {
+                mk = key[i];
+                mi = i;
+            }
+        const uint32_t best = __reduce_max_sync(kFull, mk);
+        if (best == kNone) break;
+        const int mine = mk == best ? at.base + (mi << a.lanes_log2) : 0x7FFFFFFF;
+        const int low = __reduce_min_sync(kFull, mine);
+        if (mine == low) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i == mi) key[i] = kNone;
+        }
+        if (lane == r) {
+            idx = low;
+            picked = best;
+        }
+    }
+    *near = false;
+    if (a.bias) {
+        const uint32_t next = __shfl_down_sync(kFull, picked, 1);
+        const int next_idx = __shfl_down_sync(kFull, idx, 1);
+        bool close = false;
+        if (lane < a.topk && idx >= 0 && next_idx >= 0) {
+            const float x = unordered(picked), y = unordered(next);
+            if (!(x - y > key_margin(a, x)))
+                close = load_logit(a, t, idx) != load_logit(a, t, next_idx) || __ldg(a.bias + idx) != __ldg(a.bias + next_idx);
+        }
+        *near = __any_sync(kFull, close);
+    }
+    return lane < a.topk ? idx : -1;
+}
+
+// A score whose order counts, in float64: of softmax without a bias up to a factor.
+static __device__ __noinline__ double score_exact(const Select& a, float l, float top) {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - static_cast<double>(top));
+}
+
+// A warp's list of candidates: key above, complement of the expert's index below, so that
+// the greater entry goes first. 0: none.
+QM_DEV uint64_t entry_of(uint32_t key, int e) { return (static_cast<uint64_t>(key) << 32) | ~static_cast<uint32_t>(e); }
+QM_DEV int expert_of(uint64_t entry) { return static_cast<int>(~static_cast<uint32_t>(entry)); }
+
+// Every lane's keys from `from` on, side by side in the list; returns how many (more than 32:
+// the list is not whole). Its first 32 entries are otherwise 0.
+template <int V>
+QM_DEV int gather(const Select& a, const uint32_t (&key)[V], uint32_t from, int base, uint64_t* list) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t before = (1u << lane) - 1u;
+    list[lane] = 0u;
+    __syncwarp();
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] >= from;
+        const uint32_t who = __ballot_sync(kFull, in);
+        const int at = n + __popc(who & before);
+        if (in && at < 32) list[at] = entry_of(key[i], base + (i << a.lanes_log2));
+        n += __popc(who);
+    }
+    __syncwarp();
+    return n;
+}
+
+// Two largest keys of a lane's group: its own experts', then over the group's lanes.
+template <int V>
+QM_DEV void group_top2(const Select& a, const uint32_t (&key)[V], uint32_t& m1, uint32_t& m2) {
+    m1 = m2 = kNone;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
+    }
+    for (int o = 1; o < (1 << a.lanes_log2); o <<= 1) {
+        const uint32_t p1 = __shfl_xor_sync(kFull, m1, o), p2 = __shfl_xor_sync(kFull, m2, o);
+        m2 = max(min(m1, p1), max(m2, p2));
+        m1 = max(m1, p1);
+    }
+}
+
+// A group's score from its two largest keys (-infinity: kNone), and a bound on its error:
+// of a sum of scores that no bias joins relative to them and up to a factor that all share.
+QM_DEV uint32_t group_score(const Select& a, uint32_t m1, uint32_t m2, float top, float inv_sum, float* err) {
+    *err = a.bias ? most_error(a) : 0.0f;
+    if (!a.top2) return m1;
+    if (m2 == kNone) return kNone;
+    const float k1 = unordered(m1), k2 = unordered(m2);
+    if (a.bias) {
+        *err = 2.0f * most_error(a);
+        return ordered(k1 + k2);
+    }
+    const float s1 = score_of(a, k1, top, inv_sum), s2 = score_of(a, k2, top, inv_sum);
+    const float z1 = fabsf(a.sigmoid ? k1 : k1 - top), z2 = fabsf(a.sigmoid ? k2 : k2 - top);
+    *err = s1 * fmaf(z1, 0x1p-22f, 0x1p-20f) + s2 * fmaf(z2, 0x1p-22f, 0x1p-20f) + 0x1p-124f;
+    return ordered(s1 + s2);
+}
+
+// Whether this lane's group stays, where scores about the border lie nearer than float32 can tell:
+// the groups within `tol` of the last that stayed, x, and the first that did not, y, are ranked
+// anew by float64 keys. One above x + tol is passed only by groups that stay as well, one below
+// y - tol by any that stays. Sets *all where more than that is to be done in float64.
+template <int V>
+static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane, float top, float inv_sum, float x, float y, float tol,
+                                            uint64_t* list, double* exact, bool* all) {
+    const Place at(a, lane);
+    uint32_t key[V], m1, m2;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = at.base + (i << a.lanes_log2);
+        key[i] = i < at.count ? key_of(a, load_logit(a, t, e), e, top, inv_sum) : kNone;
+    }
+    group_top2<V>(a, key, m1, m2);
+    float err;
+    const uint32_t mine = group_score(a, m1, m2, top, inv_sum, &err);
+    const float m = unordered(mine);
+    const bool real = at.group < a.groups && mine != kNone;
+    const bool above = real && m > x + tol, band = real && !above && !(m < y - tol);
+    // the elements that may be a group's largest: within both errors of the last of them
+    const uint32_t cut = a.top2 ? m2 : m1;
+    const float cv = unordered(cut);
+    const uint32_t from = !band || cut == kNone ? 0xFFFFFFFFu : (a.bias ? max(ordered(cv - key_margin(a, cv)), 1u) : cut);
+    const int n = gather<V>(a, key, from, at.base, list);
+    *all = n > 32 || (a.bias && !a.sigmoid) || !(fabsf(x) < INFINITY);
+    if (*all) return false;
+    if (lane < n) {
+        const int e = expert_of(list[lane]);
+        exact[lane] = score_exact(a, load_logit(a, t, e), top) + (a.bias ? __ldg(a.bias + e) : 0.0f);
+    }
+    __syncwarp();
+    double e1 = -INFINITY, e2 = -INFINITY;
+    for (int j = 0; j < n; ++j) {
+        if (expert_of(list[j]) / a.gsize != at.group) continue;
+        e2 = fmax(e2, fmin(e1, exact[j]));
+        e1 = fmax(e1, exact[j]);
+    }
+    const double score = a.top2 ? e1 + e2 : e1;
+    const uint32_t in_band = __ballot_sync(kFull, band), over = __ballot_sync(kFull, above);
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const int leader = g << a.lanes_log2;
+        const double other = __shfl_sync(kFull, score, leader);
+        if ((over >> leader) & 1u) ++rank;
+        else if ((in_band >> leader) & 1u) rank += other > score || (other == score && g < at.group);
+    }
+    __syncwarp();  // the list is written again
+    return above || (band && rank < a.topk_groups);
+}
+
+// HALF: 16-bit logits.
+template <int V, bool GROUPS, bool HALF>
+__global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kernel(const __grid_constant__ Select a) {
+    __shared__ uint64_t s_list[kSelectWarps][32];
+    __shared__ double s_exact[kSelectWarps][32];
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
+    uint64_t* list = s_list[threadIdx.x >> 5];
     const int64_t nw = static_cast<int64_t>(gridDim.x) * kSelectWarps;
     const Place at(a, lane);
+    const int step = GROUPS ? a.lanes_log2 : 5;
     const bool keyed = a.bias != nullptr;          // keys are sums, else the logits themselves
-    const bool softmax_sum = !a.sigmoid && (keyed || !a.renormalize || (GROUPS && a.top2));
+    const bool softmax_sum = !a.sigmoid && (keyed || !a.renormalize);
+    const int picks = a.topk + (keyed ? 1 : 0);    // with inexact keys one more: the first not chosen
+    float bias[V];
+    if (keyed) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) bias[i] = i < at.count ? __ldg(a.bias + at.base + (i << step)) : 0.0f;
+    }
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kSelectWarps + (threadIdx.x >> 5); t < a.T; t += nw) {
-        float l[V];
         uint32_t key[V];
-        bool bad = false;
-        float top = -INFINITY;
+        uint32_t mk = kNone;  // the largest of this lane's keys
+        float top = 0.0f, inv_sum = 1.0f;
+        {
+            float l[V];
+            if constexpr (HALF) {
+                const uint16_t* row = static_cast<const uint16_t*>(a.logits) + t * a.stride + at.base;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            l[i] = i < at.count ? load_logit(a, t, at.base + (i << a.lanes_log2)) : -INFINITY;
-            bad = bad || l[i] != l[i] || l[i] == INFINITY;
-            top = fmaxf(top, l[i]);
-        }
-        if (!a.sigmoid && __any_sync(kFull, bad)) {  // no softmax
-            if (lane < a.topk) {
-                a.ids[t * a.topk + lane] = -1;
-                a.weights[t * a.topk + lane] = __uint_as_float(0x7FC00000u);
+                for (int i = 0; i < V; ++i) {
+                    const uint32_t h = i < at.count ? __ldca(row + (i << step)) : 0u;
+                    l[i] = a.dtype == QM_F16 ? f16_bits_to_f32(h) : bf16_bits_to_f32(h);
+                    if (i >= at.count) l[i] = -INFINITY;
+                }
+            } else {
+                const float* row = static_cast<const float*>(a.logits) + t * a.stride + at.base;
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = i < at.count ? __ldca(row + (i << step)) : -INFINITY;
             }
-            continue;
-        }
-        float sum = 1.0f;
-        if (softmax_sum) {
-            top = unordered(__reduce_max_sync(kFull, ordered(top)));
-            sum = 0.0f;
+            if (!(keyed && a.sigmoid)) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-        }
-        // A score's error, relative to it: sigmoid 2^-22; softmax 2^-17 (2^-22 for the exponential, up to
-        // 104 * 2^-24 for its argument, 37 * 2^-24 for the sum). Of a score, at most 1, it is no more
-        // than 2^-18, since s log(1 / s) < 1/2. A key adds half a unit of its sum with the bias.
-        const float rel = a.sigmoid ? 0x1p-22f : 0x1p-17f, most_err = a.sigmoid ? 0x1p-22f : 0x1p-18f;
-        auto score = [&](float v) { return a.sigmoid ? sigmoid_key(v) : expf(v - top) / sum; };
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float k = l[i];
-            if (keyed && i < at.count) {
-                const float b = __ldg(a.bias + at.base + (i << a.lanes_log2));
-                k = l[i] > -INFINITY && b > -INFINITY ? score(l[i]) + b : -INFINITY;
+                for (int i = 0; i < V; ++i) {
+                    key[i] = ordered(l[i]);
+                    mk = max(mk, key[i]);
+                }
             }
-            key[i] = k > -INFINITY ? ordered(k) : kNone;
+            if (!a.sigmoid) {
+                const uint32_t best = __reduce_max_sync(kFull, mk);
+                if (best >= kTop) {  // NaN or +infinity: no softmax
+                    if (lane < a.topk) {
+                        a.ids[t * a.topk + lane] = -1;
+                        a.weights[t * a.topk + lane] = __uint_as_float(0x7FC00000u);
+                    }
+                    continue;
+                }
+                top = unordered(best);
+                if (softmax_sum) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum += key[i] != kNone ? expf(l[i] - top) : 0.0f;
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+                    inv_sum = 1.0f / sum;
+                }
+            }
+            if (keyed) {
+                mk = kNone;
+                if (a.sigmoid) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) key[i] = ordered(l[i] > -INFINITY ? sigmoid_score(l[i]) + bias[i] : -INFINITY);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) key[i] = ordered(l[i] > -INFINITY ? exp_fast(l[i] - top) * inv_sum + bias[i] : -INFINITY);
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) mk = max(mk, key[i]);
+            }
+            if (mk > kTop) {  // a NaN is never chosen
+                mk = kNone;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (key[i] > kTop) key[i] = kNone;
+                    mk = max(mk, key[i]);
+                }
+            }
         }
-        bool near = false;  // an order that float32 cannot tell
+        bool exact_all = false;  // for select_exact
+        bool stays = true;       // this lane's group
         if (GROUPS) {
-            uint32_t m1 = kNone, m2 = kNone;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                m2 = max(m2, min(m1, key[i]));
-                m1 = max(m1, key[i]);
-            }
-            for (int o = 1; o < (1 << a.lanes_log2); o <<= 1) {
-                const uint32_t p1 = __shfl_xor_sync(kFull, m1, o), p2 = __shfl_xor_sync(kFull, m2, o);
-                m2 = max(min(m1, p1), max(m2, p2));
-                m1 = max(m1, p1);
-            }
-            uint32_t mine = m1;
-            if (a.top2) {
-                if (m2 == kNone) mine = kNone;
-                else if (keyed) mine = ordered(unordered(m1) + unordered(m2));
-                else mine = ordered(score(unordered(m1)) + score(unordered(m2)));
-            }
+            uint32_t m1, m2;
+            group_top2<V>(a, key, m1, m2);
+            float err;
+            const uint32_t mine = group_score(a, m1, m2, top, inv_sum, &err);
             int rank = 0;
             for (int g = 0; g < a.groups; ++g) {
                 const uint32_t other = __shfl_sync(kFull, mine, g << a.lanes_log2);
                 rank += other > mine || (other == mine && g < at.group);
             }
-            const bool real = at.group < a.groups, stays = rank < a.topk_groups;
+            const bool real = at.group < a.groups;
+            stays = real && rank < a.topk_groups;
             if (keyed || a.top2) {
-                const uint32_t least = __reduce_min_sync(kFull, real && stays ? mine : 0xffffffffu);
-                const uint32_t most = __reduce_max_sync(kFull, real && !stays ? mine : kNone);
-                if (least != kNone && most != kNone) {
-                    const float x = unordered(least), y = unordered(most);
-                    // two keys' errors and their sum's rounding on either side, and as much again
-                    near = !(x - y > (keyed ? 8.0f * most_err : 4.0f * rel * (x + y)) + 0x1p-21f * (fabsf(x) + fabsf(y)));
+                const uint32_t low = __reduce_min_sync(kFull, stays ? mine : 0xFFFFFFFFu);
+                const uint32_t high = __reduce_max_sync(kFull, real && !stays ? mine : kNone);
+                if (low != kNone && high != kNone) {  // the last group that stays, the first that does not
+                    const float x = unordered(low), y = unordered(high);
+                    if (!keyed) err = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(real ? err : 0.0f)));
+                    else err = a.top2 ? 2.0f * most_error(a) : most_error(a);
+                    // both errors, the sums' roundings, and as much again
+                    const float tol = 4.0f * err + 0x1p-21f * (fabsf(x) + fabsf(y));
+                    if (!(x - y > tol))
+                        stays = regroup<V>(a, t, lane, top, inv_sum, x, y, tol, list, s_exact[threadIdx.x >> 5], &exact_all);
                 }
             }
-            if (!stays) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) key[i] = kNone;
-            }
+            if (!stays) mk = kNone;
         }
-        // the largest keys one after another; with inexact keys one more, the first that is not chosen
-        int idx = -1;
-        uint32_t picked = kNone;
-        if (!near) {
-            uint32_t mk = kNone;
-            int mi = 0;
-            auto local_best = [&]() {
-                mk = kNone;
-                mi = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (key[i] > mk) {
-                        mk = key[i];
-                        mi = i;
-                    }
-            };
-            local_best();
-            const int picks = a.topk + (keyed ? 1 : 0);
+        // Candidates: every key from the topk-th largest of the lanes' own largest on (with inexact keys the
+        // next, and a margin), no fewer than are chosen and seldom many more. A lane each.
+        int n = 0, expert = -1, rank = 32;  // this lane's candidate and its place
+        if (!exact_all) {
+            uint32_t from = kNone;
             for (int r = 0; r < picks; ++r) {
-                const uint32_t best = __reduce_max_sync(kFull, mk);
-                if (best == kNone) break;
-                const int mine = at.base + (mi << a.lanes_log2);
-                uint32_t who = __ballot_sync(kFull, mk == best);
-                if (who & (who - 1)) {  // several lanes: the lowest index
-                    const int low = __reduce_min_sync(kFull, mk == best ? mine : 0x7FFFFFFF);
-                    who = __ballot_sync(kFull, mk == best && mine == low);
-                }
-                const int src = __ffs(who) - 1;
-                const int e = __shfl_sync(kFull, mine, src);
-                if (lane == r) {
-                    idx = e;
-                    picked = best;
-                }
-                if (lane == src) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (i == mi) key[i] = kNone;
-                    local_best();
+                from = __reduce_max_sync(kFull, mk);
+                if (mk == from) mk = kNone;
+            }
+            if (from == kNone) {
+                from = 1u;  // all there are
+            } else if (keyed) {
+                const float f = unordered(from);
+                from = fabsf(f) < INFINITY ? max(ordered(f - key_margin(a, f)), 1u) : 1u;
+            }
+            n = gather<V>(a, key, stays ? from : 0xFFFFFFFFu, at.base, list);
+            if (n > 32) {  // as many equal or nearly equal keys
+                bool near;
+                expert = select_ties<V>(a, t, lane, stays, top, inv_sum, &near);
+                exact_all = near;
+                rank = expert >= 0 ? lane : 32;
+                n = __popc(__ballot_sync(kFull, expert >= 0));
+            } else {
+                const uint64_t own = list[lane];
+                rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) rank += list[j] > own;
+                if (lane < n) expert = expert_of(own);
+                else rank = 32;
+                if (keyed) {
+                    const float kf = unordered(static_cast<uint32_t>(own >> 32)), tol = key_margin(a, kf);
+                    __syncwarp();
+                    if (lane < n) list[rank] = own;  // in order now; beyond n still 0
+                    __syncwarp();
+                    const uint32_t k0 = static_cast<uint32_t>(list[lane] >> 32), k1 = lane + 1 < n ? static_cast<uint32_t>(list[lane + 1] >> 32) : kNone;
+                    // neighbours nearer than their errors
+                    bool close = lane < a.topk && k1 != kNone && !(unordered(k0) - unordered(k1) > key_margin(a, unordered(k0)));
+                    if (__any_sync(kFull, close)) {
+                        const float l = lane < n ? load_logit(a, t, expert) : 0.0f, b = lane < n ? __ldg(a.bias + expert) : 0.0f;
+                        close = false;  // but not the same sum of the same two
+                        for (int j = 0; j < n; ++j) {
+                            const float lj = __shfl_sync(kFull, l, j), bj = __shfl_sync(kFull, b, j);
+                            const float kj = __shfl_sync(kFull, kf, j);
+                            close = close || (!(fabsf(kf - kj) > tol) && (lj != l || bj != b));
+                        }
+                        if (__any_sync(kFull, close && rank < a.topk)) {
+                            if (!a.sigmoid) {
+                                exact_all = true;
+                            } else {
+                                double* exact = s_exact[threadIdx.x >> 5];
+                                const double mine = score_exact(a, l, top) + b;
+                                exact[lane] = mine;
+                                __syncwarp();
+                                rank = 0;
+                                for (int j = 0; j < n; ++j) {
+                                    const int ej = __shfl_sync(kFull, expert, j);
+                                    rank += exact[j] > mine || (exact[j] == mine && ej < expert);
+                                }
+                                if (lane >= n) rank = 32;
+                            }
+                        }
+                    }
                 }
             }
-            if (keyed) {
-                // neighbours of the order nearer than their errors, but not the same sum of the same two
-                const uint32_t next = __shfl_down_sync(kFull, picked, 1);
-                const int next_idx = __shfl_down_sync(kFull, idx, 1);
-                bool close = false;
-                if (lane < a.topk && idx >= 0 && next_idx >= 0) {
-                    const float x = unordered(picked), y = unordered(next);
-                    const float bx = __ldg(a.bias + idx), by = __ldg(a.bias + next_idx);
-                    // both errors, and as much again
-                    if (!(x - y > 2.0f * rel * (fabsf(x - bx) + fabsf(y - by)) + 0x1p-22f * (fabsf(x) + fabsf(y))))
-                        close = load_logit(a, t, idx) != load_logit(a, t, next_idx) || bx != by;
-                }
-                near = __any_sync(kFull, close);
-            }
+            __syncwarp();  // the list is written again
         }
-        if (near) idx = select_exact<V>(a, t, lane);
-        // weights, from the chosen logits anew
-        const bool on = lane < a.topk && idx >= 0;
-        const float x = on ? load_logit(a, t, idx) : -INFINITY;
+        if (exact_all) {  // lane r holds the r-th
+            expert = select_exact<V>(a, t, lane);
+            rank = expert >= 0 ? lane : 32;
+            n = __popc(__ballot_sync(kFull, expert >= 0));
+        }
+        const bool on = rank < a.topk;
+        const float l = on ? load_logit(a, t, expert) : -INFINITY;
         float w = 0.0f;
         if (a.renormalize) {
             // scores over their sum, all of them times exp(-high) where that is below zero: no score of
             // very negative logits is lost
-            const float high = unordered(__reduce_max_sync(kFull, ordered(x)));
+            const float high = unordered(__reduce_max_sync(kFull, ordered(l)));
             const float shift = a.sigmoid ? fminf(high, 0.0f) : high;
             if (on) {
-                if (!a.sigmoid) w = expf(x - shift);
-                else w = x <= 0.0f ? expf(x - shift) / (1.0f + expf(x)) : sigmoid_key(x);
+                if (!a.sigmoid) w = expf(l - shift);
+                else w = l <= 0.0f ? __fdividef(expf(l - shift), 1.0f + expf(l)) : sigmoid_weight(l);
             }
             float all = w;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
-            if (on) w = w / all;
+            if (on) w = __fdividef(w, all);  // all is in [1/2, 31]
         } else if (on) {
-            w = a.sigmoid ? sigmoid_key(x) : expf(x - top) / sum;
+            w = a.sigmoid ? sigmoid_weight(l) : expf(l - top) * inv_sum;
         }
-        if (lane < a.topk) {
-            a.ids[t * a.topk + lane] = on ? idx : -1;
-            a.weights[t * a.topk + lane] = w * a.scale;
+        if (on) {
+            a.ids[t * a.topk + rank] = expert;
+            a.weights[t * a.topk + rank] = w * a.scale;
+        }
+        if (lane >= n && lane < a.topk) {  // fewer than topk to choose from
+            a.ids[t * a.topk + lane] = -1;
+            a.weights[t * a.topk + lane] = 0.0f;
         }
     }
 }
 
 template <int V, bool GROUPS>
 cudaError_t launch_select(const Select& a, cudaStream_t st) {
-    const int64_t blocks = std::min<int64_t>((a.T + kSelectWarps - 1) / kSelectWarps, int64_t(num_sms()) * 16);
-    return launch_pdl(select_kernel<V, GROUPS>, static_cast<unsigned>(blocks), kSelectWarps * 32, 0, st, a);
+    // as many warps as stay resident: a warp reads the bias once
+    const int64_t blocks = std::min<int64_t>((a.T + kSelectWarps - 1) / kSelectWarps, int64_t(num_sms()) * 8);
+    return launch_pdl(a.dtype == QM_F32 ? select_kernel<V, GROUPS, false> : select_kernel<V, GROUPS, true>, static_cast<unsigned>(blocks),
+                      kSelectWarps * 32, 0, st, a);
 }
 
-template <bool GROUPS>
 cudaError_t by_width(const Select& a, int width, cudaStream_t st) {
-    if (width <= 1) return launch_select<1, GROUPS>(a, st);
-    if (width <= 2) return launch_select<2, GROUPS>(a, st);
-    if (width <= 4) return launch_select<4, GROUPS>(a, st);
-    if (width <= 8) return launch_select<8, GROUPS>(a, st);
-    if (width <= 16) return launch_select<16, GROUPS>(a, st);
-    if (width <= 32) return launch_select<32, GROUPS>(a, st);
-    return launch_select<64, GROUPS>(a, st);  // 1024 experts in 2^i + 1 .. groups: fewer than twice 32 to a lane
+    if (a.groups > 1) {
+        if (width <= 4) return launch_select<4, true>(a, st);
+        if (width <= 8) return launch_select<8, true>(a, st);
+        if (width <= 16) return launch_select<16, true>(a, st);
+        if (width <= 32) return launch_select<32, true>(a, st);
+        return launch_select<64, true>(a, st);  // 1024 experts in 2^i + 1 .. groups: fewer than twice 32 to a lane
+    }
+    if (width <= 4) return launch_select<4, false>(a, st);
+    if (width <= 8) return launch_select<8, false>(a, st);
+    if (width <= 16) return launch_select<16, false>(a, st);
+    return launch_select<32, false>(a, st);
 }
 
 }  // namespace
@@ -391,7 +641,7 @@ cudaError_t launch_experts_select(const qm_router& r, const void* logits, int dt
     while ((1 << g2) < a.groups) ++g2;
     a.lanes_log2 = 5 - g2;
     const int width = ((a.gsize - 1) >> a.lanes_log2) + 1;  // logits that a lane holds
-    return a.groups > 1 ? by_width<true>(a, width, st) : by_width<false>(a, width, st);
+    return by_width(a, width, st);
 }
 
 // ---------------------------------------------------------------- the sum over a token's experts
