@@ -263,9 +263,20 @@ static __device__ __noinline__ int select_ties(const Select& a, int64_t t, int l
     return lane < a.topk ? idx : -1;
 }
 
-// A score whose order counts, in float64: of softmax without a bias up to a factor.
-static __device__ __noinline__ double score_exact(const Select& a, float l, float top) {
-    return a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - static_cast<double>(top));
+// Float64 order as signed order, zeros of both signs as one: float64 arithmetic has 1/64 of float32's
+// rate here, its comparisons too.
+QM_DEV int64_t ordered64(double v) {
+    const int64_t u = __double_as_longlong(v);
+    return u < 0 ? static_cast<int64_t>(0x8000000000000000ull) - u : u;
+}
+QM_DEV double unordered64(int64_t k) {
+    return __longlong_as_double(k < 0 ? static_cast<int64_t>(0x8000000000000000ull) - k : k);
+}
+constexpr int64_t kNone64 = static_cast<int64_t>(0x8000000000000001ull);  // below -infinity
+
+// A key whose order counts, from a logit and its bias: of softmax without a bias up to a factor.
+static __device__ __noinline__ double key_exact(const Select& a, float l, float b, float top) {
+    return (a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l))) : exp(static_cast<double>(l) - static_cast<double>(top))) + b;
 }
 
 // A warp's list of candidates: key above, complement of the expert's index below, so that
@@ -294,6 +305,16 @@ QM_DEV int gather(const Select& a, const uint32_t (&key)[V], uint32_t from, int 
     return n;
 }
 
+// Two largest keys over a group's lanes.
+QM_DEV void join_top2(const Select& a, uint32_t& m1, uint32_t& m2) {
+#pragma unroll 1
+    for (int o = 1; o < (1 << a.lanes_log2); o <<= 1) {
+        const uint32_t p1 = __shfl_xor_sync(kFull, m1, o), p2 = __shfl_xor_sync(kFull, m2, o);
+        m2 = max(min(m1, p1), max(m2, p2));
+        m1 = max(m1, p1);
+    }
+}
+
 // Two largest keys of a lane's group: its own experts', then over the group's lanes.
 template <int V>
 QM_DEV void group_top2(const Select& a, const uint32_t (&key)[V], uint32_t& m1, uint32_t& m2) {
@@ -303,11 +324,7 @@ QM_DEV void group_top2(const Select& a, const uint32_t (&key)[V], uint32_t& m1, 
         m2 = max(m2, min(m1, key[i]));
         m1 = max(m1, key[i]);
     }
-    for (int o = 1; o < (1 << a.lanes_log2); o <<= 1) {
-        const uint32_t p1 = __shfl_xor_sync(kFull, m1, o), p2 = __shfl_xor_sync(kFull, m2, o);
-        m2 = max(min(m1, p1), max(m2, p2));
-        m1 = max(m1, p1);
-    }
+    join_top2(a, m1, m2);
 }
 
 // A group's score from its two largest keys (-infinity: kNone), and a bound on its error:
@@ -333,15 +350,18 @@ QM_DEV uint32_t group_score(const Select& a, uint32_t m1, uint32_t m2, float top
 // y - tol by any that stays. Sets *all where more than that is to be done in float64.
 template <int V>
 static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane, float top, float inv_sum, float x, float y, float tol,
-                                            uint64_t* list, double* exact, bool* all) {
+                                            uint64_t* list, int64_t* exact, bool* all) {
     const Place at(a, lane);
-    uint32_t key[V], m1, m2;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+    // Loops are not unrolled here: what a rare call waits for is its instructions.
+    uint32_t key[V], m1 = kNone, m2 = kNone;
+#pragma unroll 1
+    for (int i = 0; i < at.count; ++i) {
         const int e = at.base + (i << a.lanes_log2);
-        key[i] = i < at.count ? key_of(a, load_logit(a, t, e), e, top, inv_sum) : kNone;
+        key[i] = key_of(a, load_logit(a, t, e), e, top, inv_sum);
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
     }
-    group_top2<V>(a, key, m1, m2);
+    join_top2(a, m1, m2);
     float err;
     const uint32_t mine = group_score(a, m1, m2, top, inv_sum, &err);
     const float m = unordered(mine);
@@ -351,26 +371,41 @@ static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane
     const uint32_t cut = a.top2 ? m2 : m1;
     const float cv = unordered(cut);
     const uint32_t from = !band || cut == kNone ? 0xFFFFFFFFu : (a.bias ? max(ordered(cv - key_margin(a, cv)), 1u) : cut);
-    const int n = gather<V>(a, key, from, at.base, list);
+    list[lane] = 0u;
+    __syncwarp();
+    int n = 0;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        const bool in = i < at.count && key[i] >= from;
+        const uint32_t who = __ballot_sync(kFull, in);
+        const int place = n + __popc(who & ((1u << lane) - 1u));
+        if (in && place < 32) list[place] = entry_of(key[i], at.base + (i << a.lanes_log2));
+        n += __popc(who);
+    }
+    __syncwarp();
     *all = n > 32 || (a.bias && !a.sigmoid) || !(fabsf(x) < INFINITY);
     if (*all) return false;
     if (lane < n) {
         const int e = expert_of(list[lane]);
-        exact[lane] = score_exact(a, load_logit(a, t, e), top) + (a.bias ? __ldg(a.bias + e) : 0.0f);
+        exact[lane] = ordered64(key_exact(a, load_logit(a, t, e), a.bias ? __ldg(a.bias + e) : 0.0f, top));
     }
     __syncwarp();
-    double e1 = -INFINITY, e2 = -INFINITY;
+    int64_t e1 = kNone64, e2 = kNone64;
+    const int first = at.group * a.gsize;
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-        if (expert_of(list[j]) / a.gsize != at.group) continue;
-        e2 = fmax(e2, fmin(e1, exact[j]));
-        e1 = fmax(e1, exact[j]);
+        const int e = expert_of(list[j]) - first;
+        if (e < 0 || e >= a.gsize) continue;
+        e2 = max(e2, min(e1, exact[j]));
+        e1 = max(e1, exact[j]);
     }
-    const double score = a.top2 ? e1 + e2 : e1;
+    const int64_t score = a.top2 && band ? ordered64(unordered64(e1) + unordered64(e2)) : e1;
     const uint32_t in_band = __ballot_sync(kFull, band), over = __ballot_sync(kFull, above);
     int rank = 0;
+#pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
         const int leader = g << a.lanes_log2;
-        const double other = __shfl_sync(kFull, score, leader);
+        const int64_t other = __shfl_sync(kFull, score, leader);
         if ((over >> leader) & 1u) ++rank;
         else if ((in_band >> leader) & 1u) rank += other > score || (other == score && g < at.group);
     }
@@ -382,7 +417,7 @@ static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane
 template <int V, bool GROUPS, bool HALF>
 __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kernel(const __grid_constant__ Select a) {
     __shared__ uint64_t s_list[kSelectWarps][32];
-    __shared__ double s_exact[kSelectWarps][32];
+    __shared__ int64_t s_exact[kSelectWarps][32];
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
@@ -471,11 +506,15 @@ __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kern
             group_top2<V>(a, key, m1, m2);
             float err;
             const uint32_t mine = group_score(a, m1, m2, top, inv_sum, &err);
+            // how many groups go before this one: its lanes look at a share of them each
+            const int lanes = 1 << a.lanes_log2;
             int rank = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const uint32_t other = __shfl_sync(kFull, mine, g << a.lanes_log2);
-                rank += other > mine || (other == mine && g < at.group);
+            for (int g0 = 0; g0 < a.groups; g0 += lanes) {
+                const int g = g0 + (lane & (lanes - 1));
+                const uint32_t other = __shfl_sync(kFull, mine, (g << a.lanes_log2) & 31);
+                rank += g < a.groups && (other > mine || (other == mine && g < at.group));
             }
+            for (int o = 1; o < lanes; o <<= 1) rank += __shfl_xor_sync(kFull, rank, o);
             const bool real = at.group < a.groups;
             stays = real && rank < a.topk_groups;
             if (keyed || a.top2) {
@@ -533,6 +572,7 @@ __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kern
                     if (__any_sync(kFull, close)) {
                         const float l = lane < n ? load_logit(a, t, expert) : 0.0f, b = lane < n ? __ldg(a.bias + expert) : 0.0f;
                         close = false;  // but not the same sum of the same two
+#pragma unroll 1
                         for (int j = 0; j < n; ++j) {
                             const float lj = __shfl_sync(kFull, l, j), bj = __shfl_sync(kFull, b, j);
                             const float kj = __shfl_sync(kFull, kf, j);
@@ -542,11 +582,12 @@ __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kern
                             if (!a.sigmoid) {
                                 exact_all = true;
                             } else {
-                                double* exact = s_exact[threadIdx.x >> 5];
-                                const double mine = score_exact(a, l, top) + b;
+                                int64_t* exact = s_exact[threadIdx.x >> 5];
+                                const int64_t mine = ordered64(key_exact(a, l, b, top));
                                 exact[lane] = mine;
                                 __syncwarp();
                                 rank = 0;
+#pragma unroll 1
                                 for (int j = 0; j < n; ++j) {
                                     const int ej = __shfl_sync(kFull, expert, j);
                                     rank += exact[j] > mine || (exact[j] == mine && ej < expert);
