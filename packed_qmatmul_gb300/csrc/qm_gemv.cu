@@ -107,7 +107,8 @@ struct Params {
     int g_E;
     int g_Q;                 // positions per chunk
     int g_xdiv;              // activation row of position q: q / g_xdiv
-    int g_wclusters;         // clusters per chunk
+    int g_wclusters;         // clusters per chunk (a k split; else the chunks' number decides, on the device)
+    int g_resident;          // without a k split: CTAs resident at once. 0: g_wclusters clusters to a chunk
     // shared memory layout (byte offsets from the dynamic smem base)
     uint32_t nstage, stage_bytes;
     uint32_t code_seg, nbox;          // per row: bytes of codes; 128-byte boxes per stage
@@ -322,11 +323,40 @@ static __device__ __noinline__ float2 group_exact(CodeRow ra, CodeRow rb, int gi
     return make_float2(acc_a, acc_b);
 }
 
-// Grouped mode, one warp: which chunk cluster slot `slot` is -- its size
-// (s_grp[0], 0 past the last chunk), expert (s_grp[1]), positions and
-// activation rows -- from the routing offsets, 32 experts per step.
-static __device__ __noinline__ void group_lookup(const Params& p, int slot, int lane, int* s_grp, int* s_pos,
-                                                 int* s_xrow) {
+// Grouped mode, one warp: which share of which chunk cluster `cluster` takes --
+// the chunk's size (s_grp[0], 0 past the last chunk), expert (s_grp[1]), positions and
+// activation rows, the share (s_share[0]) and its 32-row stages (s_share[1]) -- from
+// the routing offsets, 32 experts per step.
+//
+// Without a k split the chunks there are, not those that P positions might make, divide
+// the GPU: each takes `w` CTAs, as many as leave all of them resident at once, or, where
+// there are more than half as many chunks as resident CTAs, the w of 1 .. 32 whose waves
+// hold the fewest stages. (Cut for the chunks expected, 64 positions over 32 experts of
+// 5760 x 2880 ran 336 CTAs on 304 places, almost twice the stages: 165 us, now 100.) A row is
+// summed the same way whichever CTA holds its stage.
+static __device__ __noinline__ void group_lookup(const Params& p, int cluster, int lane, int* s_grp, int* s_pos,
+                                                 int* s_xrow, int* s_share) {
+    int w = p.g_wclusters, spc = p.stages_per_cluster;
+    if (p.g_resident) {
+        int chunks = 0;
+        for (int e = lane; e < p.g_E; e += 32)
+            chunks += (__ldg(p.g_off + e + 1) - __ldg(p.g_off + e) + p.g_Q - 1) / p.g_Q;
+        chunks = max(1, __reduce_add_sync(0xffffffffu, chunks));
+        const int n_stages = static_cast<int>(p.n_stages), most = max(1, static_cast<int>(gridDim.x) / chunks);
+        if (2 * chunks <= p.g_resident) {
+            w = min(min(p.g_resident / chunks, most), n_stages);
+        } else {
+            const int mine = min(min(lane + 1, most), n_stages);
+            const uint32_t waves = (static_cast<uint32_t>(chunks) * mine + p.g_resident - 1) / p.g_resident;
+            const uint32_t cost = waves * ((n_stages + mine - 1) / mine);
+            const uint32_t best = __reduce_min_sync(0xffffffffu, cost);
+            w = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1);
+        }
+        spc = (n_stages + w - 1) / w;
+        w = (n_stages + spc - 1) / spc;
+    }
+    const int slot = cluster / w;
+    if (lane == 0) { s_share[0] = cluster % w; s_share[1] = spc; }
     int before = 0;  // chunks of the experts already passed
     int gm = 0, ge = 0, gb = 0;
     for (int e0 = 0; e0 < p.g_E; e0 += 32) {
@@ -402,6 +432,7 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
     int* s_pos = reinterpret_cast<int*>(smem + 368);        // [16]
     int* s_xrow = reinterpret_cast<int*>(smem + 432);       // [16], ends at 496
     volatile int& s_xbad = *reinterpret_cast<volatile int*>(smem + 496);  // an activation is inf or NaN
+    int* s_share = reinterpret_cast<int*>(smem + 500);      // [2]: this cluster's share of the chunk, its stages
 
     unsigned int* xmax = reinterpret_cast<unsigned int*>(smem + p.off_tokscale) + 32;  // [16] max |x| as bf16 bits
     if (threadIdx.x == 0) {
@@ -429,7 +460,7 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
         grid_dependency_wait();
         grid_launch_dependents();
     };
-    int M = p.M;
+    int M = p.M, spc = p.stages_per_cluster;
     int64_t wrow0 = 0;  // first row of this CTA's matrix in the codes and scales
     // the result of row `row`'s sum v for token m (gated: of an even row's sum and the next row's, u)
     auto put = [&](int64_t row, int m, float v, float u) {
@@ -441,16 +472,17 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
         // which chunk of which expert: the routing tables come from the previous kernel
         if (warp == 0) {
             wait_prev();
-            group_lookup(p, static_cast<int>(cluster / p.g_wclusters), lane, s_grp, s_pos, s_xrow);
+            group_lookup(p, cluster, lane, s_grp, s_pos, s_xrow, s_share);
         }
         __syncthreads();
         M = s_grp[0];
         if (M == 0) return;  // a slot past the last chunk; the same for every CTA of the cluster
         wrow0 = static_cast<int64_t>(s_grp[1]) * p.n;
-        cluster = static_cast<int>(cluster % p.g_wclusters);
+        cluster = s_share[0];
+        spc = s_share[1];
     }
-    const int64_t stage0 = cluster * p.stages_per_cluster;
-    const int nst = static_cast<int>(std::min<int64_t>(p.stages_per_cluster, p.n_stages - stage0));
+    const int64_t stage0 = static_cast<int64_t>(cluster) * spc;
+    const int nst = static_cast<int>(std::min<int64_t>(spc, p.n_stages - stage0));
     if (S > 1) cluster_arrive_relaxed();  // waited for before the first access to another CTA
     // x comes from the previous kernel; so may W, unless the caller marked it
     // static, in which case the producer streams its first stages before waiting
@@ -1535,7 +1567,14 @@ qm_status launch_gemv_grouped(const WDesc& w, const Epi& ep, const int32_t* offs
     }
     if (!maps) return fail(QM_ENOTSUP, "w: no tensor map for the grouped decode product");
     if (pl.grid * slots >= (int64_t(1) << 31)) return fail(QM_ENOTSUP, "ids: too many positions for one launch");
-    pl.grid *= slots;
+    if (pl.S > 1) {
+        pl.grid *= slots;
+    } else {
+        // a CTA for every place and every chunk there may be; where the chunks may take more than
+        // half the places, three waves, so that they can be cut finer (CTAs past the last share exit)
+        p.g_resident = num_sms() * (pl.cw == 16 ? 1 : 2);
+        pl.grid = std::max<int64_t>(slots, p.g_resident * (2 * slots > p.g_resident ? 3 : 1));
+    }
     const bool two = Q > 8;
     cudaError_t e = cudaErrorInvalidValue;
 #define QM_GEMV_CASE(F, B, G)                                                                  \
