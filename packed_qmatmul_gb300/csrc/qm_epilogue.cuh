@@ -61,13 +61,18 @@ QM_DEV float clamp_up(const Epi& e, float u) { return (u > e.limit ? e.limit : (
 
 QM_DEV float epi_gate(const Epi& e, float g, float u) { return epi_act(e, clamp_gate(e, g)) * clamp_up(e, u); }
 
-// Element `i` of the bias (0 without one).
-QM_DEV float epi_bias(const Epi& e, int64_t i) {
-    if (!e.bias) return 0.0f;
-    if (e.bias_dtype == QM_F32) return __ldg(static_cast<const float*>(e.bias) + i);
-    const uint32_t h = __ldg(static_cast<const uint16_t*>(e.bias) + i);
-    return e.bias_dtype == QM_F16 ? f16_bits_to_f32(h) : bf16_bits_to_f32(h);
+// Element `i` of the bias as its bits, and their value: apart, so that a load can be under way
+// while something else is done.
+QM_DEV uint32_t epi_bias_bits(const Epi& e, int64_t i) {
+    if (e.bias_dtype == QM_F32) return __ldg(static_cast<const uint32_t*>(e.bias) + i);
+    return __ldg(static_cast<const uint16_t*>(e.bias) + i);
 }
+QM_DEV float epi_bias_value(const Epi& e, uint32_t bits) {
+    return e.bias_dtype == QM_F32 ? __uint_as_float(bits) : e.bias_dtype == QM_F16 ? f16_bits_to_f32(bits) : bf16_bits_to_f32(bits);
+}
+
+// Element `i` of the bias (0 without one).
+QM_DEV float epi_bias(const Epi& e, int64_t i) { return e.bias ? epi_bias_value(e, epi_bias_bits(e, i)) : 0.0f; }
 
 // The residual of result (row, col) (0 without one): a coherent load, since y may be
 // the residual and an earlier kernel may just have written it.
@@ -80,13 +85,26 @@ QM_DEV uint16_t bf16_bits(float v) {
     return *reinterpret_cast<const uint16_t*>(&b);
 }
 
-// One result from its sum v (gated: the gate's v and the sum u beside it): bias
-// elements from brow on, result (row, col). Out of line, for the kernels that finish
-// few results to a thread: their loops keep their registers.
-static __device__ __noinline__ uint16_t epi_finish(const Epi& e, float v, float u, int64_t brow, int64_t row, int64_t col) {
-    v += epi_bias(e, brow);
-    v = e.gated ? epi_gate(e, v, u + epi_bias(e, brow + 1)) : epi_act(e, v);
-    return bf16_bits(v + epi_residual(e, row, col));
+// The activation of v, or of the gate v times u, both with their bias. Out of line and by
+// value, for the kernels that finish few results to a thread: their loops keep their registers.
+static __device__ __noinline__ float epi_value(int act, int gated, float alpha, float limit, float up_offset, float v, float u) {
+    Epi e;
+    e.act = act;
+    e.alpha = alpha;
+    e.limit = limit;
+    e.up_offset = up_offset;
+    return gated ? epi_gate(e, v, u) : epi_act(e, v);
+}
+
+// One result (row, col) from its sum v (gated: the gate's v and the sum u beside it), both with their bias.
+QM_DEV uint16_t epi_result(const Epi& e, float v, float u, int64_t row, int64_t col) {
+    const float r = epi_residual(e, row, col);
+    return bf16_bits(epi_value(e.act, e.gated, e.alpha, e.limit, e.up_offset, v, u) + r);
+}
+
+// The same with bias elements from brow on still to be added.
+QM_DEV uint16_t epi_finish(const Epi& e, float v, float u, int64_t brow, int64_t row, int64_t col) {
+    return epi_result(e, v + epi_bias(e, brow), e.gated ? u + epi_bias(e, brow + 1) : 0.0f, row, col);
 }
 
 }  // namespace qm

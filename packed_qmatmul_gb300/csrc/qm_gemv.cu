@@ -462,11 +462,11 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
     };
     int M = p.M, spc = p.stages_per_cluster;
     int64_t wrow0 = 0;  // first row of this CTA's matrix in the codes and scales
-    // the result of row `row`'s sum v for token m (gated: of an even row's sum and the next row's, u)
+    // the result of row `row`'s sum v for token m (gated: of an even row's sum and the next row's, u), biases added
     auto put = [&](int64_t row, int m, float v, float u) {
         const int64_t yr = p.g_off ? s_pos[m] : m;
         const int64_t col = p.ep.gated ? row >> 1 : row;
-        p.y[yr * p.ep.yn + col] = p.ep.on ? epi_finish(p.ep, v, u, wrow0 + row, yr, col) : bf16_bits(v);
+        p.y[yr * p.ep.yn + col] = p.ep.on ? epi_result(p.ep, v, u, yr, col) : bf16_bits(v);
     };
     if (p.g_off) {
         // which chunk of which expert: the routing tables come from the previous kernel
@@ -785,6 +785,13 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                 slot += nteams;
                 while (slot >= p.nstage) { slot -= p.nstage; ++fill; }
             }
+            // the stage's 32 biases, a row to a lane, on their way while the stage is summed (asked
+            // for at its end they come through a memory system full of weights: 8 us of 82)
+            uint32_t bias_bits = 0u;
+            if (p.ep.bias && S == 1) {
+                const int64_t row = (stage0 + j) * kRows + lane;
+                if (row < p.n) bias_bits = epi_bias_bits(p.ep, wrow0 + row);
+            }
             bool live = !s_abort;
             // A slot's first fill needs no tag: its barrier's first phase can only
             // be that fill. Later fills check that the producer has started stage j.
@@ -1043,16 +1050,21 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                 named_bar_sync(2 + team, T * 32);
                 if (live && !s_abort) {
                     const int e = wi * (32 / T) + lane;  // warp wi adds rows [wi*32/T, (wi+1)*32/T)
+                    float be = 0.0f, bn = 0.0f;
+                    if (p.ep.bias) {
+                        const float bias = epi_bias_value(p.ep, bias_bits);
+                        be = __shfl_sync(0xffffffffu, bias, e & 31);
+                        bn = __shfl_sync(0xffffffffu, bias, (e + 1) & 31);
+                    }
                     if (lane < 32 / T && !(pairs && (e & 1))) {  // an even row's lane forms a pair
                         float sum = 0.0f, beside = 0.0f;
 #pragma unroll 1
-                        for (int q = 0; q < T; ++q) sum += base[q * 32 + e];
-                        if (pairs) {
-#pragma unroll 1
-                            for (int q = 0; q < T; ++q) beside += base[q * 32 + e + 1];
+                        for (int q = 0; q < T; ++q) {
+                            sum += base[q * 32 + e];
+                            if (pairs) beside += base[q * 32 + e + 1];
                         }
                         if (S == 1) {
-                            if (row0 + e < p.n) put(row0 + e, 0, sum, beside);
+                            if (row0 + e < p.n) put(row0 + e, 0, sum + be, beside + bn);
                         } else {
                             partial[(j * kRows + e) * 16] = sum;
                         }
@@ -1072,21 +1084,36 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                         *reinterpret_cast<float4*>(mine + ((tt * NT + nt) * 32 + lane) * 4) =
                             make_float4(y[tt][nt][0], y[tt][nt][1], y[tt][nt][2], y[tt][nt][3]);
                 named_bar_sync(2 + team, T * 32);
-                if (live && !s_abort) {
+                if (live && !s_abort && (!p.ep.on || S > 1)) {
                     // warp wi adds entries [wi*E/T, (wi+1)*E/T) over the team's warps in order
                     #pragma unroll 1
                     for (int e = wi * (E / T) + lane; e < (wi + 1) * (E / T); e += 32) {
-                        const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
-                        // rows 2i and 2i + 1 lie four lanes apart, sixteen entries: the even one's thread forms the pair
-                        if (pairs && (ln & 4)) continue;
-                        float sum = 0.0f, beside = 0.0f;
+                        float sum = 0.0f;
                         #pragma unroll 1
                         for (int q = 0; q < T; ++q) sum += base[q * E + e];
-                        if (pairs) {
-                            #pragma unroll 1
-                            for (int q = 0; q < T; ++q) beside += base[q * E + e + 16];
+                        const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
+                        store(tn / NT, tn % NT, ln, i, sum, 0.0f);
+                    }
+                } else if (live && !s_abort) {
+                    // the same before an epilogue; of pairs as large a share of the even rows'
+                    // entries: rows 2i and 2i + 1 lie four lanes apart, sixteen entries
+                    const int share = (pairs ? E / 2 : E) / T;
+                    const float bias = p.ep.bias ? epi_bias_value(p.ep, bias_bits) : 0.0f;
+                    #pragma unroll 1
+                    for (int o0 = 0; o0 < share; o0 += 32) {
+                        const int o = wi * share + o0 + lane;
+                        const int e = pairs ? ((o & ~15) << 1 | (o & 15)) : o;
+                        const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
+                        const int r = 16 * (tn / NT) + (ln >> 2) + ((i & 2) ? 8 : 0);
+                        const float be = __shfl_sync(0xffffffffu, bias, r & 31), bn = __shfl_sync(0xffffffffu, bias, (r + 1) & 31);
+                        if (o0 + lane >= share) continue;
+                        float sum = 0.0f, beside = 0.0f;
+                        #pragma unroll 1
+                        for (int q = 0; q < T; ++q) {
+                            sum += base[q * E + e];
+                            if (pairs) beside += base[q * E + e + 16];
                         }
-                        store(tn / NT, tn % NT, ln, i, sum, beside);
+                        store(tn / NT, tn % NT, ln, i, sum + be, beside + bn);
                     }
                 }
                 buf ^= 1;
@@ -1130,8 +1157,9 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                     beside += own[(rr + 1) * 16 + m];
                     #pragma unroll 1
                     for (int q = 1; q < S; ++q) beside += recv[(q - 1) * ent + e + M];
+                    beside += epi_bias(p.ep, wrow0 + row + 1);
                 }
-                put(row, m, sum, beside);
+                put(row, m, sum + epi_bias(p.ep, wrow0 + row), beside);
             }
         }
     }
