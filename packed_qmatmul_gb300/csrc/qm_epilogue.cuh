@@ -2,12 +2,16 @@
 // rounding: bias, activation or gate, residual (qm_epilogue), shared by every
 // product kernel.
 //
-// sigmoid(z) is formed from t = exp(-|z|) <= 1, as 1 / (1 + t) or t / (1 + t), so
-// that nothing overflows and small results keep their relative precision:
-// exp2 of the scaled argument and the quotient are the fast forms, off by at most
-// 2^-21 + |z| 2^-23 relative (the argument's rounding), far below bf16's 2^-9
-// wherever the result is not itself below 1e-38. tanh in gelu is the same sigmoid,
-// (1 + tanh z) / 2 = sigmoid(2 z), and 1 + erf is erfc, which keeps the tail.
+// v / (1 + exp(-z)) is v times the reciprocal of 1 + 2^(-z log2 e), two special-function
+// results and three products: exp2 is off by 2^-22 and, through its argument's rounding,
+// by |z| 2^-23 relative, the reciprocal by 2^-23, both far below bf16's 2^-9. An
+// exponential that overflows gives v times 0, and results below 2^-118 in size may
+// come out as 0. tanh in gelu is the same: (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)).
+//
+// gelu's (1 + erf(v / sqrt 2)) / 2 is half of erfc(z) = exp(-z^2) g(z), z = |v| / sqrt 2, or 1 less
+// that: g falls from 1 like 1 / z, and g(z) / t, t = 1 / (1 + 0.46 z), is a polynomial of
+// degree 7 in t to 2^-20 of itself over z >= 0 (a least-squares fit reweighted towards its
+// largest relative error), so that the tail keeps its relative precision.
 #pragma once
 
 #include "qm_device.cuh"
@@ -15,30 +19,63 @@
 
 namespace qm {
 
-QM_DEV float sigmoid_f(float z) {
-    const float t = __expf(-fabsf(z));
-    return __fdividef(z < 0.0f ? t : 1.0f, 1.0f + t);  // z NaN: t NaN
+QM_DEV float ex2_ftz(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+QM_DEV float rcp_ftz(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// Maximum and minimum that keep a NaN.
+QM_DEV float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+QM_DEV float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// Out of line: the one activation of more than a dozen instructions.
-static __device__ __noinline__ float gelu_f(float v) { return 0.5f * v * erfcf(v * -0.70710678f); }
+constexpr float kLog2e = 1.44269504f;
 
+QM_DEV float gelu_f(float v) {
+    const float z = fabsf(v) * 0.70710678f, t = rcp_ftz(fmaf(0.46f, z, 1.0f));
+    float g = 0.06773512f;
+    g = fmaf(g, t, -0.22670604f);
+    g = fmaf(g, t, 0.16930445f);
+    g = fmaf(g, t, 0.05252517f);
+    g = fmaf(g, t, 0.18688236f);
+    g = fmaf(g, t, 0.23117466f);
+    g = fmaf(g, t, 0.25955793f);
+    g = fmaf(g, t, 0.25952703f);
+    const float q = 0.5f * t * g * ex2_ftz(z * z * -kLog2e);
+    return v * (v < 0.0f ? q : 1.0f - q);
+}
+
+// neg_alpha: -alpha log2 e.
 template <int ACT>
-QM_DEV float act_f(float v, float alpha) {
-    if constexpr (ACT == QM_ACT_RELU) return v < 0.0f ? 0.0f : v;  // NaN stays
-    if constexpr (ACT == QM_ACT_SILU) return v * sigmoid_f(alpha * v);
+QM_DEV float act_f(float v, float neg_alpha) {
+    if constexpr (ACT == QM_ACT_RELU) return max_nan(v, 0.0f);
+    if constexpr (ACT == QM_ACT_SILU) return v * rcp_ftz(1.0f + ex2_ftz(v * neg_alpha));
     if constexpr (ACT == QM_ACT_GELU) return gelu_f(v);
-    if constexpr (ACT == QM_ACT_GELU_TANH) return v * sigmoid_f(1.5957691f * fmaf(0.044715f * v * v, v, v));
+    if constexpr (ACT == QM_ACT_GELU_TANH)  // 2 sqrt(2 / pi) log2 e (v + 0.044715 v^3)
+        return v * rcp_ftz(1.0f + ex2_ftz(v * fmaf(v * v, -0.10294324f, -2.3022082f)));
     return v;
 }
 
 // v[0], v[STEP], ... through the activation.
 template <int STEP, int N>
 QM_DEV void act_all(const Epi& e, float (&v)[N]) {
+    const float neg_alpha = e.alpha * -kLog2e;
     switch (e.act) {
 #define QM_ACT_CASE(A)                                                                      \
     case A:                                                                                 \
-        _Pragma("unroll") for (int i = 0; i < N; i += STEP) v[i] = act_f<A>(v[i], e.alpha); \
+        _Pragma("unroll") for (int i = 0; i < N; i += STEP) v[i] = act_f<A>(v[i], neg_alpha); \
         break;
         QM_ACT_CASE(QM_ACT_RELU)
         QM_ACT_CASE(QM_ACT_SILU)
@@ -56,8 +93,8 @@ QM_DEV float epi_act(const Epi& e, float v) {
 }
 
 // A gate's argument and what stands beside it, clamped (NaN stays).
-QM_DEV float clamp_gate(const Epi& e, float g) { return g > e.limit ? e.limit : g; }
-QM_DEV float clamp_up(const Epi& e, float u) { return (u > e.limit ? e.limit : (u < -e.limit ? -e.limit : u)) + e.up_offset; }
+QM_DEV float clamp_gate(const Epi& e, float g) { return min_nan(g, e.limit); }
+QM_DEV float clamp_up(const Epi& e, float u) { return max_nan(min_nan(u, e.limit), -e.limit) + e.up_offset; }
 
 QM_DEV float epi_gate(const Epi& e, float g, float u) { return epi_act(e, clamp_gate(e, g)) * clamp_up(e, u); }
 

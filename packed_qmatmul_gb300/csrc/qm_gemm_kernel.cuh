@@ -412,7 +412,9 @@ static __device__ __noinline__ void tile_lookup(const Params& p, int mt, int bm,
 // swapped values so that each thread holds two adjacent rows (a gate and what is
 // beside it) of one token. Residuals are 4-byte (gated: 2-byte) loads of a row's
 // 64 (32) bytes, issued ahead of all of it. brow0: row0's element of the bias.
-QM_DEV void store_fused(const Params& p, uint32_t (&r)[32], uint8_t* stage, int lane, int64_t row0, int64_t brow0, int64_t m0,
+// Nothing else of the CTA runs meanwhile, so what costs is instructions: absent parts are
+// branched around, not computed with zeros.
+QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint8_t* stage, int lane, int64_t row0, int64_t brow0, int64_t m0,
                         int64_t mend, int cols) {
     const Epi& e = p.ep;
     const int odd = lane & 1, two = lane & ~1;
@@ -435,37 +437,57 @@ QM_DEV void store_fused(const Params& p, uint32_t (&r)[32], uint8_t* stage, int 
             }
             res[c / 2] = v;
         }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) res[c] = 0u;
     }
     float v[32];
-    const float b = row0 + lane < p.n ? epi_bias(e, brow0 + lane) : 0.0f;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]) + b;
+    for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+    if (e.bias) {
+        const float b = row0 + lane < p.n ? epi_bias(e, brow0 + lane) : 0.0f;
+        const float2 b2 = make_float2(b, b);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+            const float2 s = add2(make_float2(v[c], v[c + 1]), b2);
+            v[c] = s.x;
+            v[c + 1] = s.y;
+        }
+    }
     if (!gated) act_all<1>(e, v);
 #pragma unroll
     for (int c = 0; c < 32; c += 2) {  // rows two, two + 1 of token c + odd
         const float got = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + 1], 1);
-        const float own = odd ? v[c + 1] : v[c];
-        v[c] = odd ? got : own;
-        v[c + 1] = odd ? own : got;
+        v[c] = odd ? got : v[c];
+        v[c + 1] = odd ? v[c + 1] : got;
     }
     // y's columns of one token lie pitch bytes apart in the stage: 64 + 16, or gated 32 + 16
     const int pitch = gated ? 48 : 80;
     if (gated) {
+        if (e.limit < INFINITY) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) v[c] = clamp_gate(e, v[c]);
+            for (int c = 0; c < 32; c += 2) {
+                v[c] = clamp_gate(e, v[c]);
+                v[c + 1] = max_nan(min_nan(v[c + 1], e.limit), -e.limit);
+            }
+        }
         act_all<2>(e, v);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2)
-            *reinterpret_cast<uint16_t*>(stage + (c + odd) * pitch + lane / 2 * 2) =
-                bf16_bits(fmaf(v[c], clamp_up(e, v[c + 1]), bf16_bits_to_f32(res[c / 2])));
+        for (int c = 0; c < 32; c += 2) v[c] *= v[c + 1] + e.up_offset;
+        if (e.residual) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) v[c] += bf16_bits_to_f32(res[c / 2]);
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) *reinterpret_cast<uint16_t*>(stage + (c + odd) * pitch + two) = bf16_bits(v[c]);
     } else {
+        if (e.residual) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                v[c] += __uint_as_float(res[c / 2] << 16);
+                v[c + 1] += __uint_as_float(res[c / 2] & 0xFFFF0000u);
+            }
+        }
 #pragma unroll
         for (int c = 0; c < 32; c += 2)
-            *reinterpret_cast<uint32_t*>(stage + (c + odd) * pitch + lane / 2 * 4) =
-                bf2(v[c] + __uint_as_float(res[c / 2] << 16), v[c + 1] + __uint_as_float(res[c / 2] & 0xFFFF0000u));
+            *reinterpret_cast<uint32_t*>(stage + (c + odd) * pitch + two * 2) = bf2(v[c], v[c + 1]);
     }
     __syncwarp();
     const int64_t m = m0 + lane;
