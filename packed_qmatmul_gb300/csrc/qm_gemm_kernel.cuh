@@ -406,43 +406,50 @@ static __device__ __noinline__ void tile_lookup(const Params& p, int mt, int bm,
     if (lane == 0) { s_grp[0] = found; s_grp[1] = ge; s_grp[2] = gm0; s_grp[3] = gend; }
 }
 
+// The residuals that a lane adds to a block (see store_fused): 4-byte (gated: 2-byte) loads of
+// a row's 64 (32) bytes.
+QM_DEV void load_residual(const Params& p, uint32_t (&res)[16], int lane, int64_t row0, int64_t m0, int64_t mend, int cols) {
+    const Epi& e = p.ep;
+    const int odd = lane & 1, two = lane & ~1;
+    const int64_t col = e.gated ? (row0 + two) >> 1 : row0 + two;
+    const bool second = !e.gated && col + 1 < e.yn;
+    // both of a thread's rows in one word where every such word is aligned
+    const bool word = second && !(e.residual_stride & 1) && !(reinterpret_cast<uintptr_t>(e.residual) & 3);
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+        const int64_t m = m0 + c + odd;
+        uint32_t v = 0u;
+        if (c + odd < cols && m < mend && col < e.yn) {
+            const uint16_t* a = e.residual + m * e.residual_stride + col;
+            if (word) v = __ldca(reinterpret_cast<const uint32_t*>(a));
+            else v = static_cast<uint32_t>(__ldca(a)) | (second ? static_cast<uint32_t>(__ldca(a + 1)) << 16 : 0u);
+        }
+        res[c / 2] = v;
+    }
+}
+
 // The sums of a warp's 32 rows (this lane's row: row0 + lane) for `cols` tokens from
 // token m0 on (r[c]: token m0 + c), through the epilogue to y. The bias is added
 // while a lane holds one row; act runs there too, or, gated, once lane pairs have
 // swapped values so that each thread holds two adjacent rows (a gate and what is
-// beside it) of one token. Residuals are 4-byte (gated: 2-byte) loads of a row's
-// 64 (32) bytes, issued ahead of all of it. brow0: row0's element of the bias.
+// beside it) of one token. What it reads is asked for ahead of it: this lane's bias (its bits)
+// while the main loop runs, a block's residuals (load_residual) while the one before is stored, the
+// first block's before the main loop ends; waited for at each block they cost 40 us of 770 and
+// 11 of 224. ahead() is called once this block's residuals are used.
 // Nothing else of the CTA runs meanwhile, so what costs is instructions: absent parts are
 // branched around, not computed with zeros.
-QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint8_t* stage, int lane, int64_t row0, int64_t brow0, int64_t m0,
-                        int64_t mend, int cols) {
+template <class Ahead>
+QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint32_t (&res)[16], uint32_t bias_bits, uint8_t* stage, int lane,
+                        int64_t row0, int64_t m0, int64_t mend, int cols, const Ahead& ahead) {
     const Epi& e = p.ep;
     const int odd = lane & 1, two = lane & ~1;
     const bool gated = e.gated != 0;
-    const int64_t col0 = gated ? row0 >> 1 : row0;               // y's column of the warp's first row
-    const int64_t col = gated ? (row0 + two) >> 1 : row0 + two;  // this thread's, once it holds pairs
-    uint32_t res[16];
-    if (e.residual) {
-        const bool second = !gated && col + 1 < e.yn;
-        // both of a thread's rows in one word where every such word is aligned
-        const bool word = second && !(e.residual_stride & 1) && !(reinterpret_cast<uintptr_t>(e.residual) & 3);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-            const int64_t m = m0 + c + odd;
-            uint32_t v = 0u;
-            if (c + odd < cols && m < mend && col < e.yn) {
-                const uint16_t* a = e.residual + m * e.residual_stride + col;
-                if (word) v = __ldca(reinterpret_cast<const uint32_t*>(a));
-                else v = static_cast<uint32_t>(__ldca(a)) | (second ? static_cast<uint32_t>(__ldca(a + 1)) << 16 : 0u);
-            }
-            res[c / 2] = v;
-        }
-    }
+    const int64_t col0 = gated ? row0 >> 1 : row0;  // y's column of the warp's first row
     float v[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
     if (e.bias) {
-        const float b = row0 + lane < p.n ? epi_bias(e, brow0 + lane) : 0.0f;
+        const float b = epi_bias_value(e, bias_bits);
         const float2 b2 = make_float2(b, b);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -474,6 +481,7 @@ QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint8_t* stage
         if (e.residual) {
 #pragma unroll
             for (int c = 0; c < 32; c += 2) v[c] += bf16_bits_to_f32(res[c / 2]);
+            ahead();
         }
 #pragma unroll
         for (int c = 0; c < 32; c += 2) *reinterpret_cast<uint16_t*>(stage + (c + odd) * pitch + two) = bf16_bits(v[c]);
@@ -484,6 +492,7 @@ QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint8_t* stage
                 v[c] += __uint_as_float(res[c / 2] << 16);
                 v[c + 1] += __uint_as_float(res[c / 2] & 0xFFFF0000u);
             }
+            ahead();
         }
 #pragma unroll
         for (int c = 0; c < 32; c += 2)
@@ -751,6 +760,10 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
             }
         }
         // ------------------------------------------------------------ epilogue
+        uint32_t res[16], bias_bits = 0u;
+        const int64_t row0 = n0 + 32 * quarter;  // this warp's first weight row
+        if (p.ep.bias && rowok) bias_bits = epi_bias_bits(p.ep, wrow0 + grow);
+        if (p.ep.residual && S == 1) load_residual(p, res, lane, row0, m0 + grp * (NTOK / 2), mend, 32);
         const bool ok = mbar_wait(done, 0);
         if (!ok && lane == 0) give_up();
         tc_fence_after();
@@ -761,7 +774,6 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
         // lane t stores token t's 32 rows as four 16-byte pieces.
         const int part = grp;  // token columns [part * NTOK / 2, (part + 1) * NTOK / 2)
         uint8_t* stage = smem + p.off_x + (warp - 2) * (32 * 80);
-        const int64_t row0 = n0 + 32 * quarter;  // this warp's first weight row
         const bool vec = (p.n & 7) == 0 && row0 + 32 <= p.n;
         const int odd = lane & 1;
         // tokens col .. col + 31 of this warp's 32 rows (r[c]: token col + c) to y
@@ -812,8 +824,12 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 uint32_t r[32];
                 load_acc(col, r);
                 if (!ok || s_abort) continue;
-                if (p.ep.on) store_fused(p, r, stage, lane, row0, wrow0 + row0, m0 + col, mend, 32);
-                else store32(r, col);
+                if (p.ep.on)
+                    store_fused(p, r, res, bias_bits, stage, lane, row0, m0 + col, mend, 32, [&]() {
+                        if (j + 1 < NTOK / 64) load_residual(p, res, lane, row0, m0 + col + 32, mend, 32);
+                    });
+                else
+                    store32(r, col);
             }
         } else {
             // Split k. The tokens are cut into S slices of NTOK / S; CTA q adds
@@ -840,20 +856,26 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
         }
     }
     if (S > 1) {
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
+        const int slice = NTOK / S, pitch = slice + 4;
+        const int64_t row0 = n0 + 32 * quarter;
+        // this warp's tokens of the slice: 32 when the slice has 64, else 16 (slice 32)
+        const int cols = slice / 2;
+        const int c0 = part * cols;
+        const int64_t first = m0 + static_cast<int64_t>(rank) * slice + c0;
+        uint32_t res[16], bias_bits = 0u;  // of an epilogue, on their way over the barrier
+        if (warp >= 2 && warp < 2 + kDecWarps) {
+            if (p.ep.bias && row0 + lane < p.n) bias_bits = epi_bias_bits(p.ep, row0 + lane);
+            if (p.ep.residual) load_residual(p, res, lane, row0, first, mend, cols);
+        }
         __syncthreads();
         cluster_sync();  // every partial sum has arrived; nothing is written remotely after this
         if (warp >= 2 && warp < 2 + kDecWarps) {
-            const int quarter = warp & 3, part = (warp - 2) >> 2;
-            const int slice = NTOK / S, pitch = slice + 4;
             const int row = 32 * quarter + lane;
             const float* recv = reinterpret_cast<const float*>(smem + p.off_recv);
-            const int64_t row0 = n0 + 32 * quarter;
             const bool vec = (p.n & 7) == 0 && row0 + 32 <= p.n;
             const int odd = lane & 1;
             uint8_t* stage = smem + p.off_x + (warp - 2) * (32 * 80);
-            // this warp's tokens of the slice: 32 when the slice has 64, else 16 (slice 32)
-            const int cols = slice / 2;
-            const int c0 = part * cols;
             const bool live = !s_abort;
             uint32_t r[32];
 #pragma unroll
@@ -865,11 +887,10 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 r[c] = __float_as_uint(v);
             }
             if (live && p.ep.on) {
-                store_fused(p, r, stage, lane, row0, row0, m0 + static_cast<int64_t>(rank) * slice + c0, mend, cols);
+                store_fused(p, r, res, bias_bits, stage, lane, row0, first, mend, cols, []() {});
             } else if (live) {
                 // the store's tokens past `cols` belong to the next warp's part: keep them out
                 const int64_t keep_end = mend;
-                const int64_t first = m0 + static_cast<int64_t>(rank) * slice + c0;
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
                     const float lo = __uint_as_float(r[c]), hi = __uint_as_float(r[c + 1]);
