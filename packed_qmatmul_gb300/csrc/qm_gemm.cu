@@ -5,7 +5,7 @@
 
 namespace qm {
 
-uint32_t gemm_read_clear_error() { return gemm::read_clear_flag() | gemm::grouped_read_clear_flag(); }
+uint32_t gemm_read_clear_error() { return gemm::read_clear_flag() | gemm::grouped_read_clear_flag() | gemm::dual_read_clear_flag(); }
 
 namespace gemm {
 
@@ -21,17 +21,16 @@ struct Launch {
     const WDesc& w;
     const void* x;
     cudaStream_t st;
-    bool wide;
     template <int FMT, int BITS, int GS>
     cudaError_t run() const {
-        return wide ? launch_t<FMT, BITS, GS, 256, false>(p, w, x, st) : launch_t<FMT, BITS, GS, 128, true>(p, w, x, st);
+        return launch_t<FMT, BITS, GS, 256, false>(p, w, x, st);
     }
 };
 
 static cudaError_t dispatch(Params& p, const WDesc& w, const void* x, cudaStream_t st) {
     const bool wide = p.g_off ? p.M > 256 * std::max<int64_t>(1, p.g_E) : p.M > 128;
-    if (p.g_off && !wide) return dispatch_grouped_narrow(p, w, x, st);
-    return by_format(p, w, Launch{p, w, x, st, wide});
+    if (!wide) return p.g_off ? dispatch_grouped_narrow(p, w, x, st) : dispatch_dual(p, w, x, st);
+    return by_format(p, w, Launch{p, w, x, st});
 }
 
 }  // namespace gemm

@@ -1005,5 +1005,9 @@ static cudaError_t by_format(Params& p, const WDesc& w, const L& l) {
 cudaError_t dispatch_grouped_narrow(Params& p, const WDesc& w, const void* x, cudaStream_t st);
 uint32_t grouped_read_clear_flag();
 
+// Plain products of at most 128 tokens (dual layout), instantiated in qm_gemm_dual.cu likewise.
+cudaError_t dispatch_dual(Params& p, const WDesc& w, const void* x, cudaStream_t st);
+uint32_t dual_read_clear_flag();
+
 }  // namespace gemm
 }  // namespace qm

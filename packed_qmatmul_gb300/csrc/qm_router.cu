@@ -712,8 +712,9 @@ QM_DEV uint32_t pair_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// VEC: n a multiple of 8, so that every row of y and out is in 16-byte pieces.
-template <bool VEC>
+// VEC: n a multiple of 8, so that every row of y and out is in 16-byte pieces. ROWS of them are
+// asked for before the first is used.
+template <bool VEC, int ROWS>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Combine a) {
     grid_launch_dependents();
     grid_dependency_wait();
@@ -736,17 +737,17 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
                 for (int q = 0; q < 4; ++q) u[q] = static_cast<uint32_t>(__ldca(r + 2 * q)) | (static_cast<uint32_t>(__ldca(r + 2 * q + 1)) << 16);
                 res = make_uint4(u[0], u[1], u[2], u[3]);
             }
-            for (int j = 0; j < a.topk; j += 4) {
-                uint4 v[4];
-                float w[4];
+            for (int j = 0; j < a.topk; j += ROWS) {
+                uint4 v[ROWS];
+                float w[ROWS];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < ROWS; ++q) {
                     const bool live = j + q < a.topk;
-                    v[q] = live ? __ldg(reinterpret_cast<const uint4*>(yr + (j + q) * a.n)) : make_uint4(0u, 0u, 0u, 0u);
+                    v[q] = live ? __ldcs(reinterpret_cast<const uint4*>(yr + (j + q) * a.n)) : make_uint4(0u, 0u, 0u, 0u);
                     w[q] = live ? __ldg(wr + j + q) : 0.0f;
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) add8(s, v[q], w[q]);
+                for (int q = 0; q < ROWS; ++q) add8(s, v[q], w[q]);
             }
             add8(s, res, 1.0f);
             *reinterpret_cast<uint4*>(a.out + t * a.n + c) =
@@ -769,8 +770,9 @@ cudaError_t launch_experts_combine(const void* y, const float* weights, int64_t 
     a.vec_residual = aligned16(residual) && residual_stride % 8 == 0;
     const bool vec = n % 8 == 0;
     const int64_t items = T * (vec ? n / 8 : n);
-    const int64_t blocks = std::min<int64_t>((items + 127) / 128, int64_t(num_sms()) * 16);
-    return launch_pdl(vec ? combine_kernel<true> : combine_kernel<false>, static_cast<unsigned>(blocks), 128, 0, st, a);
+    const int64_t blocks = std::min<int64_t>((items + 127) / 128, int64_t(1) << 22);
+    return launch_pdl(!vec ? combine_kernel<false, 1> : topk > 4 ? combine_kernel<true, 8> : combine_kernel<true, 4>,
+                      static_cast<unsigned>(blocks), 128, 0, st, a);
 }
 
 }  // namespace qm
