@@ -5,7 +5,11 @@
 
 namespace qm {
 
-uint32_t gemm_read_clear_error() { return gemm::read_clear_flag() | gemm::grouped_read_clear_flag() | gemm::dual_read_clear_flag(); }
+uint32_t gemm_read_clear_error() {
+    using namespace gemm;
+    return read_clear_flag() | grouped_read_clear_flag() | dual_read_clear_flag() | wide_fused_read_clear_flag() |
+           grouped_fused_read_clear_flag() | dual_fused_read_clear_flag();
+}
 
 namespace gemm {
 
@@ -16,21 +20,12 @@ namespace gemm {
 // there, where many tiles queue: T = 1024 x top-4 over 32 experts 492 against
 // 347 TFLOP/s; and faster than 256-token tiles even where an expert spills a
 // second, nearly empty tile: 376 -> 392).
-struct Launch {
-    Params& p;
-    const WDesc& w;
-    const void* x;
-    cudaStream_t st;
-    template <int FMT, int BITS, int GS>
-    cudaError_t run() const {
-        return launch_t<FMT, BITS, GS, 256, false>(p, w, x, st);
-    }
-};
-
 static cudaError_t dispatch(Params& p, const WDesc& w, const void* x, cudaStream_t st) {
     const bool wide = p.g_off ? p.M > 256 * std::max<int64_t>(1, p.g_E) : p.M > 128;
-    if (!wide) return p.g_off ? dispatch_grouped_narrow(p, w, x, st) : dispatch_dual(p, w, x, st);
-    return by_format(p, w, Launch{p, w, x, st});
+    const bool fused = p.ep.on;
+    if (wide) return fused ? dispatch_wide_fused(p, w, x, st) : dispatch_tiles<256, false, false>(p, w, x, st);
+    if (p.g_off) return fused ? dispatch_grouped_fused(p, w, x, st) : dispatch_grouped(p, w, x, st);
+    return fused ? dispatch_dual_fused(p, w, x, st) : dispatch_dual(p, w, x, st);
 }
 
 }  // namespace gemm

@@ -1,0 +1,14 @@
+// qm_gemm_dual_fused.cu -- plain products of at most 128 tokens (dual
+// layout) with an epilogue,
+// instantiated here so that they compile beside qm_gemm.cu.
+#include "qm_gemm_kernel.cuh"
+
+namespace qm {
+namespace gemm {
+
+uint32_t dual_fused_read_clear_flag() { return read_clear_flag(); }
+
+cudaError_t dispatch_dual_fused(Params& p, const WDesc& w, const void* x, cudaStream_t st) { return dispatch_tiles<128, true, true>(p, w, x, st); }
+
+}  // namespace gemm
+}  // namespace qm

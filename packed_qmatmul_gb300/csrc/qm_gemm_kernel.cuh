@@ -516,7 +516,8 @@ QM_DEV void store_fused(const Params& p, const uint32_t (&r)[32], uint32_t (&res
     __syncwarp();
 }
 
-template <int FMT, int BITS, int GS, int NTOK, bool DUAL>
+// EPI: the sums pass through an epilogue (kernels of their own: plain products keep their code).
+template <int FMT, int BITS, int GS, int NTOK, bool DUAL, bool EPI>
 __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 : 1)
     gemm_kernel(const __grid_constant__ Params p) {
     using R = Raw<FMT, BITS>;
@@ -762,8 +763,8 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
         // ------------------------------------------------------------ epilogue
         uint32_t res[16], bias_bits = 0u;
         const int64_t row0 = n0 + 32 * quarter;  // this warp's first weight row
-        if (p.ep.bias && rowok) bias_bits = epi_bias_bits(p.ep, wrow0 + grow);
-        if (p.ep.residual && S == 1) load_residual(p, res, lane, row0, m0 + grp * (NTOK / 2), mend, 32);
+        if (EPI && p.ep.bias && rowok) bias_bits = epi_bias_bits(p.ep, wrow0 + grow);
+        if (EPI && p.ep.residual && S == 1) load_residual(p, res, lane, row0, m0 + grp * (NTOK / 2), mend, 32);
         const bool ok = mbar_wait(done, 0);
         if (!ok && lane == 0) give_up();
         tc_fence_after();
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 uint32_t r[32];
                 load_acc(col, r);
                 if (!ok || s_abort) continue;
-                if (p.ep.on)
+                if constexpr (EPI)
                     store_fused(p, r, res, bias_bits, stage, lane, row0, m0 + col, mend, 32, [&]() {
                         if (j + 1 < NTOK / 64) load_residual(p, res, lane, row0, m0 + col + 32, mend, 32);
                     });
@@ -865,8 +866,8 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
         const int64_t first = m0 + static_cast<int64_t>(rank) * slice + c0;
         uint32_t res[16], bias_bits = 0u;  // of an epilogue, on their way over the barrier
         if (warp >= 2 && warp < 2 + kDecWarps) {
-            if (p.ep.bias && row0 + lane < p.n) bias_bits = epi_bias_bits(p.ep, row0 + lane);
-            if (p.ep.residual) load_residual(p, res, lane, row0, first, mend, cols);
+            if (EPI && p.ep.bias && row0 + lane < p.n) bias_bits = epi_bias_bits(p.ep, row0 + lane);
+            if (EPI && p.ep.residual) load_residual(p, res, lane, row0, first, mend, cols);
         }
         __syncthreads();
         cluster_sync();  // every partial sum has arrived; nothing is written remotely after this
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
                 }
                 r[c] = __float_as_uint(v);
             }
-            if (live && p.ep.on) {
+            if (EPI && live) {
                 store_fused(p, r, res, bias_bits, stage, lane, row0, first, mend, cols, []() {});
             } else if (live) {
                 // the store's tokens past `cols` belong to the next warp's part: keep them out
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(threads_for(DUAL), (NTOK <= 128 && !DUAL) ? 2 
     }
 }
 
-template <int FMT, int BITS, int GS, int NTOK, bool DUAL>
+template <int FMT, int BITS, int GS, int NTOK, bool DUAL, bool EPI>
 static cudaError_t launch_t(Params& p, const WDesc& w, const void* x, cudaStream_t st) {
     using R = Raw<FMT, BITS>;
     p.mtiles = p.g_off ? static_cast<int>(std::min<int64_t>(p.M, p.M / NTOK + p.g_E))  // sum of ceil(count / NTOK)
@@ -950,7 +951,7 @@ static cudaError_t launch_t(Params& p, const WDesc& w, const void* x, cudaStream
     if (!make_tmap_2d(&p.tm_raw, w.codes, w.code_row_bytes, w.rows, w.code_row_bytes, R::BYTES, ts::BW, R::SW,
                       R::ELEM))
         return cudaErrorNotSupported;
-    auto kern = gemm_kernel<FMT, BITS, GS, NTOK, DUAL>;
+    auto kern = gemm_kernel<FMT, BITS, GS, NTOK, DUAL, EPI>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     p.ntiles = static_cast<int>(ntiles);
@@ -1000,14 +1001,37 @@ static cudaError_t by_format(Params& p, const WDesc& w, const L& l) {
     return cudaErrorInvalidValue;
 }
 
-// Grouped products with 128-token tiles (classic layout, two CTAs to an SM),
-// instantiated in qm_gemm_grouped.cu so that they compile beside the rest.
-cudaError_t dispatch_grouped_narrow(Params& p, const WDesc& w, const void* x, cudaStream_t st);
-uint32_t grouped_read_clear_flag();
+// One tile shape's kernels, for the weight's format.
+template <int NTOK, bool DUAL, bool EPI>
+struct Launch {
+    Params& p;
+    const WDesc& w;
+    const void* x;
+    cudaStream_t st;
+    template <int FMT, int BITS, int GS>
+    cudaError_t run() const {
+        return launch_t<FMT, BITS, GS, NTOK, DUAL, EPI>(p, w, x, st);
+    }
+};
+template <int NTOK, bool DUAL, bool EPI>
+static cudaError_t dispatch_tiles(Params& p, const WDesc& w, const void* x, cudaStream_t st) {
+    return by_format(p, w, Launch<NTOK, DUAL, EPI>{p, w, x, st});
+}
 
-// Plain products of at most 128 tokens (dual layout), instantiated in qm_gemm_dual.cu likewise.
+// Each is instantiated in a unit of its own, so that they compile side by side: 256-token tiles in
+// qm_gemm.cu; grouped products' 128-token tiles (classic layout, two CTAs to an SM) in qm_gemm_grouped.cu;
+// plain products of at most 128 tokens (dual layout) in qm_gemm_dual.cu; the three with an
+// epilogue in their _fused units.
+cudaError_t dispatch_grouped(Params& p, const WDesc& w, const void* x, cudaStream_t st);
 cudaError_t dispatch_dual(Params& p, const WDesc& w, const void* x, cudaStream_t st);
+cudaError_t dispatch_wide_fused(Params& p, const WDesc& w, const void* x, cudaStream_t st);
+cudaError_t dispatch_grouped_fused(Params& p, const WDesc& w, const void* x, cudaStream_t st);
+cudaError_t dispatch_dual_fused(Params& p, const WDesc& w, const void* x, cudaStream_t st);
+uint32_t grouped_read_clear_flag();
 uint32_t dual_read_clear_flag();
+uint32_t wide_fused_read_clear_flag();
+uint32_t grouped_fused_read_clear_flag();
+uint32_t dual_fused_read_clear_flag();
 
 }  // namespace gemm
 }  // namespace qm
