@@ -653,13 +653,13 @@ def qm_cache_attend(cache: Cache, batch: Batch, q: torch.Tensor, out: torch.Tens
 
 def _bf16(t: torch.Tensor, name: str) -> int:
     """The address of a contiguous bfloat16 tensor."""
-    if t.dtype != torch.bfloat16 or not t.is_contiguous():
+    if t.dtype is not torch.bfloat16 or not t.is_contiguous():
         _refuse(f"{name}: must be contiguous bfloat16")
     return t.data_ptr()
 
 
 def _residual(residual: torch.Tensor, rows: int, n: int) -> None:
-    if residual.shape != (rows, n) or residual.dtype != torch.bfloat16:
+    if residual.shape != (rows, n) or residual.dtype is not torch.bfloat16:
         _refuse(f"residual: must be bfloat16 {(rows, n)}")
     if residual.stride(1) != 1 and n > 1:
         _refuse("residual: rows must be contiguous")
@@ -675,22 +675,40 @@ def _fused_columns(w: QWeight, ep: Epilogue, ndim: int) -> int:
     return shape[-2] // 2 if ep.gated else shape[-2]
 
 
+def _here(gpu: int, stream) -> Optional[int]:
+    """The stream's handle; refuses tensors on another GPU than the current one, where the kernels would run."""
+    now = _device()
+    if gpu != now:
+        _refuse(f"device: the tensors are on GPU {gpu}, the current one is {now}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(gpu)
+    return _stream(stream)
+
+
+# The calls below check as the others do, in an order that leaves a step of small products little of it: a
+# new output is on its input's GPU, and _one_gpu is asked only where the short comparison fails.
 def _fused(w: QWeight, x: torch.Tensor, ep: Epilogue, residual, y, stream) -> torch.Tensor:
     n = _fused_columns(w, ep, 2)
-    if x.dim() != 2 or x.shape[1] != w.shape[1]:
-        _refuse(f"x: shape {tuple(x.shape)}, expected {('M', w.shape[1])}")
-    M, gpu = x.shape[0], x.get_device()
-    xp = _bf16(x, "x")
+    xs = x.shape
+    if len(xs) != 2 or xs[1] != w.shape[1]:
+        _refuse(f"x: shape {tuple(xs)}, expected {('M', w.shape[1])}")
+    M, gpu, xp = xs[0], x.get_device(), _bf16(x, "x")
     if y is None:
         y = torch.empty((M, n), dtype=torch.bfloat16, device=x.device)
-    elif y.shape != (M, n):
-        _refuse(f"y: shape {tuple(y.shape)}, expected {(M, n)}")
+        yp, on = y.data_ptr(), gpu
+    else:
+        if y.shape != (M, n):
+            _refuse(f"y: shape {tuple(y.shape)}, expected {(M, n)}")
+        yp, on = _bf16(y, "y"), y.get_device()
     c = ep._c
     if residual is not None:
         _residual(residual, M, n)
         c = ep._with(residual)
-    _one_gpu((gpu, y.get_device(), w.codes.get_device(), ep.gpu, _gpu(residual)), ("x", "y", "w", "bias", "residual"))
-    _check(load_library().qm_apply_fused(w._ref(), xp, M, QM_BF16, c, _bf16(y, "y"), _stream(stream)))
+    if gpu < 0 or on != gpu or w.codes.get_device() != gpu or ep.gpu not in (None, gpu) or (residual is not None and residual.get_device() != gpu):
+        _one_gpu((gpu, on, w.codes.get_device(), ep.gpu, _gpu(residual)), ("x", "y", "w", "bias", "residual"))
+    st = load_library().qm_apply_fused(w._ref(), xp, M, QM_BF16, c, yp, _here(gpu, stream))
+    if st:
+        _check(st)
     return y
 
 
@@ -707,20 +725,27 @@ def _experts_fused(w: QWeight, ids: torch.Tensor, x: torch.Tensor, ep: Epilogue,
     itype = _ITYPES.get(ids.dtype)
     if itype is None or not ids.is_contiguous():
         _refuse("ids: must be contiguous int32 or int64")
-    if x.dim() != 2 or x.shape[1] != w.shape[2] or x.shape[0] not in (T, T * topk):
-        _refuse(f"x: shape {tuple(x.shape)}, expected {('T or T*topk', w.shape[2])}")
+    xs = x.shape
+    if len(xs) != 2 or xs[1] != w.shape[2] or (xs[0] != T and xs[0] != T * topk):
+        _refuse(f"x: shape {tuple(xs)}, expected {('T or T*topk', w.shape[2])}")
+    gpu, xp = x.get_device(), _bf16(x, "x")
     if y is None:
         y = torch.empty((T, topk, n), dtype=torch.bfloat16, device=x.device)
-    elif y.shape != (T, topk, n):
-        _refuse(f"y: shape {tuple(y.shape)}, expected {(T, topk, n)}")
+        yp, on = y.data_ptr(), gpu
+    else:
+        if y.shape != (T, topk, n):
+            _refuse(f"y: shape {tuple(y.shape)}, expected {(T, topk, n)}")
+        yp, on = _bf16(y, "y"), y.get_device()
     if workspace is None:
         need = qm_apply_experts_workspace(w, T, topk)
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    _one_gpu((x.get_device(), ids.get_device(), y.get_device(), w.codes.get_device(), ep.gpu, _gpu(workspace)),
+    _one_gpu((gpu, ids.get_device(), on, w.codes.get_device(), ep.gpu, _gpu(workspace)),
              ("x", "ids", "y", "w", "bias", "workspace"))
-    _check(load_library().qm_apply_experts_fused(
-        w._ref(), ids.data_ptr(), itype, T, topk, _bf16(x, "x"), x.shape[0], QM_BF16, ep._c, _bf16(y, "y"), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = load_library().qm_apply_experts_fused(
+        w._ref(), ids.data_ptr(), itype, T, topk, xp, xs[0], QM_BF16, ep._c, yp, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _here(gpu, stream))
+    if st:
+        _check(st)
     return y
 
 
@@ -731,27 +756,31 @@ def qm_apply_experts_fused(w: QWeight, ids: torch.Tensor, x: torch.Tensor, ep: E
 
 
 def _select(logits: torch.Tensor, router: Router, ids, weights, stream):
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         _refuse("logits: must be [T, experts]")
-    T, E = logits.shape
+    T, E = shape
     dtype = _DTYPES.get(logits.dtype)
     if dtype is None:
         _refuse("logits: must be float32, bfloat16 or float16")
     stride, es = logits.stride()
     if es != 1 and E > 1:
         _refuse("logits: rows must be contiguous")
-    c, shape = router._c(E), (T, router.topk)
+    c, shape, gpu = router._c(E), (T, router.topk), logits.get_device()
     if ids is None:
         device = logits.device
         ids, weights = torch.empty(shape, dtype=torch.int32, device=device), torch.empty(shape, dtype=torch.float32, device=device)
+        if gpu < 0 or router.gpu not in (None, gpu):
+            _one_gpu((gpu, router.gpu), ("logits", "bias"))
     else:
         if ids.shape != shape or ids.dtype != torch.int32 or not ids.is_contiguous():
             _refuse(f"ids: must be contiguous int32 {shape}")
         if weights.shape != shape or weights.dtype != torch.float32 or not weights.is_contiguous():
             _refuse(f"weights: must be contiguous float32 {shape}")
-    _one_gpu((logits.get_device(), ids.get_device(), weights.get_device(), router.gpu), ("logits", "ids", "weights", "bias"))
-    _check(load_library().qm_experts_select(c, logits.data_ptr(), dtype, stride, T, ids.data_ptr(), weights.data_ptr(),
-                                            _stream(stream)))
+        _one_gpu((gpu, ids.get_device(), weights.get_device(), router.gpu), ("logits", "ids", "weights", "bias"))
+    st = load_library().qm_experts_select(c, logits.data_ptr(), dtype, stride, T, ids.data_ptr(), weights.data_ptr(), _here(gpu, stream))
+    if st:
+        _check(st)
     return ids, weights
 
 
@@ -761,22 +790,29 @@ def qm_experts_select(logits: torch.Tensor, router: Router, ids: torch.Tensor, w
 
 
 def _combine(y: torch.Tensor, weights: torch.Tensor, residual, out, stream) -> torch.Tensor:
-    if y.dim() != 3:
+    shape = y.shape
+    if len(shape) != 3:
         _refuse("y: must be [T, topk, n]")
-    T, topk, n = y.shape
-    if weights.shape != (T, topk) or weights.dtype != torch.float32 or not weights.is_contiguous():
+    T, topk, n = shape
+    if weights.shape != (T, topk) or weights.dtype is not torch.float32 or not weights.is_contiguous():
         _refuse(f"weights: must be contiguous float32 {(T, topk)}")
+    gpu, yp = y.get_device(), _bf16(y, "y")
     if out is None:
         out = torch.empty((T, n), dtype=torch.bfloat16, device=y.device)
-    elif out.shape != (T, n):
-        _refuse(f"out: shape {tuple(out.shape)}, expected {(T, n)}")
+        op, on = out.data_ptr(), gpu
+    else:
+        if out.shape != (T, n):
+            _refuse(f"out: shape {tuple(out.shape)}, expected {(T, n)}")
+        op, on = _bf16(out, "out"), out.get_device()
     rp, stride = None, 0
     if residual is not None:
         _residual(residual, T, n)
         rp, stride = residual.data_ptr(), residual.stride(0)
-    _one_gpu((y.get_device(), weights.get_device(), out.get_device(), _gpu(residual)), ("y", "weights", "out", "residual"))
-    _check(load_library().qm_experts_combine(_bf16(y, "y"), weights.data_ptr(), T, topk, n, QM_BF16, rp, stride, _bf16(out, "out"),
-                                             _stream(stream)))
+    if gpu < 0 or on != gpu or weights.get_device() != gpu or (residual is not None and residual.get_device() != gpu):
+        _one_gpu((gpu, weights.get_device(), on, _gpu(residual)), ("y", "weights", "out", "residual"))
+    st = load_library().qm_experts_combine(yp, weights.data_ptr(), T, topk, n, QM_BF16, rp, stride, op, _here(gpu, stream))
+    if st:
+        _check(st)
     return out
 
 

@@ -589,3 +589,14 @@ def test_gates_laid_out_by_take():
     x = randn(101, M, k)
     ep = qm.Epilogue(act="silu", gated=True)
     check(qm.apply_fused(pairs, x, ep), *expected(values[order.long()], x, None, ep, None))
+
+
+def test_tensors_of_another_gpu_than_the_current_one(monkeypatch):
+    w, _ = make("affine4_g64", 1, 8, 64)
+    experts, _ = make("mxfp4", 2, 64, 64, (4,))
+    ids = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    monkeypatch.setattr(qm, "_device", lambda: 1)
+    for call in (lambda: qm.apply_fused(w, randn(1, 3, 64), qm.Epilogue(act="silu")), lambda: qm.apply_experts_fused(experts, ids, randn(1, 3, 64), qm.Epilogue()),
+                 lambda: qm.experts_select(randn(1, 3, 16), qm.Router(2)), lambda: qm.experts_combine(randn(1, 3, 2, 8), torch.ones(3, 2, device="cuda"))):
+        with pytest.raises(qm.QMError, match="device"):
+            call()
