@@ -247,7 +247,7 @@ extern "C" {
 
 const char* qm_last_error(void) { return g_last_error.c_str(); }
 
-int32_t qm_version(void) { return 200; }
+int32_t qm_version(void) { return 300; }
 
 qm_status qm_dequant(const qm_weight* w, int32_t out_dtype, void* out, qm_stream_t stream) {
     set_error("");

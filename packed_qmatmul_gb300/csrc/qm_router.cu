@@ -6,18 +6,30 @@
 // of the logits is the order of the keys, and they are compared as they are. A
 // warp takes a token and holds its logits in registers: 32 / G' lanes to a group (G'
 // the groups rounded up to a power of two), a group's experts dealt to its lanes in
-// turn. Group scores then meet by shuffles within a group's lanes, each
-// group's rank is counted over all of them, and the topk largest keys are taken one after
-// another: a warp maximum over order-preserving integers, the lowest index where
-// several lanes hold it.
+// turn. Keys are order-preserving integers from then on. Group scores meet by shuffles
+// within a group's lanes, and each group counts those before it. The topk-th largest
+// of the lanes' own largest keys is a bound that at least topk keys reach and seldom
+// many more: those move to a list, a lane each, and each counts the entries before
+// its own, which is its place. (One maximum after another over all keys: 57 us for the
+// case below; a list: 36.)
 //
 // Keys that are sums or exponentials carry float32 roundings, and two of them may
 // lie closer than those. Neighbours in the order (and group scores about the border)
-// nearer than a bound on their errors, unless their logit and bias are the same, send the
-// token to select_exact, which orders it anew by float64 keys.
+// nearer than a bound on their errors, unless their logit and bias are the same, are
+// compared by float64 keys of the candidates concerned, one to a lane; what does not fit
+// a list goes to select_ties (many equal keys, one after another) or select_exact (all of
+// a token in float64).
 //
-// Sum. Eight columns of one token to a thread, the rows of its experts loaded
-// together before the first is used.
+// It reads each logit once; what bounds it is instructions, some 500 a token without a
+// bias or groups and 1080 with both, at 70 % of the issue slots: 16384 tokens of 256
+// experts take 10.3 us (top 8 of all) and 24 us (sigmoid, bias, 4 of 8 groups by their
+// two best), against 2.6 us of memory time. Some 60 of the latter's tokens need float64,
+// whose chain of operations at 1/64 of float32's rate the last of them shows: 5 us. Asking
+// for the next token's logits ahead changed nothing (32 warps to an SM hide them).
+//
+// Sum. Eight columns of one token to a thread, up to eight of its experts' rows asked for
+// before the first is used: 4096 tokens x 8 rows of 2880 take 44 us, 5.3 TB/s (four rows
+// at a time 51).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -695,7 +707,6 @@ struct Combine {
     uint16_t* out;
     int64_t residual_stride, n, T;
     int topk;
-    int vec_residual;  // residual rows in 16-byte pieces
 };
 
 QM_DEV void add8(float (&s)[8], uint4 v, float w) {
@@ -712,52 +723,89 @@ QM_DEV uint32_t pair_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// VEC: n a multiple of 8, so that every row of y and out is in 16-byte pieces. ROWS of them are
-// asked for before the first is used.
+// Up to eight elements at an even address, as loaded: a first one where the address is odd in
+// words, then words (a half where only their first element is live). Packed later, so that
+// several rows' loads are under way at once.
+struct Loose {
+    uint32_t first, word[4];
+};
+QM_DEV Loose load_loose(const uint16_t* p, int live) {
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+    Loose r;
+    r.first = odd && live > 0 ? __ldca(p) : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = 2 * k + odd;
+        r.word[k] = 0u;
+        if (e + 1 < live) r.word[k] = __ldca(reinterpret_cast<const uint32_t*>(p + e));
+        else if (e < live) r.word[k] = __ldca(p + e);
+    }
+    return r;
+}
+QM_DEV uint4 packed(const Loose& r, const uint16_t* p) {
+    if (!(reinterpret_cast<uintptr_t>(p) & 2)) return make_uint4(r.word[0], r.word[1], r.word[2], r.word[3]);
+    return make_uint4(r.first | r.word[0] << 16, __funnelshift_r(r.word[0], r.word[1], 16), __funnelshift_r(r.word[1], r.word[2], 16),
+                      __funnelshift_r(r.word[2], r.word[3], 16));
+}
+QM_DEV void store_loose(uint16_t* p, const uint32_t (&v)[4], int live) {
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+    if (odd) p[0] = static_cast<uint16_t>(v[0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = 2 * k + odd;
+        const uint32_t w = odd ? __funnelshift_r(v[k], k < 3 ? v[k + 1] : 0u, 16) : v[k];
+        if (e + 1 < live) *reinterpret_cast<uint32_t*>(p + e) = w;
+        else if (e < live) p[e] = static_cast<uint16_t>(w);
+    }
+}
+
+// VEC: n a multiple of 8, so that every row of y and out is in 16-byte pieces, and the residual's too; else rows begin at
+// any even address, and a row's last piece may be short (n = 1001: 43 us an element at a time, 4096
+// tokens x 8 rows). ROWS of them are asked for before the first is used.
 template <bool VEC, int ROWS>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Combine a) {
     grid_launch_dependents();
     grid_dependency_wait();
-    constexpr int W = VEC ? 8 : 1;
-    const int64_t per = a.n / W, total = a.T * per, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    const int64_t per = (a.n + 7) / 8, total = a.T * per, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
         const int64_t t = total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per)) : i / per;
-        const int64_t c = (i - t * per) * W;
+        const int64_t c = (i - t * per) * 8;
+        const int live = VEC ? 8 : static_cast<int>(min(static_cast<int64_t>(8), a.n - c));
         const uint16_t* yr = a.y + t * a.topk * a.n + c;
         const float* wr = a.weights + t * a.topk;
-        if constexpr (VEC) {
-            float s[8] = {};
-            uint4 res = make_uint4(0u, 0u, 0u, 0u);
-            if (a.residual && a.vec_residual) {
-                res = __ldca(reinterpret_cast<const uint4*>(a.residual + t * a.residual_stride + c));
-            } else if (a.residual) {
-                const uint16_t* r = a.residual + t * a.residual_stride + c;
-                uint32_t u[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) u[q] = static_cast<uint32_t>(__ldca(r + 2 * q)) | (static_cast<uint32_t>(__ldca(r + 2 * q + 1)) << 16);
-                res = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            for (int j = 0; j < a.topk; j += ROWS) {
-                uint4 v[ROWS];
-                float w[ROWS];
-#pragma unroll
-                for (int q = 0; q < ROWS; ++q) {
-                    const bool live = j + q < a.topk;
-                    v[q] = live ? __ldcs(reinterpret_cast<const uint4*>(yr + (j + q) * a.n)) : make_uint4(0u, 0u, 0u, 0u);
-                    w[q] = live ? __ldg(wr + j + q) : 0.0f;
-                }
-#pragma unroll
-                for (int q = 0; q < ROWS; ++q) add8(s, v[q], w[q]);
-            }
-            add8(s, res, 1.0f);
-            *reinterpret_cast<uint4*>(a.out + t * a.n + c) =
-                make_uint4(pair_bf16(s[0], s[1]), pair_bf16(s[2], s[3]), pair_bf16(s[4], s[5]), pair_bf16(s[6], s[7]));
-        } else {
-            float s = 0.0f;
-            for (int j = 0; j < a.topk; ++j) s = fmaf(__ldg(wr + j), bf16_bits_to_f32(__ldg(yr + j * a.n)), s);
-            if (a.residual) s += bf16_bits_to_f32(__ldca(a.residual + t * a.residual_stride + c));
-            a.out[t * a.n + c] = bf16_bits(s);
+        const uint16_t* rr = a.residual + t * a.residual_stride + c;
+        float s[8] = {};
+        uint4 res = make_uint4(0u, 0u, 0u, 0u);
+        Loose loose_res{};
+        if (a.residual) {
+            if constexpr (VEC) res = __ldca(reinterpret_cast<const uint4*>(rr));
+            else loose_res = load_loose(rr, live);
         }
+        for (int j = 0; j < a.topk; j += ROWS) {
+            uint4 v[ROWS];
+            Loose r[ROWS];
+            float w[ROWS];
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) {
+                const bool on = j + q < a.topk;
+                if constexpr (VEC) v[q] = on ? __ldcs(reinterpret_cast<const uint4*>(yr + (j + q) * a.n)) : make_uint4(0u, 0u, 0u, 0u);
+                else r[q] = load_loose(yr + (j + q) * a.n, on ? live : 0);
+                w[q] = on ? __ldg(wr + j + q) : 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < ROWS; ++q) {
+                if constexpr (!VEC) v[q] = packed(r[q], yr + (j + q) * a.n);
+                add8(s, v[q], w[q]);
+            }
+        }
+        if (a.residual) {
+            if constexpr (!VEC) res = packed(loose_res, rr);
+            add8(s, res, 1.0f);
+        }
+        const uint32_t o[4] = {pair_bf16(s[0], s[1]), pair_bf16(s[2], s[3]), pair_bf16(s[4], s[5]), pair_bf16(s[6], s[7])};
+        uint16_t* out = a.out + t * a.n + c;
+        if constexpr (VEC) *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+        else store_loose(out, o, live);
     }
 }
 
@@ -766,12 +814,11 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
 cudaError_t launch_experts_combine(const void* y, const float* weights, int64_t T, int64_t topk, int64_t n, const void* residual,
                                    int64_t residual_stride, void* out, cudaStream_t st) {
     Combine a{static_cast<const uint16_t*>(y), weights, static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out),
-              residual_stride, n, T, static_cast<int>(topk), 0};
-    a.vec_residual = aligned16(residual) && residual_stride % 8 == 0;
-    const bool vec = n % 8 == 0;
-    const int64_t items = T * (vec ? n / 8 : n);
+              residual_stride, n, T, static_cast<int>(topk)};
+    const bool vec = n % 8 == 0 && (!residual || (aligned16(residual) && residual_stride % 8 == 0));
+    const int64_t items = T * ((n + 7) / 8);
     const int64_t blocks = std::min<int64_t>((items + 127) / 128, int64_t(1) << 22);
-    return launch_pdl(!vec ? combine_kernel<false, 1> : topk > 4 ? combine_kernel<true, 8> : combine_kernel<true, 4>,
+    return launch_pdl(!vec ? combine_kernel<false, 4> : topk > 4 ? combine_kernel<true, 8> : combine_kernel<true, 4>,
                       static_cast<unsigned>(blocks), 128, 0, st, a);
 }
 

@@ -463,7 +463,8 @@ def test_select_of_many_tokens_and_outputs():
 
 
 # ---------------------------------------------------------------- the sum over a token's experts
-@pytest.mark.parametrize("T,topk,n", [(1, 4, 2880), (3, 1, 8), (5, 8, 1001), (7, 3, 24), (2, 31, 40), (300, 6, 512), (1, 0, 16), (9, 5, 7), (2000, 4, 1016)])
+@pytest.mark.parametrize("T,topk,n", [(1, 4, 2880), (3, 1, 8), (5, 8, 1001), (7, 3, 24), (2, 31, 40), (300, 6, 512), (1, 0, 16), (9, 5, 7), (2000, 4, 1016), (33, 9, 1002),
+                                      (11, 2, 1), (6, 4, 13), (5, 17, 2003)])
 def test_combine_against_the_definition(T, topk, n):
     y, w = randn(70, T, topk, n), torch.rand(T, topk, device="cuda") - 0.3
     wide = randn(71, T, n + 8)
@@ -479,6 +480,20 @@ def test_combine_against_the_definition(T, topk, n):
     want = qm.experts_combine(y, w, out.clone())
     qm.qm_experts_combine(y, w, out, residual=out)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("n", [8, 9, 15, 1001])
+def test_combine_writes_its_rows_alone(n):
+    """Buffers cut from the middle of larger ones: nothing beside the rows is written, NaN beside y's is not read."""
+    T, topk = 5, 3
+    y = torch.full((T * topk * n + 64,), math.nan, dtype=torch.bfloat16, device="cuda")
+    y[32:32 + T * topk * n] = randn(75, T * topk * n)
+    out = torch.full((T * n + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    w = torch.rand(T, topk, device="cuda")
+    body = y[32:32 + T * topk * n].view(T, topk, n)
+    qm.qm_experts_combine(body, w, out[32:32 + T * n].view(T, n))
+    assert torch.equal(out[32:32 + T * n].view(T, n), qm.experts_combine(body.clone(), w)) and torch.isfinite(out).all()
+    assert (out[:32] == 7.0).all() and (out[32 + T * n:] == 7.0).all()
 
 
 def test_combine_passes_on_what_is_not_finite():
