@@ -28,8 +28,7 @@
 // for the next token's logits ahead changed nothing (32 warps to an SM hide them).
 //
 // Sum. Eight columns of one token to a thread, up to eight of its experts' rows asked for
-// before the first is used: 4096 tokens x 8 rows of 2880 take 44 us, 5.3 TB/s (four rows
-// at a time 51).
+// before the first is used: 4096 tokens x 8 rows of 2880 take 34 us, 6.9 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -761,9 +760,10 @@ QM_DEV void store_loose(uint16_t* p, const uint32_t (&v)[4], int live) {
 
 // VEC: n a multiple of 8, so that every row of y and out is in 16-byte pieces, and the residual's too; else rows begin at
 // any even address, and a row's last piece may be short (n = 1001: 43 us an element at a time, 4096
-// tokens x 8 rows). ROWS of them are asked for before the first is used.
+// tokens x 8 rows; now 25). ROWS of them are asked for before the first is used; the blocks to an SM leave
+// the registers for that (8 rows of 2880: 34 us with 6 blocks, 36 with 8, 44 and more without a bound).
 template <bool VEC, int ROWS>
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Combine a) {
+__global__ void __launch_bounds__(128, VEC && ROWS == 2 ? 12 : VEC && ROWS == 8 ? 6 : 8) combine_kernel(const __grid_constant__ Combine a) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t per = (a.n + 7) / 8, total = a.T * per, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -818,7 +818,10 @@ cudaError_t launch_experts_combine(const void* y, const float* weights, int64_t 
     const bool vec = n % 8 == 0 && (!residual || (aligned16(residual) && residual_stride % 8 == 0));
     const int64_t items = T * ((n + 7) / 8);
     const int64_t blocks = std::min<int64_t>((items + 127) / 128, int64_t(1) << 22);
-    return launch_pdl(!vec ? combine_kernel<false, 4> : topk > 4 ? combine_kernel<true, 8> : combine_kernel<true, 4>,
+    return launch_pdl(!vec ? combine_kernel<false, 4>
+                           : topk > 4 ? combine_kernel<true, 8>
+                           : topk > 2 ? combine_kernel<true, 4>
+                                      : combine_kernel<true, 2>,
                       static_cast<unsigned>(blocks), 128, 0, st, a);
 }
 
