@@ -336,7 +336,7 @@ static __device__ __noinline__ float2 group_exact(CodeRow ra, CodeRow rb, int gi
 // the GPU: each takes `w` CTAs, as many as leave all of them resident at once, or, where
 // there are more than half as many chunks as resident CTAs, the w of 1 .. 32 whose waves
 // hold the fewest stages. (Cut for the chunks expected, 64 positions over 32 experts of
-// 5760 x 2880 ran 336 CTAs on 304 places, almost twice the stages: 165 us, now 100.) A row is
+// 5760 x 2880 ran 336 CTAs on 304 places, almost twice the stages: 129 us, now 82.) A row is
 // summed the same way whichever CTA holds its stage.
 static __device__ __noinline__ void group_lookup(const Params& p, int cluster, int lane, int* s_grp, int* s_pos,
                                                  int* s_xrow, int* s_share) {
@@ -1035,6 +1035,8 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
             // ---- the team's sum in warp order, spread over the team's warps;
             //      then undo the token scale and store
             const int64_t row0 = (stage0 + j) * kRows;
+            // abandoned or not, for the whole warp where it shuffles
+            auto abandoned = [&]() { return EPI ? __any_sync(0xffffffffu, s_abort != 0) != 0 : s_abort != 0; };
             const bool pairs = EPI && p.ep.gated && S == 1;  // a split's pairs meet after the ranks' sums
             auto store = [&](int tt, int nt, int ln, int i, float v, float u) {
                 const int m = nt * 8 + 2 * (ln & 3) + (i & 1);
@@ -1058,7 +1060,7 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                     }
                 }
                 named_bar_sync(2 + team, T * 32);
-                if (live && !s_abort) {
+                if (live && !abandoned()) {
                     const int e = wi * (32 / T) + lane;  // warp wi adds rows [wi*32/T, (wi+1)*32/T)
                     float be = 0.0f, bn = 0.0f;
                     if (EPI && p.ep.bias) {
@@ -1094,7 +1096,8 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                         *reinterpret_cast<float4*>(mine + ((tt * NT + nt) * 32 + lane) * 4) =
                             make_float4(y[tt][nt][0], y[tt][nt][1], y[tt][nt][2], y[tt][nt][3]);
                 named_bar_sync(2 + team, T * 32);
-                if (live && !s_abort && (!EPI || S > 1)) {
+                const bool go = live && !abandoned();
+                if (go && (!EPI || S > 1)) {
                     // warp wi adds entries [wi*E/T, (wi+1)*E/T) over the team's warps in order
                     #pragma unroll 1
                     for (int e = wi * (E / T) + lane; e < (wi + 1) * (E / T); e += 32) {
@@ -1104,7 +1107,7 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                         const int i = e & 3, ln = (e >> 2) & 31, tn = e >> 7;
                         store(tn / NT, tn % NT, ln, i, sum, 0.0f);
                     }
-                } else if (EPI && live && !s_abort) {
+                } else if (EPI && go) {
                     // the same before an epilogue; of pairs as large a share of the even rows'
                     // entries: rows 2i and 2i + 1 lie four lanes apart, sixteen entries
                     const int share = (pairs ? E / 2 : E) / T;
