@@ -22,9 +22,9 @@
 //
 // It reads each logit once; what bounds it is instructions, some 500 a token without a
 // bias or groups and 1080 with both, at 70 % of the issue slots: 16384 tokens of 256
-// experts take 10.3 us (top 8 of all) and 24 us (sigmoid, bias, 4 of 8 groups by their
+// experts take 9.6 us (top 8 of all) and 22 us (sigmoid, bias, 4 of 8 groups by their
 // two best), against 2.6 us of memory time. Some 60 of the latter's tokens need float64,
-// whose chain of operations at 1/64 of float32's rate the last of them shows: 5 us. Asking
+// whose chain of operations at 1/64 of float32's rate the last of them shows: 3 us. Asking
 // for the next token's logits ahead changed nothing (32 warps to an SM hide them).
 //
 // Sum. Eight columns of one token to a thread, up to eight of its experts' rows asked for
@@ -359,22 +359,12 @@ QM_DEV uint32_t group_score(const Select& a, uint32_t m1, uint32_t m2, float top
 // the groups within `tol` of the last that stayed, x, and the first that did not, y, are ranked
 // anew by float64 keys. One above x + tol is passed only by groups that stay as well, one below
 // y - tol by any that stays. Sets *all where more than that is to be done in float64.
+// What a rare call waits for is its instructions: it takes the keys as they are (a copy of this
+// lane's), and its loops are not unrolled.
 template <int V>
-static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane, float top, float inv_sum, float x, float y, float tol,
-                                            uint64_t* list, int64_t* exact, bool* all) {
+static __device__ __noinline__ bool regroup(const Select& a, int64_t t, int lane, const uint32_t* key, uint32_t mine, uint32_t m1, uint32_t m2,
+                                            float top, float x, float y, float tol, uint64_t* list, int64_t* exact, bool* all) {
     const Place at(a, lane);
-    // Loops are not unrolled here: what a rare call waits for is its instructions.
-    uint32_t key[V], m1 = kNone, m2 = kNone;
-#pragma unroll 1
-    for (int i = 0; i < at.count; ++i) {
-        const int e = at.base + (i << a.lanes_log2);
-        key[i] = key_of(a, load_logit(a, t, e), e, top, inv_sum);
-        m2 = max(m2, min(m1, key[i]));
-        m1 = max(m1, key[i]);
-    }
-    join_top2(a, m1, m2);
-    float err;
-    const uint32_t mine = group_score(a, m1, m2, top, inv_sum, &err);
     const float m = unordered(mine);
     const bool real = at.group < a.groups && mine != kNone;
     const bool above = real && m > x + tol, band = real && !above && !(m < y - tol);
@@ -537,8 +527,14 @@ __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kern
                     else err = a.top2 ? 2.0f * most_error(a) : most_error(a);
                     // both errors, the sums' roundings, and as much again
                     const float tol = 4.0f * err + 0x1p-21f * (fabsf(x) + fabsf(y));
-                    if (!(x - y > tol))
-                        stays = regroup<V>(a, t, lane, top, inv_sum, x, y, tol, list, s_exact[threadIdx.x >> 5], &exact_all);
+                    if (!(x - y > tol)) {
+                        uint32_t copy[V];
+                        bool all;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) copy[i] = key[i];
+                        stays = regroup<V>(a, t, lane, copy, mine, m1, m2, top, x, y, tol, list, s_exact[threadIdx.x >> 5], &all);
+                        exact_all = all;
+                    }
                 }
             }
             if (!stays) mk = kNone;
@@ -648,8 +644,9 @@ __global__ void __launch_bounds__(kSelectWarps * 32, V <= 8 ? 8 : 1) select_kern
 
 template <int V, bool GROUPS>
 cudaError_t launch_select(const Select& a, cudaStream_t st) {
-    // as many warps as stay resident: a warp reads the bias once
-    const int64_t blocks = std::min<int64_t>((a.T + kSelectWarps - 1) / kSelectWarps, int64_t(num_sms()) * 8);
+    // twice as many blocks as stay resident: a warp reads the bias once for a token or two, and what
+    // one of them waits for (float64) the rest is not dealt out to wait behind (8 an SM 24.1, 16 23.8, 32 25.5 us)
+    const int64_t blocks = std::min<int64_t>((a.T + kSelectWarps - 1) / kSelectWarps, int64_t(num_sms()) * 16);
     return launch_pdl(a.dtype == QM_F32 ? select_kernel<V, GROUPS, false> : select_kernel<V, GROUPS, true>, static_cast<unsigned>(blocks),
                       kSelectWarps * 32, 0, st, a);
 }
