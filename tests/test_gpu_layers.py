@@ -615,3 +615,69 @@ def test_tensors_of_another_gpu_than_the_current_one(monkeypatch):
                  lambda: qm.experts_select(randn(1, 3, 16), qm.Router(2)), lambda: qm.experts_combine(randn(1, 3, 2, 8), torch.ones(3, 2, device="cuda"))):
         with pytest.raises(qm.QMError, match="device"):
             call()
+
+
+# ---------------------------------------------------------------- where calls go wrong
+def same(a, b):
+    """Equal, with every NaN equal to every other."""
+    nan = torch.isnan(a)
+    return torch.equal(nan, torch.isnan(b)) and torch.equal(a[~nan], b[~nan])
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 40, 200])
+def test_activations_that_are_not_finite(M):
+    """Infinite and NaN activations: what the plain product gives, through relu and an added row."""
+    w, _ = make("affine4_g64", 110, 130, 512)
+    x = randn(111, M, 512)
+    x[0, 3] = math.inf
+    if M > 1:
+        x[1, 9] = math.nan
+        x[-1, 11] = -math.inf
+    plain, res = qm.apply(w, x), randn(112, 1, 130).expand(M, 130)
+    y = qm.apply_fused(w, x, qm.Epilogue(act="relu"))
+    assert same(y, torch.relu(plain) + 0.0)
+    y = qm.apply_fused(w, x, qm.Epilogue(), res)
+    odd = ~torch.isfinite(plain)
+    assert odd.any() and same(y[odd], plain[odd])
+    assert torch.isfinite(y[~odd]).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [dict(), dict(groups=4, topk_groups=2), dict(groups=4, topk_groups=2, group_score="top2")])
+def test_select_with_a_bias_that_is_not_finite(score, groups):
+    x = randn(113, 9, 64, dtype=torch.float32)
+    bias = randn(114, 64, dtype=torch.float32) * 0.1
+    bias[[5, 21]] = math.inf
+    bias[40] = math.nan
+    bias[[50, 51, 52]] = -math.inf
+    bias[33] = 1e30
+    check_select(x, 7, score=score, bias=bias, **groups)
+    check_select(x, 7, score=score, bias=torch.full((64,), -math.inf, device="cuda"), **groups)
+
+
+def test_past_two_to_the_31_elements():
+    """Offsets that 32 bits do not hold, in each of the calls; rows at the ends and about the border are looked at."""
+    T, topk, n = 93_300, 8, 2880
+    y = torch.empty(T, topk, n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(115))
+    w = torch.rand(T, topk, device="cuda")
+    out = qm.experts_combine(y, w)
+    at = torch.tensor([0, 1, (1 << 31) // (topk * n), (1 << 31) // (topk * n) + 1, T - 1], device="cuda")
+    assert torch.equal(out[at], qm.experts_combine(y[at].contiguous(), w[at].contiguous()))
+    del y, out
+    T, E = 2_100_000, 1024
+    logits = torch.empty(T, E, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(116))
+    router = qm.Router(4)
+    ids, weights = qm.experts_select(logits, router)
+    at = torch.tensor([0, (1 << 31) // E - 1, (1 << 31) // E, T - 1], device="cuda")
+    few = qm.experts_select(logits[at].contiguous(), router)
+    assert torch.equal(ids[at], few[0]) and torch.equal(weights[at], few[1])
+    del logits, ids, weights
+    M, n, k = 150_100, 14336, 64
+    wq, _ = make("mxfp4", 117, n, k)
+    x, res = randn(118, M, k), torch.empty(M, n, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(119))
+    ep = qm.Epilogue(act="silu")
+    at = torch.tensor([0, (1 << 31) // n, (1 << 31) // n + 1, M - 1], device="cuda").repeat_interleave(80)  # 320 rows: the same kernel
+    want = qm.apply_fused(wq, x[at].contiguous(), ep, res[at].contiguous())
+    qm.qm_apply_fused(wq, x, ep, res, residual=res)
+    assert torch.equal(res[at], want)
+    qm.qm_device_status()
