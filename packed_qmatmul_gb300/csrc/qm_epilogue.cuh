@@ -117,6 +117,9 @@ QM_DEV float epi_residual(const Epi& e, int64_t row, int64_t col) {
     return e.residual ? bf16_bits_to_f32(__ldca(e.residual + row * e.residual_stride + col)) : 0.0f;
 }
 
+// Asks for the line at p, which a later load then finds in L1.
+QM_DEV void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 QM_DEV uint16_t bf16_bits(float v) {
     const __nv_bfloat16 b = __float2bfloat16_rn(v);
     return *reinterpret_cast<const uint16_t*>(&b);

@@ -802,6 +802,15 @@ __global__ void __launch_bounds__(kThreadsOf(CW), CW == 8 ? 2 : 1) gemv_kernel(c
                 const int64_t row = (stage0 + j) * kRows + lane;
                 if (row < p.n) bias_bits = epi_bias_bits(p.ep, wrow0 + row);
             }
+            if (EPI && !p.g_off && rank == 0) {
+                // the stage's residuals (32 columns of each token, or 16) and, where they are added to
+                // the ranks' sums at the end, its biases
+                const int64_t row = (stage0 + j) * kRows + ((lane & 1) ? 31 : 0), last = min(row, p.n - 1);
+                if (p.ep.residual && (lane >> 1) < M)
+                    prefetch_l1(p.ep.residual + (lane >> 1) * p.ep.residual_stride + (p.ep.gated ? last >> 1 : last));
+                if (p.ep.bias && S > 1 && lane < 2)
+                    prefetch_l1(static_cast<const uint8_t*>(p.ep.bias) + last * (p.ep.bias_dtype == QM_F32 ? 4 : 2));
+            }
             bool live = !s_abort;
             // A slot's first fill needs no tag: its barrier's first phase can only
             // be that fill. Later fills check that the producer has started stage j.
